@@ -10,6 +10,10 @@ Entry points (names follow the C ABI):
   decode_step(q, k, v, g, beta, S, ...) -> o           (S updated in place)
   chunk_fwd_workspace_size(...), chunk_fwd_path(...), chunk_bwd_path(...),
   read_device_error(...)
+Around the recurrence (layer.py):
+  linear_scan_fwd, linear_scan_bwd, linear_scan_step: gated linear recurrence
+  short_conv_fwd, short_conv_bwd, short_conv_step: short causal convolution
+  group_norm_fwd, group_norm_bwd: group norm with an activation or a gate
 """
 from __future__ import annotations
 
@@ -19,12 +23,16 @@ import os
 
 from . import _abi
 from ._abi import GdrError, ChunkArgs, DecodeArgs, F32, BF16, READ_POST, READ_PRE  # noqa: F401
+from .layer import (group_norm_bwd, group_norm_fwd, linear_scan_bwd, linear_scan_fwd,
+                    linear_scan_step, short_conv_bwd, short_conv_fwd, short_conv_step)
 
 __all__ = ["chunk_fwd", "chunk_fwd_bidir", "chunk_bwd", "decode_step",
            "chunk_fwd_workspace_size", "chunk_fwd_bidir_workspace_size",
            "chunk_bwd_workspace_size", "chunk_fwd_path", "chunk_bwd_path",
            "read_device_error", "chunk_fwd_noalloc", "noalloc_read_device_error", "library",
-           "GdrError"]
+           "GdrError",
+           "linear_scan_fwd", "linear_scan_bwd", "linear_scan_step", "short_conv_fwd",
+           "short_conv_bwd", "short_conv_step", "group_norm_fwd", "group_norm_bwd"]
 
 
 def library():

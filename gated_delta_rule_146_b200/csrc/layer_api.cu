@@ -1,0 +1,224 @@
+// layer_api.cu -- the C ABI of the operators around the delta rule: host-side validation and
+// dispatch (scan.cu, scan_bwd.cu, conv.cu, norm.cu, norm_seq.cu).
+#include <cmath>
+#include <initializer_list>
+
+#include "layer.cuh"
+
+using namespace gdr;
+
+namespace {
+
+bool off16(std::initializer_list<const void*> ptrs) {
+    uintptr_t bits = 0;
+    for (const void* p : ptrs) bits |= reinterpret_cast<uintptr_t>(p);
+    return (bits & 15u) != 0;
+}
+
+bool off4(std::initializer_list<const void*> ptrs) {
+    uintptr_t bits = 0;
+    for (const void* p : ptrs) bits |= reinterpret_cast<uintptr_t>(p);
+    return (bits & 3u) != 0;
+}
+
+bool any_null(std::initializer_list<const void*> ptrs) {
+    for (const void* p : ptrs)
+        if (!p) return true;
+    return false;
+}
+
+bool valid_dtype(gdr_dtype d) { return d == GDR_F32 || d == GDR_BF16; }
+
+// Token and channel counts of every operator: kernels hold token numbers (and one tile more) in
+// 32 bits, element offsets in 64.
+gdr_status check_sizes(long long B, long long T, long long D, long long n_seqs) {
+    if (B < 1 || T < 0 || D < 1 || n_seqs < 1) return GDR_ERR_INVALID_ARG;
+    if (B * T > 0x7fff0000LL || n_seqs > 0x7fff0000LL) return GDR_ERR_INVALID_ARG;
+    if (D > (1 << 20)) return GDR_ERR_UNSUPPORTED;
+    return GDR_OK;
+}
+
+template <typename A>
+gdr_status check_layout(const A* a, const int32_t* cu) {
+    if (cu ? a->B != 1 : a->n_seqs != a->B) return GDR_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(a->status) & 3u) return GDR_ERR_ALIGNMENT;
+    return GDR_OK;
+}
+
+gdr_status check_scan(const gdr_scan_args* a) {
+    if (!a) return GDR_ERR_INVALID_ARG;
+    if (const gdr_status st = check_sizes(a->B, a->T, a->D, a->n_seqs); st != GDR_OK) return st;
+    if (!valid_dtype(a->io_dtype) || !valid_dtype(a->gate_dtype)) return GDR_ERR_INVALID_ARG;
+    if (a->write != GDR_WRITE_PLAIN && a->write != GDR_WRITE_GATE && a->write != GDR_WRITE_TIED)
+        return GDR_ERR_INVALID_ARG;
+    if (a->reverse & ~1) return GDR_ERR_INVALID_ARG;
+    return GDR_OK;
+}
+
+gdr_status check_conv(const gdr_conv_args* a) {
+    if (!a) return GDR_ERR_INVALID_ARG;
+    if (const gdr_status st = check_sizes(a->B, a->T, a->D, a->n_seqs); st != GDR_OK) return st;
+    if (!valid_dtype(a->io_dtype) || a->width < 1 || (a->reverse & ~1)) return GDR_ERR_INVALID_ARG;
+    if (a->activation != GDR_ACT_NONE && a->activation != GDR_ACT_SILU)
+        return a->activation == GDR_ACT_SIGMOID ? GDR_ERR_UNSUPPORTED : GDR_ERR_INVALID_ARG;
+    if (a->width < 2 || a->width > 4) return GDR_ERR_UNSUPPORTED;
+    return GDR_OK;
+}
+
+gdr_status check_norm(const gdr_norm_args* a) {
+    if (!a) return GDR_ERR_INVALID_ARG;
+    if (a->H < 1 || a->d < 1) return GDR_ERR_INVALID_ARG;
+    if (const gdr_status st = check_sizes(a->B, a->T, (long long)a->H * a->d, a->n_seqs); st != GDR_OK)
+        return st;
+    if (!valid_dtype(a->io_dtype)) return GDR_ERR_INVALID_ARG;
+    if ((a->per_sequence | a->center | a->shared_weight) & ~1) return GDR_ERR_INVALID_ARG;
+    if (a->activation != GDR_ACT_NONE && a->activation != GDR_ACT_SILU &&
+        a->activation != GDR_ACT_SIGMOID)
+        return GDR_ERR_INVALID_ARG;
+    if (!(std::isfinite(a->eps) && a->eps >= 0.f)) return GDR_ERR_INVALID_ARG;
+    // a grid has at most one block per (token, head) and per (sequence, head)
+    if (((long long)a->B * a->T + 1) * a->H > 0x7fffffffLL || (long long)a->n_seqs * a->H > 0x7fffffffLL)
+        return GDR_ERR_UNSUPPORTED;
+    return norm_supported(*a) ? GDR_OK : GDR_ERR_UNSUPPORTED;
+}
+
+gdr_status check_workspace(const void* ws, size_t have, size_t need) {
+    if (need == 0) return GDR_OK;
+    if (!ws || have < need) return GDR_ERR_WORKSPACE;
+    return (reinterpret_cast<uintptr_t>(ws) & 255u) ? GDR_ERR_ALIGNMENT : GDR_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+gdr_status gdr_scan_fwd(const gdr_scan_args* a, const void* v, const void* g, const void* beta,
+                        const float* h0, const int32_t* cu, void* o, float* h_final,
+                        void* stream) {
+    gdr_status st = check_scan(a);
+    if (st != GDR_OK || (st = check_layout(a, cu)) != GDR_OK) return st;
+    const bool tokens = (long long)a->B * a->T > 0, gate = a->write == GDR_WRITE_GATE;
+    if (tokens && (any_null({v, g, o}) || gate != (beta != nullptr))) return GDR_ERR_INVALID_ARG;
+    if (off16({v, g, beta, h0, cu, o, h_final})) return GDR_ERR_ALIGNMENT;
+    ScanPtrs p{};
+    p.v = v; p.g = g; p.beta = beta; p.h0 = h0; p.cu = cu; p.o = o; p.h_final = h_final;
+    return launch_scan_fwd(*a, p, static_cast<cudaStream_t>(stream));
+}
+
+gdr_status gdr_scan_bwd(const gdr_scan_args* a, const void* v, const void* g, const void* beta,
+                        const void* o, const void* dO, const float* h0, const int32_t* cu,
+                        const float* dh_final, void* dv, void* dg, void* dbeta, float* dh0,
+                        void* stream) {
+    gdr_status st = check_scan(a);
+    if (st != GDR_OK || (st = check_layout(a, cu)) != GDR_OK) return st;
+    const bool tokens = (long long)a->B * a->T > 0, gate = a->write == GDR_WRITE_GATE;
+    if (tokens && (any_null({g, o, dO, dv, dg}) || gate != (beta != nullptr) ||
+                   gate != (dbeta != nullptr) || (a->write != GDR_WRITE_PLAIN && !v)))
+        return GDR_ERR_INVALID_ARG;
+    if (off16({v, g, beta, o, dO, h0, cu, dh_final, dv, dg, dbeta, dh0})) return GDR_ERR_ALIGNMENT;
+    ScanPtrs p{};
+    p.v = v; p.g = g; p.beta = beta; p.o_in = o; p.dO = dO; p.h0 = h0; p.cu = cu;
+    p.dh_final = dh_final; p.dv = dv; p.dg = dg; p.dbeta = dbeta; p.dh0 = dh0;
+    return launch_scan_bwd(*a, p, static_cast<cudaStream_t>(stream));
+}
+
+gdr_status gdr_scan_step(const gdr_scan_args* a, const void* v, const void* g, const void* beta,
+                         const float* h, float* h_out, void* o, void* stream) {
+    gdr_status st = check_scan(a);
+    if (st != GDR_OK || (st = check_layout(a, nullptr)) != GDR_OK) return st;
+    if (a->T != 1 || a->reverse) return GDR_ERR_INVALID_ARG;
+    const bool gate = a->write == GDR_WRITE_GATE;
+    if (any_null({v, g, h, h_out, o}) || gate != (beta != nullptr)) return GDR_ERR_INVALID_ARG;
+    if (off16({v, g, beta, h, h_out, o})) return GDR_ERR_ALIGNMENT;
+    ScanPtrs p{};
+    p.v = v; p.g = g; p.beta = beta; p.h0 = h; p.h_final = h_out; p.o = o;
+    return launch_scan_step(*a, p, static_cast<cudaStream_t>(stream));
+}
+
+gdr_status gdr_conv_fwd(const gdr_conv_args* a, const void* x, const float* w, const float* bias,
+                        const void* state, const int32_t* cu, void* y, void* state_out,
+                        void* stream) {
+    gdr_status st = check_conv(a);
+    if (st != GDR_OK || (st = check_layout(a, cu)) != GDR_OK) return st;
+    if ((long long)a->B * a->T > 0 && any_null({x, y})) return GDR_ERR_INVALID_ARG;
+    if (!w || (state && state == state_out)) return GDR_ERR_INVALID_ARG;
+    if (off16({x, state, cu, y, state_out}) || off4({w, bias})) return GDR_ERR_ALIGNMENT;
+    ConvPtrs p{};
+    p.x = x; p.w = w; p.bias = bias; p.state = state; p.cu = cu; p.y = y; p.state_out = state_out;
+    return launch_conv_fwd(*a, p, static_cast<cudaStream_t>(stream));
+}
+
+size_t gdr_conv_bwd_workspace_size(const gdr_conv_args* a) {
+    return check_conv(a) == GDR_OK ? conv_bwd_workspace(*a) : 0;
+}
+
+gdr_status gdr_conv_bwd(const gdr_conv_args* a, const void* x, const float* w, const float* bias,
+                        const void* dy, const void* state, const int32_t* cu, void* dx, float* dw,
+                        float* dbias, void* dstate, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+    gdr_status st = check_conv(a);
+    if (st != GDR_OK || (st = check_layout(a, cu)) != GDR_OK) return st;
+    if ((long long)a->B * a->T > 0 && any_null({x, dy, dx})) return GDR_ERR_INVALID_ARG;
+    if (!w || !dw) return GDR_ERR_INVALID_ARG;
+    if (off16({x, dy, state, cu, dx, dstate}) || off4({w, bias, dw, dbias})) return GDR_ERR_ALIGNMENT;
+    if ((st = check_workspace(workspace, workspace_bytes, conv_bwd_workspace(*a))) != GDR_OK) return st;
+    ConvPtrs p{};
+    p.x = x; p.w = w; p.bias = bias; p.dy = dy; p.state = state; p.cu = cu; p.dx = dx; p.dw = dw;
+    p.dbias = dbias; p.dstate = dstate; p.ws = static_cast<float*>(workspace);
+    return launch_conv_bwd(*a, p, static_cast<cudaStream_t>(stream));
+}
+
+gdr_status gdr_conv_step(const gdr_conv_args* a, const void* x, const float* w, const float* bias,
+                         const void* state, void* state_out, void* y, void* stream) {
+    gdr_status st = check_conv(a);
+    if (st != GDR_OK || (st = check_layout(a, nullptr)) != GDR_OK) return st;
+    if (a->T != 1 || a->reverse) return GDR_ERR_INVALID_ARG;
+    if (any_null({x, w, state, state_out, y})) return GDR_ERR_INVALID_ARG;
+    if (off16({x, state, state_out, y}) || off4({w, bias})) return GDR_ERR_ALIGNMENT;
+    ConvPtrs p{};
+    p.x = x; p.w = w; p.bias = bias; p.state = state; p.y = y; p.state_out = state_out;
+    return launch_conv_step(*a, p, static_cast<cudaStream_t>(stream));
+}
+
+size_t gdr_norm_fwd_workspace_size(const gdr_norm_args* a) {
+    return check_norm(a) == GDR_OK ? norm_fwd_workspace(*a) : 0;
+}
+
+gdr_status gdr_norm_fwd(const gdr_norm_args* a, const void* x, const float* w, const float* bias,
+                        const void* z, const int32_t* cu, void* y, float* stats, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+    gdr_status st = check_norm(a);
+    if (st != GDR_OK || (st = check_layout(a, cu)) != GDR_OK) return st;
+    if ((long long)a->B * a->T > 0 && any_null({x, y})) return GDR_ERR_INVALID_ARG;
+    if (stats && !a->per_sequence) return GDR_ERR_INVALID_ARG;
+    if (off16({x, z, cu, y, stats}) || off4({w, bias})) return GDR_ERR_ALIGNMENT;
+    if ((st = check_workspace(workspace, workspace_bytes, norm_fwd_workspace(*a))) != GDR_OK) return st;
+    NormPtrs p{};
+    p.x = x; p.w = w; p.b = bias; p.z = z; p.cu = cu; p.y = y; p.stats = stats;
+    p.ws = static_cast<float*>(workspace);
+    return launch_norm_fwd(*a, p, static_cast<cudaStream_t>(stream));
+}
+
+size_t gdr_norm_bwd_workspace_size(const gdr_norm_args* a) {
+    return check_norm(a) == GDR_OK ? norm_bwd_workspace(*a) : 0;
+}
+
+gdr_status gdr_norm_bwd(const gdr_norm_args* a, const void* x, const float* w, const float* bias,
+                        const void* z, const void* dy, const int32_t* cu, const float* stats,
+                        void* dx, float* dw, float* dbias, void* dz, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+    gdr_status st = check_norm(a);
+    if (st != GDR_OK || (st = check_layout(a, cu)) != GDR_OK) return st;
+    const bool tokens = (long long)a->B * a->T > 0;
+    if (tokens && any_null({x, dy, dx})) return GDR_ERR_INVALID_ARG;
+    if (tokens && (z != nullptr) != (dz != nullptr)) return GDR_ERR_INVALID_ARG;
+    if (a->per_sequence && !stats) return GDR_ERR_INVALID_ARG;
+    if (off16({x, z, dy, cu, stats, dx, dz}) || off4({w, bias, dw, dbias})) return GDR_ERR_ALIGNMENT;
+    if ((st = check_workspace(workspace, workspace_bytes, norm_bwd_workspace(*a))) != GDR_OK) return st;
+    NormPtrs p{};
+    p.x = x; p.w = w; p.b = bias; p.z = z; p.dy = dy; p.cu = cu; p.stats_in = stats; p.dx = dx;
+    p.dw = dw; p.db = dbias; p.dz = dz; p.ws = static_cast<float*>(workspace);
+    return launch_norm_bwd(*a, p, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,284 @@
+// norm.cu -- group norm of every token's heads with an activation or a gate: forward, backward;
+// and the dispatch of the per-sequence form (norm_seq.cu).
+//
+//     n = (x - mean) rstd (or x rstd), u = n w + b, y = u act(z) | act(u)
+//     dx = rstd (q - mean(q) - n mean(q n)),  q = du w      (mean(q) with centering only)
+//
+// A group's channels stay in one warp's registers: the statistics are two passes over registers
+// (sums of squares about the mean, no cancellation), the tensors are read and written once: 4 or
+// 6 (gate) bytes per element forward, 6 or 10 backward in bf16.  HBM bounds both.
+//
+// Each lane group keeps one head, so that weights, and in the backward the sums for dw and db,
+// stay in registers over all its rows; the sums are joined over the block, then over the blocks
+// by a second kernel, in a fixed order.
+#include "norm_impl.cuh"
+
+namespace gdr {
+
+namespace {
+
+// How the rows (token, head) are dealt out.  A slot is one lane group of one block; slot i takes
+// rows i, i + slots, ...; slots is a multiple of H, so a slot's head stays.
+struct Deal {
+    int blocks;
+    int used;          // lane groups of a block that take part
+    long long slots;
+    int part_rows;     // rows of partial sums
+};
+
+Deal deal(const gdr_norm_args& a, int groups, int per_slot) {
+    const long long rows = (long long)a.B * a.T * a.H;
+    Deal d;
+    // 148 * 4 blocks fill the GPU at the kernels' register use; a slot takes at least
+    // `per_slot` rows where there are so many, so that partial sums stay a small share of the
+    // traffic
+    if (a.H <= groups) {
+        d.used = groups / a.H * a.H;
+        long long b = (rows + (long long)d.used * per_slot - 1) / ((long long)d.used * per_slot);
+        d.blocks = (int)(b < 1 ? 1 : b > 148 * 4 ? 148 * 4 : b);
+        d.slots = (long long)d.blocks * d.used;
+        d.part_rows = d.blocks;
+    } else {
+        d.used = groups;
+        long long per_head = rows / a.H / per_slot;
+        const long long most = 148LL * 4 * groups / a.H;
+        if (per_head > most) per_head = most;
+        if (per_head < 1) per_head = 1;
+        d.slots = per_head * a.H;
+        d.blocks = (int)((d.slots + groups - 1) / groups);
+        d.part_rows = a.shared_weight ? d.blocks : (int)per_head;
+    }
+    return d;
+}
+
+template <typename S>
+__device__ __forceinline__ void token_stats(const float (&x)[S::NV][S::VEC], int l, int d,
+                                            int center, float eps, float& mean, float& rstd) {
+    const float inv = 1.f / d;
+    mean = 0.f;
+    if (center) {
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < S::NV; ++k) {
+#pragma unroll
+            for (int j = 0; j < S::VEC; ++j) s += x[k][j];
+        }
+        mean = group_sum<S::LPG>(s) * inv;
+    }
+    float v = 0.f;
+#pragma unroll
+    for (int k = 0; k < S::NV; ++k) {
+        const bool in = (k * S::LPG + l) * S::VEC < d;
+#pragma unroll
+        for (int j = 0; j < S::VEC; ++j) {
+            const float t = x[k][j] - mean;
+            v = in ? fmaf(t, t, v) : v;
+        }
+    }
+    rstd = 1.f / sqrtf(group_sum<S::LPG>(v) * inv + eps);
+}
+
+template <typename S>
+__global__ void __launch_bounds__(kNormThreads)
+norm_token_fwd(const NormParams<typename S::IO> p, int used, long long slots) {
+    const int g = threadIdx.x / S::LPG, l = threadIdx.x % S::LPG;
+    const long long slot = (long long)blockIdx.x * used + g;
+    const bool on = g < used && slot < slots;
+    const int head = (int)(slot % p.H);
+    float w[S::NV][S::VEC], b[S::NV][S::VEC];
+    load_affine<S>(p.w, 1.f, head, l, p.d, p.shared, w);
+    load_affine<S>(p.b, 0.f, head, l, p.d, p.shared, b);
+    const bool gate = p.z != nullptr;
+    // every lane takes part in the group sums until the block's last row
+    for (long long r0 = (long long)blockIdx.x * used; r0 < p.rows; r0 += slots) {
+        const long long r = r0 + g;
+        const bool in = on && r < p.rows;
+        const size_t at = (size_t)(in ? r : 0) * p.d;
+        float x[S::NV][S::VEC], z[S::NV][S::VEC], y[S::NV][S::VEC];
+        load_row<S>(p.x + at, l, p.d, in, x);
+        if (gate) load_row<S>(p.z + at, l, p.d, in, z);
+        float mean, rstd;
+        token_stats<S>(x, l, p.d, p.center, p.eps, mean, rstd);
+        if (!in) continue;
+#pragma unroll
+        for (int k = 0; k < S::NV; ++k) {
+#pragma unroll
+            for (int j = 0; j < S::VEC; ++j)
+                y[k][j] = norm_out((x[k][j] - mean) * rstd, w[k][j], b[k][j], gate,
+                                   gate ? z[k][j] : 0.f, p.act);
+        }
+        store_row<S>(p.y + at, l, p.d, y);
+    }
+}
+
+template <typename S>
+__global__ void __launch_bounds__(kNormThreads)
+norm_token_bwd(const NormParams<typename S::IO> p, int used, long long slots) {
+    const int g = threadIdx.x / S::LPG, l = threadIdx.x % S::LPG;
+    const long long slot = (long long)blockIdx.x * used + g;
+    const bool on = g < used && slot < slots;
+    const int head = (int)(slot % p.H);
+    float w[S::NV][S::VEC], b[S::NV][S::VEC];
+    float dw[S::NV][S::VEC] = {}, db[S::NV][S::VEC] = {};
+    load_affine<S>(p.w, 1.f, head, l, p.d, p.shared, w);
+    load_affine<S>(p.b, 0.f, head, l, p.d, p.shared, b);
+    const bool gate = p.z != nullptr;
+    const float inv = 1.f / p.d;
+    for (long long r0 = (long long)blockIdx.x * used; r0 < p.rows; r0 += slots) {
+        const long long r = r0 + g;
+        const bool in = on && r < p.rows;
+        const size_t at = (size_t)(in ? r : 0) * p.d;
+        float x[S::NV][S::VEC], z[S::NV][S::VEC], dy[S::NV][S::VEC];
+        load_row<S>(p.x + at, l, p.d, in, x);
+        load_row<S>(p.dy + at, l, p.d, in, dy);
+        if (gate) load_row<S>(p.z + at, l, p.d, in, z);
+        float mean, rstd;
+        token_stats<S>(x, l, p.d, p.center, p.eps, mean, rstd);
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int k = 0; k < S::NV; ++k) {
+            const bool c = (k * S::LPG + l) * S::VEC < p.d && in;
+#pragma unroll
+            for (int j = 0; j < S::VEC; ++j) {
+                const float n = (x[k][j] - mean) * rstd;
+                float dz = 0.f;
+                const float du = norm_du(n, w[k][j], b[k][j], gate, gate ? z[k][j] : 0.f,
+                                         dy[k][j], p.act, dz);
+                x[k][j] = n;
+                z[k][j] = dz;
+                const float q = du * w[k][j];
+                dy[k][j] = q;
+                if (!c) continue;
+                dw[k][j] = fmaf(du, n, dw[k][j]);
+                db[k][j] += du;
+                s1 += q;
+                s2 = fmaf(q, n, s2);
+            }
+        }
+        s1 = p.center ? group_sum<S::LPG>(s1) * inv : 0.f;
+        s2 = group_sum<S::LPG>(s2) * inv;
+        if (!in) continue;
+#pragma unroll
+        for (int k = 0; k < S::NV; ++k) {
+#pragma unroll
+            for (int j = 0; j < S::VEC; ++j)
+                dy[k][j] = rstd * (dy[k][j] - s1 - x[k][j] * s2);
+        }
+        store_row<S>(p.dx + at, l, p.d, dy);
+        if (gate) store_row<S>(p.dz + at, l, p.d, z);
+    }
+    if (!p.part) return;
+
+    // sums over the block's lane groups of one head (of all, for a shared weight)
+    constexpr int kCh = S::LPG * S::VEC;
+    __shared__ float sh[S::kGroups * kCh];
+    const int heads = p.shared ? 1 : p.H <= S::kGroups ? p.H : 0;
+    for (int which = 0; which < 2; ++which) {
+#pragma unroll
+        for (int k = 0; k < S::NV; ++k) {
+            if (heads == 0) {  // more heads than lane groups: nothing to join
+                if (!on) continue;
+#pragma unroll
+                for (int j = 0; j < S::VEC; ++j) {
+                    const int c = (k * S::LPG + l) * S::VEC + j;
+                    if (c < p.d)
+                        p.part[(((size_t)(slot / p.H) * 2 + which) * p.H + head) * p.d + c] =
+                            which ? db[k][j] : dw[k][j];
+                }
+                continue;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < S::VEC; ++j)
+                sh[g * kCh + l * S::VEC + j] = on ? (which ? db[k][j] : dw[k][j]) : 0.f;
+            __syncthreads();
+            for (int i = threadIdx.x; i < heads * kCh; i += kNormThreads) {
+                const int h = i / kCh, c = k * kCh + i % kCh;
+                if (c >= p.d) continue;
+                float v = 0.f;
+                for (int gg = h; gg < used; gg += heads) v += sh[gg * kCh + i % kCh];
+                p.part[(((size_t)blockIdx.x * 2 + which) * heads + h) * p.d + c] = v;
+            }
+        }
+    }
+}
+
+// 32 channels of one head a block (all heads for a shared weight); its 32 warps over the rows.
+__global__ void __launch_bounds__(1024)
+norm_reduce_kernel(const float* __restrict__ part, int rows, int H, int d, float* __restrict__ dw,
+                   float* __restrict__ db) {
+    __shared__ float sh[32][33];
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + lane, h = blockIdx.y, which = blockIdx.z;
+    float* out = which ? db : dw;
+    if (!out) return;
+    float v = 0.f;
+    if (c < d)
+        for (int r = wid; r < rows; r += 32) v += part[(((size_t)r * 2 + which) * H + h) * d + c];
+    sh[wid][lane] = v;
+    __syncthreads();
+    if (wid == 0 && c < d) {
+#pragma unroll 8
+        for (int k = 1; k < 32; ++k) v += sh[k][lane];
+        out[(size_t)h * d + c] = v;
+    }
+}
+
+// Rows a lane group takes at least, where there are so many.
+constexpr int kPerSlot = 8;
+
+struct TokenFwd {
+    template <typename S>
+    static void go(const gdr_norm_args& a, const NormPtrs& x, cudaStream_t st) {
+        const Deal d = deal(a, S::kGroups, 1);
+        norm_token_fwd<S><<<d.blocks, kNormThreads, 0, st>>>(norm_params<typename S::IO>(a, x),
+                                                             d.used, d.slots);
+    }
+};
+
+struct TokenBwd {
+    template <typename S>
+    static void go(const gdr_norm_args& a, const NormPtrs& x, cudaStream_t st) {
+        const Deal d = deal(a, S::kGroups, kPerSlot);
+        auto p = norm_params<typename S::IO>(a, x);
+        if (!x.dw && !x.db) p.part = nullptr;
+        norm_token_bwd<S><<<d.blocks, kNormThreads, 0, st>>>(p, d.used, d.slots);
+        if (p.part) launch_norm_reduce(a, x.ws, d.part_rows, x.dw, x.db, st);
+    }
+};
+
+}  // namespace
+
+gdr_status launch_norm_reduce(const gdr_norm_args& a, const float* part, int rows, float* dw,
+                              float* db, cudaStream_t st) {
+    const int H = a.shared_weight ? 1 : a.H;
+    norm_reduce_kernel<<<dim3((a.d + 31) / 32, H, 2), 1024, 0, st>>>(part, rows, H, a.d, dw, db);
+    return cudaGetLastError() == cudaSuccess ? GDR_OK : GDR_ERR_CUDA;
+}
+
+bool norm_supported(const gdr_norm_args& a) {
+    const int v = a.io_dtype == GDR_BF16 ? 8 : 4;
+    return a.d <= (a.d % v == 0 ? 1024 : 256) && a.H <= 65535;
+}
+
+size_t norm_fwd_workspace(const gdr_norm_args& a) {
+    return a.per_sequence ? norm_seq_fwd_workspace(a) : 0;
+}
+
+size_t norm_bwd_workspace(const gdr_norm_args& a) {
+    if (a.per_sequence) return norm_seq_bwd_workspace(a);
+    const Deal d = deal(a, norm_groups(a), kPerSlot);
+    return align_up(sizeof(float) * 2 * (size_t)d.part_rows * (a.shared_weight ? 1 : a.H) * a.d, 256);
+}
+
+gdr_status launch_norm_fwd(const gdr_norm_args& a, const NormPtrs& x, cudaStream_t st) {
+    if (a.per_sequence) return launch_norm_seq_fwd(a, x, st);
+    if ((long long)a.B * a.T == 0) return GDR_OK;
+    return norm_dispatch<TokenFwd>(a, x, st);
+}
+
+gdr_status launch_norm_bwd(const gdr_norm_args& a, const NormPtrs& x, cudaStream_t st) {
+    return a.per_sequence ? launch_norm_seq_bwd(a, x, st) : norm_dispatch<TokenBwd>(a, x, st);
+}
+
+}  // namespace gdr

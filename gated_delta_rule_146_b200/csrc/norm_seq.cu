@@ -1,0 +1,413 @@
+// norm_seq.cu -- group norm with statistics over all tokens of a sequence: forward, backward.
+//
+// A group is one head's channels over a whole sequence, more than a block can hold, so each
+// direction is two passes over the tensors with the sums joined between them: sums of every
+// (tile of tokens, head), their join per (sequence, head), then the elements.  The second pass
+// reads x again: from L2 where the tensors fit there.
+//
+// A tile may meet several sequences.  Tile i and sequence s have the piece number i + s: along
+// the token axis each step goes to the next tile or to the next sequence, so the numbers are
+// distinct and a sequence's pieces lie side by side, whatever the lengths.
+//
+// Variances: each piece's sum of squares is taken about the piece's own mean, from registers,
+// and pieces are joined pairwise with the difference of their means, so that no large squares
+// cancel.  Every join has a fixed order.
+#include "norm_impl.cuh"
+
+namespace gdr {
+
+namespace {
+
+__device__ __forceinline__ float block_sum(float x, float* sh) {
+    x = warp_sum(x);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
+    __syncthreads();
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < kNormWarps; ++i) v += sh[i];
+    return v;
+}
+
+// Tokens a lane group holds at once in the statistics pass.
+template <typename S>
+constexpr int kHold = S::NV >= 8 ? 1 : 8 / S::NV;
+
+// part[(tile + s) * H + h] = (mean, sum of squares about it) of the piece's values; without
+// centering (0, sum of squares).
+template <typename S>
+__global__ void __launch_bounds__(kNormThreads)
+norm_seq_stats(const NormParams<typename S::IO> p) {
+    using IO = typename S::IO;
+    constexpr int kTokens = S::kGroups * kHold<S>;
+    __shared__ float sh[kNormWarps];
+    const int g = threadIdx.x / S::LPG, l = threadIdx.x % S::LPG;
+    const int tile = blockIdx.x / p.H, h = blockIdx.x % p.H;
+    if (blockIdx.x == 0) check_cu(p.q, p.status, threadIdx.x, kNormThreads);
+    const int t0 = (int)min((long long)p.q.total, (long long)tile * kTokens);
+    const int t1 = (int)min((long long)p.q.total, (long long)t0 + kTokens);
+    Vec<IO, S::VEC> x[kHold<S>][S::NV];
+#pragma unroll
+    for (int i = 0; i < kHold<S>; ++i) {
+        const int t = t0 + g + i * S::kGroups;
+#pragma unroll
+        for (int k = 0; k < S::NV; ++k) {
+            const int c = (k * S::LPG + l) * S::VEC;
+            if (t < t1 && c < p.d)
+                x[i][k] = load_vec<IO, S::VEC>(p.x + ((size_t)t * p.H + h) * p.d + c);
+        }
+    }
+    for (int s = p.q.of(t0); s < p.q.n; ++s) {
+        const int b = p.q.begin(s), e = p.q.end(s);
+        if (b >= t1) break;
+        const int lo = max(b, t0), hi = min(e, t1);
+        if (lo >= hi) continue;
+        float mean = 0.f;
+        if (p.center) {
+            float v = 0.f;
+#pragma unroll
+            for (int i = 0; i < kHold<S>; ++i) {
+                const int t = t0 + g + i * S::kGroups;
+#pragma unroll
+                for (int k = 0; k < S::NV; ++k) {
+                    if (t < lo || t >= hi || (k * S::LPG + l) * S::VEC >= p.d) continue;
+#pragma unroll
+                    for (int j = 0; j < S::VEC; ++j) v += to_f(x[i][k].x[j]);
+                }
+            }
+            mean = block_sum(v, sh) / ((float)(hi - lo) * p.d);
+        }
+        float v = 0.f;
+#pragma unroll
+        for (int i = 0; i < kHold<S>; ++i) {
+            const int t = t0 + g + i * S::kGroups;
+#pragma unroll
+            for (int k = 0; k < S::NV; ++k) {
+                if (t < lo || t >= hi || (k * S::LPG + l) * S::VEC >= p.d) continue;
+#pragma unroll
+                for (int j = 0; j < S::VEC; ++j) {
+                    const float u = to_f(x[i][k].x[j]) - mean;
+                    v = fmaf(u, u, v);
+                }
+            }
+        }
+        v = block_sum(v, sh);
+        if (threadIdx.x == 0)
+            reinterpret_cast<float2*>(p.part)[((size_t)tile + s) * p.H + h] = make_float2(mean, v);
+    }
+}
+
+// One warp per (sequence, head): joins the pieces' (mean, sum of squares).
+__global__ void __launch_bounds__(128)
+norm_seq_join_stats(Seqs q, int H, int d, int tokens, float eps, const float2* __restrict__ part,
+                    float2* __restrict__ stats) {
+    const long long unit = (long long)blockIdx.x * 4 + threadIdx.x / 32;
+    const int lane = threadIdx.x & 31;
+    if (unit >= (long long)q.n * H) return;
+    const int s = (int)(unit / H), h = (int)(unit % H);
+    const int b = q.begin(s), e = q.end(s);
+    float n = 0.f, mean = 0.f, m2 = 0.f;
+    auto join = [&](float nb, float mb, float sb) {
+        if (nb == 0.f) return;
+        const float all = n + nb, diff = mb - mean, f = nb / all;
+        mean = fmaf(diff, f, mean);
+        m2 += sb + diff * diff * n * f;
+        n = all;
+    };
+    if (b < e) {
+        for (int i = b / tokens + lane; i <= (e - 1) / tokens; i += 32) {
+            const float2 v = part[((size_t)i + s) * H + h];
+            const long long lo = max((long long)b, (long long)i * tokens);
+            const long long hi = min((long long)e, (long long)i * tokens + tokens);
+            join((float)(hi - lo) * d, v.x, v.y);
+        }
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float nb = __shfl_down_sync(0xffffffffu, n, o);
+        const float mb = __shfl_down_sync(0xffffffffu, mean, o);
+        const float sb = __shfl_down_sync(0xffffffffu, m2, o);
+        if (lane + o < 32) join(nb, mb, sb);
+    }
+    if (lane == 0)
+        stats[unit] = make_float2(mean, 1.f / sqrtf((n > 0.f ? m2 / n : 0.f) + eps));
+}
+
+// The sequence of token t, not before s.
+__device__ __forceinline__ int seq_from(const Seqs& q, int s, int t) {
+    while (s + 1 < q.n && t >= q.end(s)) ++s;
+    return s;
+}
+
+template <typename S>
+__global__ void __launch_bounds__(kNormThreads)
+norm_seq_apply(const NormParams<typename S::IO> p, int tokens) {
+    const int g = threadIdx.x / S::LPG, l = threadIdx.x % S::LPG;
+    const int tile = blockIdx.x / p.H, h = blockIdx.x % p.H;
+    const int t0 = (int)min((long long)p.q.total, (long long)tile * tokens);
+    const int t1 = (int)min((long long)p.q.total, (long long)t0 + tokens);
+    float w[S::NV][S::VEC], b[S::NV][S::VEC];
+    load_affine<S>(p.w, 1.f, h, l, p.d, p.shared, w);
+    load_affine<S>(p.b, 0.f, h, l, p.d, p.shared, b);
+    const bool gate = p.z != nullptr;
+    int s = t0 + g < t1 ? p.q.of(t0 + g) : 0;
+    for (int t = t0 + g; t < t1; t += S::kGroups) {
+        s = seq_from(p.q, s, t);
+        const float2 st = __ldg(reinterpret_cast<const float2*>(p.stats) + (size_t)s * p.H + h);
+        const size_t at = ((size_t)t * p.H + h) * p.d;
+        float x[S::NV][S::VEC], z[S::NV][S::VEC], y[S::NV][S::VEC];
+        load_row<S>(p.x + at, l, p.d, true, x);
+        if (gate) load_row<S>(p.z + at, l, p.d, true, z);
+#pragma unroll
+        for (int k = 0; k < S::NV; ++k) {
+#pragma unroll
+            for (int j = 0; j < S::VEC; ++j)
+                y[k][j] = norm_out((x[k][j] - st.x) * st.y, w[k][j], b[k][j], gate,
+                                   gate ? z[k][j] : 0.f, p.act);
+        }
+        store_row<S>(p.y + at, l, p.d, y);
+    }
+}
+
+// First pass of the backward: dz, the tile's sums for dw and db, and per piece the sums of q
+// and q n.
+template <typename S>
+__global__ void __launch_bounds__(kNormThreads)
+norm_seq_bwd_sums(const NormParams<typename S::IO> p, int tokens, float2* __restrict__ pieces) {
+    constexpr int kCh = S::LPG * S::VEC;
+    __shared__ float sh[kNormWarps], shw[S::kGroups * kCh];
+    const int g = threadIdx.x / S::LPG, l = threadIdx.x % S::LPG;
+    const int tile = blockIdx.x / p.H, h = blockIdx.x % p.H;
+    if (blockIdx.x == 0) check_cu(p.q, p.status, threadIdx.x, kNormThreads);
+    const int t0 = (int)min((long long)p.q.total, (long long)tile * tokens);
+    const int t1 = (int)min((long long)p.q.total, (long long)t0 + tokens);
+    float w[S::NV][S::VEC], b[S::NV][S::VEC];
+    float dw[S::NV][S::VEC] = {}, db[S::NV][S::VEC] = {};
+    load_affine<S>(p.w, 1.f, h, l, p.d, p.shared, w);
+    load_affine<S>(p.b, 0.f, h, l, p.d, p.shared, b);
+    const bool gate = p.z != nullptr;
+    for (int s = t0 < t1 ? p.q.of(t0) : p.q.n; s < p.q.n; ++s) {
+        const int sb = p.q.begin(s), se = p.q.end(s);
+        if (sb >= t1) break;
+        const int lo = max(sb, t0), hi = min(se, t1);
+        if (lo >= hi) continue;
+        const float2 st = __ldg(reinterpret_cast<const float2*>(p.stats) + (size_t)s * p.H + h);
+        float s1 = 0.f, s2 = 0.f;
+        for (int t = lo + g; t < hi; t += S::kGroups) {
+            const size_t at = ((size_t)t * p.H + h) * p.d;
+            float x[S::NV][S::VEC], z[S::NV][S::VEC], dy[S::NV][S::VEC];
+            load_row<S>(p.x + at, l, p.d, true, x);
+            load_row<S>(p.dy + at, l, p.d, true, dy);
+            if (gate) load_row<S>(p.z + at, l, p.d, true, z);
+#pragma unroll
+            for (int k = 0; k < S::NV; ++k) {
+                const bool in = (k * S::LPG + l) * S::VEC < p.d;
+#pragma unroll
+                for (int j = 0; j < S::VEC; ++j) {
+                    const float n = (x[k][j] - st.x) * st.y;
+                    float dz = 0.f;
+                    const float du = norm_du(n, w[k][j], b[k][j], gate, gate ? z[k][j] : 0.f,
+                                             dy[k][j], p.act, dz);
+                    z[k][j] = dz;
+                    if (!in) continue;
+                    dw[k][j] = fmaf(du, n, dw[k][j]);
+                    db[k][j] += du;
+                    const float q = du * w[k][j];
+                    s1 += q;
+                    s2 = fmaf(q, n, s2);
+                }
+            }
+            if (gate) store_row<S>(p.dz + at, l, p.d, z);
+        }
+        s1 = block_sum(s1, sh);
+        s2 = block_sum(s2, sh);
+        if (threadIdx.x == 0) pieces[((size_t)tile + s) * p.H + h] = make_float2(s1, s2);
+    }
+    if (!p.part) return;
+    for (int which = 0; which < 2; ++which) {
+#pragma unroll
+        for (int k = 0; k < S::NV; ++k) {
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < S::VEC; ++j)
+                shw[g * kCh + l * S::VEC + j] = which ? db[k][j] : dw[k][j];
+            __syncthreads();
+            for (int i = threadIdx.x; i < kCh; i += kNormThreads) {
+                const int c = k * kCh + i;
+                if (c >= p.d) continue;
+                float v = 0.f;
+                for (int gg = 0; gg < S::kGroups; ++gg) v += shw[gg * kCh + i];
+                const size_t row = p.shared ? ((size_t)blockIdx.x * 2 + which)
+                                            : (((size_t)tile * 2 + which) * p.H + h);
+                p.part[row * p.d + c] = v;
+            }
+        }
+    }
+}
+
+// One warp per (sequence, head): means of q and q n over the group.
+__global__ void __launch_bounds__(128)
+norm_seq_join_sums(Seqs q, int H, int d, int tokens, int center, const float2* __restrict__ pieces,
+                   float2* __restrict__ means) {
+    const long long unit = (long long)blockIdx.x * 4 + threadIdx.x / 32;
+    const int lane = threadIdx.x & 31;
+    if (unit >= (long long)q.n * H) return;
+    const int s = (int)(unit / H), h = (int)(unit % H);
+    const int b = q.begin(s), e = q.end(s);
+    if (b >= e) return;
+    float s1 = 0.f, s2 = 0.f;
+    for (int i = b / tokens + lane; i <= (e - 1) / tokens; i += 32) {
+        const float2 v = pieces[((size_t)i + s) * H + h];
+        s1 += v.x;
+        s2 += v.y;
+    }
+    s1 = warp_sum(s1);
+    s2 = warp_sum(s2);
+    const float n = (float)(e - b) * d;
+    if (lane == 0) means[unit] = make_float2(center ? s1 / n : 0.f, s2 / n);
+}
+
+template <typename S>
+__global__ void __launch_bounds__(kNormThreads)
+norm_seq_bwd_apply(const NormParams<typename S::IO> p, int tokens,
+                   const float2* __restrict__ means) {
+    const int g = threadIdx.x / S::LPG, l = threadIdx.x % S::LPG;
+    const int tile = blockIdx.x / p.H, h = blockIdx.x % p.H;
+    const int t0 = (int)min((long long)p.q.total, (long long)tile * tokens);
+    const int t1 = (int)min((long long)p.q.total, (long long)t0 + tokens);
+    float w[S::NV][S::VEC], b[S::NV][S::VEC];
+    load_affine<S>(p.w, 1.f, h, l, p.d, p.shared, w);
+    load_affine<S>(p.b, 0.f, h, l, p.d, p.shared, b);
+    const bool gate = p.z != nullptr;
+    int s = t0 + g < t1 ? p.q.of(t0 + g) : 0;
+    for (int t = t0 + g; t < t1; t += S::kGroups) {
+        s = seq_from(p.q, s, t);
+        const float2 st = __ldg(reinterpret_cast<const float2*>(p.stats) + (size_t)s * p.H + h);
+        const float2 m = __ldg(means + (size_t)s * p.H + h);
+        const size_t at = ((size_t)t * p.H + h) * p.d;
+        float x[S::NV][S::VEC], z[S::NV][S::VEC], dy[S::NV][S::VEC];
+        load_row<S>(p.x + at, l, p.d, true, x);
+        load_row<S>(p.dy + at, l, p.d, true, dy);
+        if (gate) load_row<S>(p.z + at, l, p.d, true, z);
+#pragma unroll
+        for (int k = 0; k < S::NV; ++k) {
+#pragma unroll
+            for (int j = 0; j < S::VEC; ++j) {
+                const float n = (x[k][j] - st.x) * st.y;
+                float dz;
+                const float du = norm_du(n, w[k][j], b[k][j], gate, gate ? z[k][j] : 0.f,
+                                         dy[k][j], p.act, dz);
+                x[k][j] = st.y * (du * w[k][j] - m.x - n * m.y);
+            }
+        }
+        store_row<S>(p.dx + at, l, p.d, x);
+    }
+}
+
+// ---- launching ---------------------------------------------------------------------------------
+
+// Tokens of a tile in the statistics pass: what a block holds in registers.
+int stats_tile(const gdr_norm_args& a) {
+    const int v = a.io_dtype == GDR_BF16 ? 8 : 4;
+    const int n = a.d % v ? a.d : a.d / v;             // vectors of a row
+    const int nv = n <= 32 ? 1 : n <= 64 ? 2 : n <= 128 ? 4 : 8;
+    return norm_groups(a) * (8 / nv);
+}
+
+// Tokens of a tile in the other passes: a multiple of the block's lane groups, so many that the
+// partial sums stay small, so few that the blocks fill the GPU.
+int apply_tile(const gdr_norm_args& a) {
+    const int g = norm_groups(a);
+    const long long tokens = (long long)a.B * a.T;
+    long long per = tokens * a.H / (148 * 8) / g;
+    return (int)(per < 1 ? 1 : per > 64 ? 64 : per) * g;
+}
+
+long long tiles_of(const gdr_norm_args& a, int tile) {
+    return ((long long)a.B * a.T + tile - 1) / tile;
+}
+
+size_t pair_bytes(long long rows, int H) {
+    return align_up(sizeof(float2) * (size_t)rows * H, 256);
+}
+
+struct SeqStats {
+    template <typename S>
+    static void go(const gdr_norm_args& a, const NormPtrs& x, cudaStream_t st) {
+        norm_seq_stats<S><<<(unsigned)(tiles_of(a, stats_tile(a)) * a.H), kNormThreads, 0, st>>>(
+            norm_params<typename S::IO>(a, x));
+    }
+};
+
+struct SeqApply {
+    template <typename S>
+    static void go(const gdr_norm_args& a, const NormPtrs& x, cudaStream_t st) {
+        const int tile = apply_tile(a);
+        norm_seq_apply<S><<<(unsigned)(tiles_of(a, tile) * a.H), kNormThreads, 0, st>>>(
+            norm_params<typename S::IO>(a, x), tile);
+    }
+};
+
+unsigned unit_blocks(const gdr_norm_args& a) {
+    return (unsigned)(((long long)a.n_seqs * a.H + 3) / 4);
+}
+
+struct SeqBwd {
+    template <typename S>
+    static void go(const gdr_norm_args& a, const NormPtrs& x, cudaStream_t st) {
+        const int tile = apply_tile(a);
+        const long long tiles = tiles_of(a, tile);
+        const unsigned blocks = (unsigned)(tiles * a.H);
+        auto p = norm_params<typename S::IO>(a, x);
+        char* ws = reinterpret_cast<char*>(x.ws);
+        float2* pieces = reinterpret_cast<float2*>(ws);
+        float2* means = reinterpret_cast<float2*>(ws + pair_bytes(tiles + a.n_seqs, a.H));
+        p.part = reinterpret_cast<float*>(ws + pair_bytes(tiles + a.n_seqs, a.H) +
+                                          pair_bytes(a.n_seqs, a.H));
+        if (!x.dw && !x.db) p.part = nullptr;
+        if (tiles) {
+            norm_seq_bwd_sums<S><<<blocks, kNormThreads, 0, st>>>(p, tile, pieces);
+            norm_seq_join_sums<<<unit_blocks(a), 128, 0, st>>>(p.q, a.H, a.d, tile, a.center,
+                                                               pieces, means);
+            norm_seq_bwd_apply<S><<<blocks, kNormThreads, 0, st>>>(p, tile, means);
+        }
+        if (p.part)
+            launch_norm_reduce(a, p.part, (int)(a.shared_weight ? tiles * a.H : tiles), x.dw, x.db,
+                               st);
+    }
+};
+
+}  // namespace
+
+size_t norm_seq_fwd_workspace(const gdr_norm_args& a) {
+    return pair_bytes(tiles_of(a, stats_tile(a)) + a.n_seqs, a.H) + pair_bytes(a.n_seqs, a.H);
+}
+
+size_t norm_seq_bwd_workspace(const gdr_norm_args& a) {
+    const long long tiles = tiles_of(a, apply_tile(a));
+    return pair_bytes(tiles + a.n_seqs, a.H) + pair_bytes(a.n_seqs, a.H) +
+           align_up(sizeof(float) * 2 * (size_t)tiles * a.H * a.d, 256);
+}
+
+gdr_status launch_norm_seq_fwd(const gdr_norm_args& a, const NormPtrs& x, cudaStream_t st) {
+    const int tile = stats_tile(a);
+    const long long tiles = tiles_of(a, tile);
+    NormPtrs y = x;
+    const float2* part = reinterpret_cast<const float2*>(x.ws);
+    if (!y.stats)
+        y.stats = reinterpret_cast<float*>(reinterpret_cast<char*>(x.ws) +
+                                           pair_bytes(tiles + a.n_seqs, a.H));
+    y.stats_in = y.stats;
+    if (tiles && norm_dispatch<SeqStats>(a, y, st) != GDR_OK) return GDR_ERR_CUDA;
+    norm_seq_join_stats<<<unit_blocks(a), 128, 0, st>>>(
+        Seqs{x.cu, a.n_seqs, a.T, a.B * a.T}, a.H, a.d, tile, a.eps, part,
+        reinterpret_cast<float2*>(y.stats));
+    if (cudaGetLastError() != cudaSuccess) return GDR_ERR_CUDA;
+    return tiles ? norm_dispatch<SeqApply>(a, y, st) : GDR_OK;
+}
+
+gdr_status launch_norm_seq_bwd(const gdr_norm_args& a, const NormPtrs& x, cudaStream_t st) {
+    return norm_dispatch<SeqBwd>(a, x, st);
+}
+
+}  // namespace gdr

@@ -345,6 +345,184 @@ gdr_status gdr_decode_step(const gdr_decode_args* args,
                            const void* g, const void* beta,
                            float* S_inout, void* o, void* stream);
 
+/*
+ * ---- Operators around the recurrence --------------------------------------------------------
+ *
+ * The rest of a recurrent layer: the short causal convolution in front of the delta rule, the
+ * gated linear recurrence (diagonal: one state per channel) that can stand beside it or in its
+ * place, and the group norm behind either.  They follow the conventions above, with these
+ * additions:
+ * - The tokens are B rows of T, or with cu_seqlens (B == 1) packed sequences of T tokens
+ *   together; sequences of no or one token are allowed.
+ * - reverse = 1 runs every sequence from its last token to its first, in place: "scan order"
+ *   below is that order, and outputs stand at each token's own position.
+ * - No workspace except where a `_workspace_size` is declared.  A cu_seqlens that does not
+ *   start at 0, decreases or does not end at T is reported as GDR_ERR_DEVICE_CHECK in
+ *   args->status (an optional device int as in gdr_chunk_args); the outputs are then
+ *   unspecified, but no access leaves the tensors.
+ * - Channel arrays (weights, biases, their gradients) are fp32 and 4-byte aligned, everything
+ *   else 16-byte aligned.  An output may not overlap an input unless that is said.
+ * - Sums, states and statistics are fp32; results are rounded once.  Repeated calls give the
+ *   same bits.  Calls that overlap on the GPU share nothing but their arguments.
+ */
+
+/*
+ * Gated linear recurrence over D independent channels, alpha_t = exp(g_t):
+ *
+ *     h_t = alpha_t h_{t-1} + b_t,    o_t = h_t
+ *     b_t = v_t                  write = GDR_WRITE_PLAIN
+ *     b_t = beta_t v_t           write = GDR_WRITE_GATE
+ *     b_t = (1 - alpha_t) v_t    write = GDR_WRITE_TIED
+ *
+ * g may be -inf (alpha = 0: the state is dropped).  Where decays grow (g > 0), their product
+ * over any run of tokens of a sequence has to stay in the fp32 range, since runs of tokens are
+ * formed at once and joined by it.  A sequence never sees another one's values, infinities and
+ * NaN included.
+ */
+typedef enum { GDR_WRITE_PLAIN = 0, GDR_WRITE_GATE = 1, GDR_WRITE_TIED = 2 } gdr_write;
+
+typedef struct {
+    int B, T;              /* rows and tokens per row (with cu_seqlens B must be 1);
+                              B * T <= 2^31 - 2^16 */
+    int D;                 /* channels (heads times head size), any number >= 1 */
+    int n_seqs;            /* == B without cu_seqlens */
+    gdr_dtype io_dtype;    /* v, o and their gradients */
+    gdr_dtype gate_dtype;  /* g, beta and their gradients */
+    gdr_write write;
+    int reverse;
+    int* status;
+} gdr_scan_args;
+
+/*
+ *   v, o         [B, T, D] io_dtype
+ *   g, beta      [B, T, D] gate_dtype (beta with GDR_WRITE_GATE only, else NULL)
+ *   h0           [n_seqs, D] fp32 or NULL for zero
+ *   h_final      [n_seqs, D] fp32 or NULL; may alias h0.  An empty sequence keeps its h0.
+ */
+gdr_status gdr_scan_fwd(const gdr_scan_args* args, const void* v, const void* g,
+                        const void* beta, const float* h0, const int32_t* cu_seqlens,
+                        void* o, float* h_final, void* stream);
+
+/*
+ * Gradients of <dO, o> + <dh_final, h_final> with respect to v, g, beta and h0:
+ *     lam_t = dO_t + m_{t+1},  m_t = alpha_t lam_t,  m behind the last token = dh_final
+ *     dv = lam | beta lam | (1 - alpha) lam      dbeta = v lam
+ *     dg = m h_{t-1}  (TIED: m (h_{t-1} - v))    dh0 = m of the first token
+ * h_{t-1} is read from o, as gdr_scan_fwd wrote it (for bf16, with that rounding).
+ *   v            not read with GDR_WRITE_PLAIN (may be NULL there)
+ *   dh_final     [n_seqs, D] fp32 or NULL for zero;  dh0 [n_seqs, D] fp32 or NULL; may alias
+ *                dh_final
+ *   dv, dg, dbeta   outputs, shaped and typed as v, g, beta
+ */
+gdr_status gdr_scan_bwd(const gdr_scan_args* args, const void* v, const void* g,
+                        const void* beta, const void* o, const void* dO, const float* h0,
+                        const int32_t* cu_seqlens, const float* dh_final, void* dv, void* dg,
+                        void* dbeta, float* dh0, void* stream);
+
+/*
+ * One token for each of B sequences (T == 1, n_seqs == B): v, g, beta, o [B, D]; the state h
+ * [B, D] fp32 is read and the new one written to h_out, which may be h itself.
+ */
+gdr_status gdr_scan_step(const gdr_scan_args* args, const void* v, const void* g,
+                         const void* beta, const float* h, float* h_out, void* o, void* stream);
+
+/*
+ * Short causal depthwise convolution with an activation, over scan order:
+ *
+ *     p_t = bias + sum_{j < width} w[c][width - 1 - j] x_{t-j},   y_t = act(p_t)
+ *
+ * with the inputs before a sequence's first token taken from its state, or zero.
+ */
+typedef enum { GDR_ACT_NONE = 0, GDR_ACT_SILU = 1, GDR_ACT_SIGMOID = 2 } gdr_activation;
+
+typedef struct {
+    int B, T, D, n_seqs;   /* as in gdr_scan_args */
+    int width;             /* 2, 3 or 4 */
+    gdr_dtype io_dtype;    /* x, y, the states and their gradients */
+    gdr_activation activation;  /* GDR_ACT_NONE or GDR_ACT_SILU */
+    int reverse;
+    int* status;
+} gdr_conv_args;
+
+/*
+ *   x, y         [B, T, D] io_dtype;  w [D, width] fp32;  bias [D] fp32 or NULL
+ *   state        [n_seqs, width - 1, D] io_dtype, oldest input first, or NULL for zero
+ *   state_out    [n_seqs, width - 1, D] io_dtype or NULL: every sequence's last width - 1
+ *                inputs (its state's behind them where it is shorter); must not overlap state
+ */
+gdr_status gdr_conv_fwd(const gdr_conv_args* args, const void* x, const float* w,
+                        const float* bias, const void* state, const int32_t* cu_seqlens,
+                        void* y, void* state_out, void* stream);
+
+/*
+ * Gradients of <dy, y>; p is formed again from x.  dw [D, width], dbias [D] (or NULL), dx
+ * [B, T, D], dstate [n_seqs, width - 1, D] io_dtype (or NULL).
+ *   workspace    at least gdr_conv_bwd_workspace_size(args) bytes, 256-byte aligned, no
+ *                initialisation needed
+ */
+size_t gdr_conv_bwd_workspace_size(const gdr_conv_args* args);
+gdr_status gdr_conv_bwd(const gdr_conv_args* args, const void* x, const float* w,
+                        const float* bias, const void* dy, const void* state,
+                        const int32_t* cu_seqlens, void* dx, float* dw, float* dbias,
+                        void* dstate, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One token for each of B sequences (T == 1, n_seqs == B): x, y [B, D]; state
+ * [B, width - 1, D]; state_out receives the state with x appended, and may be state itself.
+ */
+gdr_status gdr_conv_step(const gdr_conv_args* args, const void* x, const float* w,
+                         const float* bias, const void* state, void* state_out, void* y,
+                         void* stream);
+
+/*
+ * Group norm with an activation, channels last: the H groups are the heads of x [B, T, H, d].
+ *
+ *     n = (x - mean) / sqrt(var + eps)        center = 1
+ *     n = x / sqrt(mean(x^2) + eps)           center = 0
+ *     u = n w + bias,    y = u act(z) with a gate z, y = act(u) without
+ *
+ * The statistics of a group are over the d channels of one token (per_sequence = 0: the output
+ * norm of gated_rmsnorm kind, as gdr_decode_step fuses it), or over those of all tokens of a
+ * sequence (per_sequence = 1).
+ */
+typedef struct {
+    int B, T, H, d, n_seqs;
+    gdr_dtype io_dtype;    /* x, z, y and their gradients */
+    int per_sequence;
+    int center;
+    gdr_activation activation;
+    int shared_weight;     /* 1: w, bias and their gradients are [d], for every head; 0: [H, d] */
+    float eps;             /* finite, >= 0 */
+    int* status;
+} gdr_norm_args;
+
+/*
+ *   x, z, y      [B, T, H, d] io_dtype; z NULL for no gate
+ *   w, bias      fp32 [H, d] or [d]; NULL for ones and zeros
+ *   cu_seqlens   read with per_sequence only
+ *   stats        [n_seqs, H, 2] fp32 or NULL, per_sequence only: mean (0 without center) and
+ *                1 / sqrt(var + eps) of every group, for the backward pass
+ *   workspace    at least gdr_norm_fwd_workspace_size(args) bytes (0 unless per_sequence; then
+ *                NULL is allowed), 256-byte aligned, no initialisation needed
+ * Sizes: d up to 1024 where d elements are a multiple of 16 bytes, else up to 256.
+ */
+size_t gdr_norm_fwd_workspace_size(const gdr_norm_args* args);
+gdr_status gdr_norm_fwd(const gdr_norm_args* args, const void* x, const float* w,
+                        const float* bias, const void* z, const int32_t* cu_seqlens, void* y,
+                        float* stats, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of <dy, y>; the normalised values are formed again from x.
+ *   stats        as gdr_norm_fwd wrote them; required with per_sequence, else ignored
+ *   dx, dz       [B, T, H, d] (dz with z only); dw, dbias shaped as w, bias, or NULL
+ */
+size_t gdr_norm_bwd_workspace_size(const gdr_norm_args* args);
+gdr_status gdr_norm_bwd(const gdr_norm_args* args, const void* x, const float* w,
+                        const float* bias, const void* z, const void* dy,
+                        const int32_t* cu_seqlens, const float* stats, void* dx, float* dw,
+                        float* dbias, void* dz, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
 /* Human-readable name of a status. */
 const char* gdr_status_string(gdr_status status);
 

@@ -1,0 +1,127 @@
+"""The operators together, as a recurrent layer uses them: convolution, recurrence, gated norm,
+with gradients through all three, and one token at a time behind a prefill."""
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_146_b200 as gdr
+from oracle import layer as ol
+
+pytestmark = pytest.mark.gpu
+
+
+def layer_inputs(T, H, d, n, dtype, seed):
+    g = torch.Generator().manual_seed(seed)
+    rn = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    D = H * d
+    return dict(x=rn(1, T, D).to(dtype), w=0.5 * rn(D, 4), b=0.2 * rn(D),
+                g=(-torch.nn.functional.softplus(rn(1, T, D) - 2)).to(dtype),
+                z=rn(1, T, H, d).to(dtype), nw=1 + 0.1 * rn(d), dy=rn(1, T, H, d).to(dtype),
+                st=rn(n, 3, D).to(dtype), h0=rn(n, D))
+
+
+def reference(x, cu, H, d):
+    f = {k: ol.f64(t) for k, t in x.items()}
+    flat = {k: f[k].reshape(-1, H * d) for k in ("x", "g")}
+    v, st, _ = ol.conv(flat["x"], f["w"], f["b"], f["st"], cu)
+    h, hf = ol.scan(v, flat["g"], None, f["h0"], cu, tied=True)
+    z, dy = (f[k].reshape(-1, H, d) for k in ("z", "dy"))
+    y, _ = ol.norm(h.reshape(-1, H, d), f["nw"], None, z, cu, center=False)
+    dh, dnw, _, dz = ol.norm_backward(h.reshape(-1, H, d), f["nw"], None, z, dy, cu, center=False)
+    dv, dg, _, dh0 = ol.scan_backward(v, flat["g"], None, h, dh.reshape(-1, H * d), f["h0"], None,
+                                      cu, tied=True)
+    dx, dw, db, dst = ol.conv_backward(flat["x"], f["w"], f["b"], dv, f["st"], cu)
+    return dict(y=y, st=st, hf=hf, dnw=dnw.sum(0), dz=dz, dg=dg, dh0=dh0, dx=dx, dw=dw, db=db, dst=dst)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_layer_with_its_gradients(dtype):
+    H, d, lengths = 3, 64, [70, 0, 1, 130]
+    cu = np.concatenate([[0], np.cumsum(lengths)]).tolist()
+    x = layer_inputs(cu[-1], H, d, len(lengths), dtype, 1)
+    t = {k: v.cuda() for k, v in x.items()}
+    c = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    v, st = gdr.short_conv_fwd(t["x"], t["w"], t["b"], t["st"], c)
+    h, hf = gdr.linear_scan_fwd(v, t["g"], None, t["h0"], c, tied=True)
+    hh = h.view(1, -1, H, d)
+    y = gdr.group_norm_fwd(hh, t["nw"], None, t["z"], center=False)
+    dh, dnw, _, dz = gdr.group_norm_bwd(hh, t["nw"], None, t["z"], t["dy"], center=False)
+    dv, dg, _, dh0 = gdr.linear_scan_bwd(v, t["g"], None, h, dh.view_as(v), t["h0"], c, tied=True)
+    dx, dw, db, dst = gdr.short_conv_bwd(t["x"], t["w"], t["b"], dv, t["st"], c)
+    got = dict(y=y, st=st, hf=hf, dnw=dnw, dz=dz, dg=dg, dh0=dh0, dx=dx, dw=dw, db=db, dst=dst)
+    want = reference(x, cu, H, d)
+    # Relative to the tensor's 2-norm.  fp32: each operator is within a few hundred steps of its
+    # inputs' precision (layer_helpers), 6e-8 each.  bf16: at most six tensors rounded on the
+    # way (v, h, dh, dv and the result, v and h taken twice), each off by 2^-8 at most and a
+    # third of a step's square on average, 2^-8 / sqrt(3); the norm's division by small groups
+    # can double a share.
+    tol = 3e-5 if dtype == torch.float32 else 2 * 6 ** 0.5 * 2.0 ** -8
+    for k, w in want.items():
+        a = ol.f64(got[k]).reshape(w.shape)
+        off = np.linalg.norm(a - w) / np.linalg.norm(w)
+        assert off <= (0 if k == "st" else tol), (k, off)
+
+
+def test_prefill_then_tokens():
+    """A prompt through the sequence forms, then single tokens from the states they leave, equal
+    the whole sequence through the sequence forms."""
+    N, T, extra, H, d = 3, 33, 6, 2, 64
+    x = layer_inputs(N * (T + extra), H, d, N, torch.bfloat16, 2)
+    t = {k: v.cuda() for k, v in x.items()}
+    D = H * d
+    rows = {k: t[k].view(N, T + extra, D) for k in ("x", "g", "z")}
+
+    def sequence(lo, hi, st, h):
+        part = {k: v[:, lo:hi].contiguous() for k, v in rows.items()}
+        v, st = gdr.short_conv_fwd(part["x"], t["w"], t["b"], st)
+        o, h = gdr.linear_scan_fwd(v, part["g"], None, h, tied=True)
+        return gdr.group_norm_fwd(o.view(N, hi - lo, H, d), t["nw"], None,
+                                  part["z"].view(N, hi - lo, H, d), center=False), st, h
+
+    whole, st_w, h_w = sequence(0, T + extra, t["st"], t["h0"])
+    y, st, h = sequence(0, T, t["st"], t["h0"])
+    outs = [y]
+    for i in range(T, T + extra):
+        tok = {k: v[:, i].contiguous() for k, v in rows.items()}
+        v = gdr.short_conv_step(tok["x"], t["w"], t["b"], st)
+        o = gdr.linear_scan_step(v, tok["g"], None, h, tied=True)
+        outs.append(gdr.group_norm_fwd(o.view(N, 1, H, d), t["nw"], None,
+                                       tok["z"].view(N, 1, H, d), center=False))
+    assert torch.equal(st, st_w)
+    # the scan joins its runs in another order than the tokens one by one: fp32 states differ by
+    # a few steps, and a bf16 value next to a border by one step of bf16, twice (o and y)
+    assert (h - h_w).abs().max() <= 1e-5 * h_w.abs().max()
+    got, want = torch.cat(outs, 1).float(), whole.float()
+    assert ((got - want).abs() <= 2.0 ** -6 * want.abs() + 1e-3).all()
+    assert (got != want).float().mean() < 0.02
+
+
+def test_the_norm_behind_the_delta_rule():
+    """The output norm of the decode step's epilogue, for whole sequences behind chunk_fwd."""
+    H, d, T = 2, 64, 100
+    g = torch.Generator().manual_seed(3)
+    rn = lambda *s: torch.randn(*s, generator=g).cuda()  # noqa: E731
+    q, k, v, z = (rn(1, T, H, d) for _ in range(4))
+    gate, beta = -torch.nn.functional.softplus(rn(1, T, H) - 2), torch.sigmoid(rn(1, T, H))
+    w = 1 + 0.1 * rn(d)
+    o, _ = gdr.chunk_fwd(q, k, v, gate, beta)
+    y = gdr.group_norm_fwd(o, w, None, z, center=False, eps=1e-6)
+    S = torch.zeros(1, H, d, d, device="cuda")
+    for t in range(T):
+        step = gdr.decode_step(*(a[:, t].clone() for a in (q, k, v, gate, beta)), S,
+                               norm_z=z[:, t].clone(), norm_weight=w, norm_eps=1e-6)
+        # both within 1e-4 of the recurrence (the bound of its fp32 form), times the norm's gain
+        scale = 1 / o[:, t].square().mean(-1, keepdim=True).sqrt()
+        assert ((step - y[:, t]).abs() <= 3e-4 * (1 + scale) * (1 + z[:, t].abs())).all()
+
+
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="one GPU")
+def test_tensors_of_another_device_than_the_current_one():
+    x = torch.randn(1, 70, 64, device="cuda:1")
+    w = torch.randn(64, 4, device="cuda:1")
+    with torch.cuda.device(0):
+        a, _ = gdr.short_conv_fwd(x, w)
+        b, _ = gdr.linear_scan_fwd(x, -x.abs())
+    with torch.cuda.device(1):
+        assert torch.equal(a, gdr.short_conv_fwd(x, w)[0])
+        assert torch.equal(b, gdr.linear_scan_fwd(x, -x.abs())[0])
