@@ -10,8 +10,11 @@ namespace gdr {
 
 namespace {
 
-constexpr int kSeg = 8;  // tokens of a lane's run
-constexpr int kTile = kScanWarps * kSeg;
+constexpr int kStages = 3;
+
+// Tokens of a warp's run: eight in bf16, four where fp32 doubles the bytes of a tile.
+template <typename IO, typename GT>
+constexpr int seg_of = sizeof(IO) + sizeof(GT) > 4 ? 4 : 8;
 
 template <typename IO, typename GT>
 struct FwdParams {
@@ -37,113 +40,198 @@ __device__ __forceinline__ void decay_write(float g, float v, float beta, float&
     }
 }
 
+template <typename IO, typename GT, int kWrite>
+constexpr int stage_bytes = Rows<IO, seg_of<IO, GT>>::kBytes +
+                            (kWrite == GDR_WRITE_GATE ? 2 : 1) * Rows<GT, seg_of<IO, GT>>::kBytes;
+
+// One tile's elements of a lane, from the forming of its run to the output.
+template <int kSeg>
+struct Elements {
+    float a[kSeg][2], b[kSeg][2];
+    Run before;  // the block's runs before the warp's
+    Marks m;
+};
+
 // kSeqs: one row holds all sequences, whose starts reset the state; else a row is a sequence.
-template <typename IO, typename GT, int kWrite, int VEC, bool kSeqs>
-__global__ void __launch_bounds__(kScanThreads)
+template <typename IO, typename GT, int kWrite, Copy kCopy, bool kSeqs>
+__global__ void __launch_bounds__(kScanThreads, 2)
 scan_fwd_kernel(const FwdParams<IO, GT> p, const int cluster) {
-    __shared__ ScanShared<VEC> sh;
+    extern __shared__ __align__(128) char stages[];
+    __shared__ ScanShared sh;
+    constexpr int kSeg = seg_of<IO, GT>, kTile = kScanWarps * kSeg;
+    constexpr int kStage = stage_bytes<IO, GT, kWrite>;
+    using RowsIO = Rows<IO, kSeg>;
+    using RowsGT = Rows<GT, kSeg>;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int rank = blockIdx.x % cluster;
     const int unit = blockIdx.x / cluster;
     const int slab = unit % p.slabs, row = unit / p.slabs;
-    const int c = (slab * 32 + lane) * VEC;
-    const bool on = c < p.D;
-    const int L = p.L;
-    const size_t row0 = (size_t)row * L;
+    const int left = p.D - slab * kSlab;       // channels of the slab
+    const int c = slab * kSlab + 2 * lane, mine = left - 2 * lane;
+    const int L = p.L, D = p.D;
+    const int origin = p.reverse ? L - 1 : 0, dir = p.reverse ? -1 : 1;
 
     if (kSeqs && blockIdx.x == 0) check_cu(p.q, p.status, tid, kScanThreads);
-    if (kSeqs && rank == 0 && p.h_final && on) {  // empty sequences keep their state
+    if (kSeqs && rank == 0 && p.h_final) {  // empty sequences keep their state
         for (int s = wid; s < p.q.n; s += kScanWarps) {
             if (p.q.begin(s) != p.q.end(s)) continue;
-            float x[VEC] = {};
-            if (p.h0) load_f<float, VEC>(p.h0 + (size_t)s * p.D + c, x);
-            store_vec<float, VEC>(p.h_final + (size_t)s * p.D + c, x);
+            float x[2] = {};
+            if (p.h0) load_state<kCopy>(p.h0 + (size_t)s * D + c, x, mine);
+            store_pair<float, kCopy>(p.h_final + (size_t)s * D + c, x, mine);
         }
     }
 
-    float carry[VEC] = {};
-    if (!kSeqs && p.h0 && on) load_f<float, VEC>(p.h0 + (size_t)row * p.D + c, carry);
-
-    Vec<IO, VEC> rv[kSeg];
-    Vec<GT, VEC> rg[kSeg], rb[kSeg];
-    auto place = [&](int i) { return p.reverse ? L - 1 - i : i; };
-    auto fetch = [&](int first) {
-#pragma unroll
-        for (int i = 0; i < kSeg; ++i) {
-            if (!on || first + i >= L) continue;
-            const size_t at = (row0 + place(first + i)) * p.D + c;
-            rv[i] = load_vec<IO, VEC>(p.v + at);
-            rg[i] = load_vec<GT, VEC>(p.g + at);
-            if constexpr (kWrite == GDR_WRITE_GATE) rb[i] = load_vec<GT, VEC>(p.beta + at);
-        }
+    const size_t base = (size_t)row * L * D + slab * kSlab;
+    char* const buf = stages + wid * kStages * kStage;
+    auto feed = [&](int first, int stage) {
+        char* s = buf + stage * kStage;
+        feed_rows<IO, kCopy, kSeg>(s, p.v + base, origin, dir, first, L, D, left, lane);
+        s += RowsIO::kBytes;
+        feed_rows<GT, kCopy, kSeg>(s, p.g + base, origin, dir, first, L, D, left, lane);
+        if constexpr (kWrite == GDR_WRITE_GATE)
+            feed_rows<GT, kCopy, kSeg>(s + RowsGT::kBytes, p.beta + base, origin, dir, first, L, D, left,
+                                 lane);
     };
 
     const int stride = cluster * kTile;
-    int first = rank * kTile + wid * kSeg;
-    fetch(first);
-    int step = 0;
-    for (int base = 0; base < L; base += stride, first += stride, ++step) {
-        const int n = min(kSeg, L - first);  // tokens of this lane's run (may be <= 0)
-        float a[kSeg][VEC], b[kSeg][VEC];
+    const int steps = (int)(((long long)L + stride - 1) / stride);
+    const int first0 = rank * kTile + wid * kSeg;
+    // places behind L may pass 2^31: a tile that starts there is empty
+    auto place = [&](int k) {
+        const long long f = first0 + (long long)k * stride;
+        return (int)(f < L ? f : L);
+    };
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) {
+        feed(place(k), k);
+        copy_commit();
+    }
+
+    Here here{0, 0};
+    int stage = 0;  // of the next tile to be formed
+    // Forms the run of tile k and hands it to the block.
+    auto form = [&](int k, Elements<kSeg>& e) {
+        copy_wait<kStages - 2>();
+        __syncwarp();
+        // the stage of the tile before: every lane has read it
+        feed(place(k + kStages - 1), stage == 0 ? kStages - 1 : stage - 1);
+        copy_commit();
+        const char* s = buf + stage * kStage;
+        stage = stage == kStages - 1 ? 0 : stage + 1;
 #pragma unroll
         for (int i = 0; i < kSeg; ++i) {
+            float v[2], g[2], w[2] = {};
+            RowsIO::read(s, i, lane, v);
+            RowsGT::read(s + RowsIO::kBytes, i, lane, g);
+            if constexpr (kWrite == GDR_WRITE_GATE)
+                RowsGT::read(s + RowsIO::kBytes + RowsGT::kBytes, i, lane, w);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                if (i < n && on)
-                    decay_write<kWrite>(to_f(rg[i].x[j]), to_f(rv[i].x[j]),
-                                        kWrite == GDR_WRITE_GATE ? to_f(rb[i].x[j]) : 0.f,
-                                        a[i][j], b[i][j]);
-                else { a[i][j] = 1.f; b[i][j] = 0.f; }
-            }
+            for (int j = 0; j < 2; ++j) decay_write<kWrite>(g[j], v[j], w[j], e.a[i][j], e.b[i][j]);
         }
-        fetch(first + stride);
-
-        Marks m{0u, 0u, 0};
         if constexpr (kSeqs) {
-            m = find_marks<kSeg>(p.q, [&](int i) { return place(first + i); }, n, p.reverse, lane);
-            if (m.start && p.h0) {  // b at a start takes the initial state in
+            const int first = place(k);
+            e.m = find_marks(p.q, here, origin, dir, first, min(kSeg, L - first), lane);
+            if (e.m.start && p.h0) {  // b at a start takes the initial state in
 #pragma unroll
                 for (int i = 0; i < kSeg; ++i) {
-                    if (!(m.start >> i & 1u)) continue;
-                    const int s = __shfl_sync(0xffffffffu, m.seq, i);
-                    float x[VEC] = {};
-                    if (on) load_f<float, VEC>(p.h0 + (size_t)s * p.D + c, x);
+                    if (!(e.m.start >> i & 1u)) continue;
+                    const int q = __shfl_sync(0xffffffffu, e.m.seq, i);
+                    float x[2];
+                    load_state<kCopy>(p.h0 + (size_t)q * D + c, x, mine);
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) b[i][j] = fmaf(a[i][j], x[j], b[i][j]);
+                    for (int j = 0; j < 2; ++j) e.b[i][j] = fmaf(e.a[i][j], x[j], e.b[i][j]);
                 }
             }
         }
-        Run<VEC> run;
+        Run run;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            float A = 1.f, H = 0.f;
+        for (int j = 0; j < 2; ++j) {
+            float A = e.a[0][j], H = e.b[0][j];
 #pragma unroll
-            for (int i = 0; i < kSeg; ++i) {
-                H = kSeqs && (m.start >> i & 1u) ? b[i][j] : fmaf(a[i][j], H, b[i][j]);
-                A *= a[i][j];
+            for (int i = 1; i < kSeg; ++i) {
+                const float y = fmaf(e.a[i][j], H, e.b[i][j]);
+                H = kSeqs && (e.m.start >> i & 1u) ? e.b[i][j] : y;
+                A *= e.a[i][j];
             }
-            run.A[j] = kSeqs && m.start ? kReset : A;
+            run.A[j] = kSeqs && e.m.start ? kReset : A;
             run.H[j] = H;
         }
-        float h[VEC];
-        join_runs(sh, run, step, cluster, rank, wid, lane, carry, h);
+        sh.warp[k & 1][wid][lane] = run;
+    };
+
+    float carry[2] = {};
+    if (!kSeqs && p.h0) load_state<kCopy>(p.h0 + (size_t)row * D + c, carry, mine);
+
+    auto cl = cooperative_groups::this_cluster();
+    Run whole;   // the block's tile, where the cluster is the block
+    // Joins the block's runs of tile k and, in a cluster, hands the result to every block.
+    auto publish = [&](int k, Elements<kSeg>& e) {
+        join_block<kSeqs>(sh.warp[k & 1], wid, lane, e.before, whole);
+        if (cluster > 1) {
+            if (wid < cluster) *cl.map_shared_rank(&sh.block[k & 3][rank][lane], wid) = whole;
+            cl.barrier_arrive();
+        }
+    };
+    // Finishes tile k: its states from the carry, which becomes the state behind the step.
+    auto finish = [&](int k, const Elements<kSeg>& e, const Run& tile) {
+        float h[2];
+        if (cluster == 1) {
+            h[0] = carry[0];
+            h[1] = carry[1];
+            run_apply<kSeqs>(tile, carry);
+        } else {
+            for (int r = 0; r < cluster; ++r) {
+                if (r == rank) { h[0] = carry[0]; h[1] = carry[1]; }
+                run_apply<kSeqs>(sh.block[k & 3][r][lane], carry);
+            }
+        }
+        run_apply<kSeqs>(e.before, h);
+        const int first = place(k), n = min(kSeg, L - first);
+        IO* out = p.o + base + (long long)(origin + dir * first) * D + 2 * lane;
+        const long long next = (long long)dir * D;
 #pragma unroll
         for (int i = 0; i < kSeg; ++i) {
 #pragma unroll
-            for (int j = 0; j < VEC; ++j)
-                h[j] = kSeqs && (m.start >> i & 1u) ? b[i][j] : fmaf(a[i][j], h[j], b[i][j]);
-            if (i < n && on) store_vec<IO, VEC>(p.o + (row0 + place(first + i)) * p.D + c, h);
-            if (kSeqs && (m.end >> i & 1u) && p.h_final) {
-                const int s = __shfl_sync(0xffffffffu, m.seq, i);
-                if (on) store_vec<float, VEC>(p.h_final + (size_t)s * p.D + c, h);
+            for (int j = 0; j < 2; ++j) {
+                const float y = fmaf(e.a[i][j], h[j], e.b[i][j]);
+                h[j] = kSeqs && (e.m.start >> i & 1u) ? e.b[i][j] : y;
+            }
+            if (i < n) store_pair<IO, kCopy>(out, h, mine);
+            out += next;
+            if (kSeqs && (e.m.end >> i & 1u) && p.h_final) {
+                const int q = __shfl_sync(0xffffffffu, e.m.seq, i);
+                store_pair<float, kCopy>(p.h_final + (size_t)q * D + c, h, mine);
             }
         }
+    };
+
+    // One step of the walk: tile k + 1's run goes out before tile k is finished.  The block
+    // barrier between form and publish also keeps the parities apart: a run is written again two
+    // tiles later, behind a barrier that every reader of the first has passed.
+    auto turn = [&](int k, Elements<kSeg>& now, Elements<kSeg>& next) {
+        const Run tile = whole;
+        if (k + 1 < steps) {
+            form(k + 1, next);
+            __syncthreads();
+        }
+        if (cluster > 1) cl.barrier_wait();
+        if (k + 1 < steps) publish(k + 1, next);
+        finish(k, now, tile);
+    };
+    Elements<kSeg> even, odd;
+    form(0, even);
+    __syncthreads();
+    publish(0, even);
+    for (int k = 0; k < steps; k += 2) {
+        turn(k, even, odd);
+        if (k + 1 < steps) turn(k + 1, odd, even);
     }
-    if (!kSeqs && p.h_final && rank == 0 && wid == 0 && on)
-        store_vec<float, VEC>(p.h_final + (size_t)row * p.D + c, carry);
+    copy_wait<0>();
+    if (!kSeqs && p.h_final && rank == 0 && wid == 0)
+        store_pair<float, kCopy>(p.h_final + (size_t)row * D + c, carry, mine);
 }
 
-template <typename IO, typename GT, int kWrite, int VEC>
+template <typename IO, typename GT, int kWrite, Copy kCopy>
 gdr_status fwd_launch(const gdr_scan_args& a, const ScanPtrs& x, cudaStream_t st) {
     const bool seqs = scan_one_row(a, x.cu);
     FwdParams<IO, GT> p;
@@ -157,22 +245,24 @@ gdr_status fwd_launch(const gdr_scan_args& a, const ScanPtrs& x, cudaStream_t st
     p.q = Seqs{x.cu, a.n_seqs, a.T, a.B * a.T};
     p.D = a.D;
     p.L = seqs ? a.B * a.T : a.T;
-    p.slabs = (a.D + 32 * VEC - 1) / (32 * VEC);
+    p.slabs = (a.D + kSlab - 1) / kSlab;
     p.reverse = a.reverse;
     const long long units = (long long)p.slabs * (seqs ? 1 : a.B);
-    return seqs ? scan_launch(scan_fwd_kernel<IO, GT, kWrite, VEC, true>, p, units, p.L, kTile, st)
-                : scan_launch(scan_fwd_kernel<IO, GT, kWrite, VEC, false>, p, units, p.L, kTile, st);
-}
-
-template <typename IO, typename GT, int kWrite>
-gdr_status fwd_vec(const gdr_scan_args& a, const ScanPtrs& x, cudaStream_t st) {
-    return a.D % 2 ? fwd_launch<IO, GT, kWrite, 1>(a, x, st) : fwd_launch<IO, GT, kWrite, 2>(a, x, st);
+    const int tile = kScanWarps * seg_of<IO, GT>;
+    const size_t smem = (size_t)kScanWarps * kStages * stage_bytes<IO, GT, kWrite>;
+    return seqs ? scan_launch(scan_fwd_kernel<IO, GT, kWrite, kCopy, true>, p, units, p.L, tile, smem, st)
+                : scan_launch(scan_fwd_kernel<IO, GT, kWrite, kCopy, false>, p, units, p.L, tile, smem, st);
 }
 
 struct Fwd {
     template <typename IO, typename GT, int kWrite>
     static gdr_status go(const gdr_scan_args& a, const ScanPtrs& x, cudaStream_t st) {
-        return fwd_vec<IO, GT, kWrite>(a, x, st);
+        const Copy copy = scan_copy(a);
+        if (copy == kCopy16) return fwd_launch<IO, GT, kWrite, kCopy16>(a, x, st);
+        if constexpr (sizeof(IO) == sizeof(GT)) {
+            if (copy == kCopyPair) return fwd_launch<IO, GT, kWrite, kCopyPair>(a, x, st);
+        }
+        return fwd_launch<IO, GT, kWrite, kCopyOne>(a, x, st);
     }
 };
 

@@ -12,7 +12,8 @@ namespace gdr {
 
 namespace {
 
-constexpr int kSeg = 4;
+constexpr int kStages = 4;
+constexpr int kSeg = 4;                    // tokens of a warp's run
 constexpr int kTile = kScanWarps * kSeg;
 
 template <typename IO, typename GT>
@@ -26,136 +27,209 @@ struct BwdParams {
     int D, L, slabs, reverse;
 };
 
-template <typename IO, typename GT, int kWrite, int VEC, bool kSeqs>
-__global__ void __launch_bounds__(kScanThreads)
+// Where a warp's tokens of each tensor lie in a stage: g, dO, o of the token before, v, beta.
+template <typename IO, typename GT, int kWrite>
+struct Stage {
+    static constexpr int kG = Rows<GT, kSeg>::kBytes, kI = Rows<IO, kSeg>::kBytes;
+    static constexpr int dO = kG, o = dO + kI, v = o + kI, beta = v + kI;
+    static constexpr int kBytes = v + (kWrite == GDR_WRITE_PLAIN ? 0 : kI) +
+                                  (kWrite == GDR_WRITE_GATE ? kG : 0);
+};
+
+struct Elements {
+    float a[kSeg][2], d[kSeg][2];  // alpha; dO, with dh_final at a sequence's last token
+    Run before;
+    Marks m;                       // start: the last token of a sequence, end: its first
+};
+
+template <typename IO, typename GT, int kWrite, Copy kCopy, bool kSeqs>
+__global__ void __launch_bounds__(kScanThreads, 2)
 scan_bwd_kernel(const BwdParams<IO, GT> p, const int cluster) {
-    __shared__ ScanShared<VEC> sh;
+    extern __shared__ __align__(128) char stages[];
+    __shared__ ScanShared sh;
+    using St = Stage<IO, GT, kWrite>;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int rank = blockIdx.x % cluster;
     const int unit = blockIdx.x / cluster;
     const int slab = unit % p.slabs, row = unit / p.slabs;
-    const int c = (slab * 32 + lane) * VEC;
-    const bool on = c < p.D;
-    const int L = p.L;
-    const size_t row0 = (size_t)row * L;
+    const int left = p.D - slab * kSlab;
+    const int c = slab * kSlab + 2 * lane, mine = left - 2 * lane;
+    const int L = p.L, D = p.D;
+    // the adjoint's order: the forward's, backwards
+    const int origin = p.reverse ? 0 : L - 1, dir = p.reverse ? 1 : -1;
 
     if (kSeqs && blockIdx.x == 0) check_cu(p.q, p.status, tid, kScanThreads);
-    if (kSeqs && rank == 0 && p.dh0 && on) {  // the state passes an empty sequence unchanged
+    if (kSeqs && rank == 0 && p.dh0) {  // the state's gradient passes an empty sequence unchanged
         for (int s = wid; s < p.q.n; s += kScanWarps) {
             if (p.q.begin(s) != p.q.end(s)) continue;
-            float x[VEC] = {};
-            if (p.dh_final) load_f<float, VEC>(p.dh_final + (size_t)s * p.D + c, x);
-            store_vec<float, VEC>(p.dh0 + (size_t)s * p.D + c, x);
+            float x[2] = {};
+            if (p.dh_final) load_state<kCopy>(p.dh_final + (size_t)s * D + c, x, mine);
+            store_pair<float, kCopy>(p.dh0 + (size_t)s * D + c, x, mine);
         }
     }
 
-    float carry[VEC] = {}, h0_row[VEC] = {};
-    if (!kSeqs && on) {
-        if (p.dh_final) load_f<float, VEC>(p.dh_final + (size_t)row * p.D + c, carry);
-        if (p.h0) load_f<float, VEC>(p.h0 + (size_t)row * p.D + c, h0_row);
-    }
-
-    Vec<IO, VEC> rv[kSeg], ro[kSeg], rd[kSeg];
-    Vec<GT, VEC> rg[kSeg], rb[kSeg];
-    // place i of the adjoint's order: the forward's, backwards
-    auto place = [&](int i) { return p.reverse ? i : L - 1 - i; };
-    auto fetch = [&](int first) {
-#pragma unroll
-        for (int i = 0; i < kSeg; ++i) {
-            if (!on || first + i >= L) continue;
-            const size_t at = (row0 + place(first + i)) * p.D + c;
-            rg[i] = load_vec<GT, VEC>(p.g + at);
-            rd[i] = load_vec<IO, VEC>(p.dO + at);
-            if constexpr (kWrite != GDR_WRITE_PLAIN) rv[i] = load_vec<IO, VEC>(p.v + at);
-            if constexpr (kWrite == GDR_WRITE_GATE) rb[i] = load_vec<GT, VEC>(p.beta + at);
-            if (first + i + 1 < L)  // h of the token before, in the forward's order
-                ro[i] = load_vec<IO, VEC>(p.o + (row0 + place(first + i + 1)) * p.D + c);
-        }
+    const size_t base = (size_t)row * L * D + slab * kSlab;
+    char* const buf = stages + wid * kStages * St::kBytes;
+    auto feed = [&](int first, int stage) {
+        char* s = buf + stage * St::kBytes;
+        feed_rows<GT, kCopy, kSeg>(s, p.g + base, origin, dir, first, L, D, left, lane);
+        feed_rows<IO, kCopy, kSeg>(s + St::dO, p.dO + base, origin, dir, first, L, D, left, lane);
+        feed_rows<IO, kCopy, kSeg>(s + St::o, p.o + base, origin, dir, first + 1, L, D, left, lane);
+        if constexpr (kWrite != GDR_WRITE_PLAIN)
+            feed_rows<IO, kCopy, kSeg>(s + St::v, p.v + base, origin, dir, first, L, D, left, lane);
+        if constexpr (kWrite == GDR_WRITE_GATE)
+            feed_rows<GT, kCopy, kSeg>(s + St::beta, p.beta + base, origin, dir, first, L, D, left,
+                                       lane);
+        copy_commit();
     };
 
     const int stride = cluster * kTile;
-    int first = rank * kTile + wid * kSeg;
-    int step = 0;
-    for (int base = 0; base < L; base += stride, first += stride, ++step) {
-        const int n = min(kSeg, L - first);
-        fetch(first);
-        Marks m{0u, 0u, 0};  // start: the forward's last token of a sequence, end: its first
-        if constexpr (kSeqs)
-            m = find_marks<kSeg>(p.q, [&](int i) { return place(first + i); }, n, !p.reverse, lane);
-        float a[kSeg][VEC], d[kSeg][VEC];
+    const int steps = (int)(((long long)L + stride - 1) / stride);
+    const int first0 = rank * kTile + wid * kSeg;
+    auto place = [&](int k) {
+        const long long f = first0 + (long long)k * stride;
+        return (int)(f < L ? f : L);
+    };
+    // a tile's stage is read until the tile is finished, a step after it was formed
+#pragma unroll
+    for (int k = 0; k < kStages - 2; ++k) feed(place(k), k);
+
+    Here here{0, 0};
+    auto form = [&](int k, Elements& e) {
+        copy_wait<kStages - 3>();
+        __syncwarp();
+        feed(place(k + kStages - 2), (k + kStages - 2) % kStages);
+        const char* s = buf + (k % kStages) * St::kBytes;
+        if constexpr (kSeqs) {
+            const int first = place(k);
+            e.m = find_marks(p.q, here, origin, dir, first, min(kSeg, L - first), lane);
+        }
 #pragma unroll
         for (int i = 0; i < kSeg; ++i) {
-            const bool in = i < n && on;
+            float g[2];
+            Rows<GT, kSeg>::read(s, i, lane, g);
+            Rows<IO, kSeg>::read(s + St::dO, i, lane, e.d[i]);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                a[i][j] = in ? expf(to_f(rg[i].x[j])) : 1.f;
-                d[i][j] = in ? to_f(rd[i].x[j]) : 0.f;
-            }
-            if (kSeqs && (m.start >> i & 1u) && p.dh_final) {
-                const int s = __shfl_sync(0xffffffffu, m.seq, i);
-                float x[VEC] = {};
-                if (on) load_f<float, VEC>(p.dh_final + (size_t)s * p.D + c, x);
+            for (int j = 0; j < 2; ++j) e.a[i][j] = expf(g[j]);
+            if (kSeqs && (e.m.start >> i & 1u) && p.dh_final) {
+                const int q = __shfl_sync(0xffffffffu, e.m.seq, i);
+                float x[2];
+                load_state<kCopy>(p.dh_final + (size_t)q * D + c, x, mine);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) d[i][j] += x[j];
+                for (int j = 0; j < 2; ++j) e.d[i][j] += x[j];
             }
         }
-        Run<VEC> run;
+        Run run;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
+        for (int j = 0; j < 2; ++j) {
             float A = 1.f, H = 0.f;
 #pragma unroll
             for (int i = 0; i < kSeg; ++i) {
-                H = a[i][j] * (kSeqs && (m.start >> i & 1u) ? d[i][j] : d[i][j] + H);
-                A *= a[i][j];
+                H = e.a[i][j] * (kSeqs && (e.m.start >> i & 1u) ? e.d[i][j] : e.d[i][j] + H);
+                A *= e.a[i][j];
             }
-            run.A[j] = kSeqs && m.start ? kReset : A;
+            run.A[j] = kSeqs && e.m.start ? kReset : A;
             run.H[j] = H;
         }
-        float mu[VEC];
-        join_runs(sh, run, step, cluster, rank, wid, lane, carry, mu);
-#pragma unroll
-        for (int i = 0; i < kSeg; ++i) {
-            const bool ends = kSeqs ? (m.end >> i & 1u) : first + i == L - 1;
-            const int s = kSeqs ? __shfl_sync(0xffffffffu, m.seq, i) : row;
-            float lam[VEC], hp[VEC] = {}, out[VEC];
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                lam[j] = kSeqs && (m.start >> i & 1u) ? d[i][j] : d[i][j] + mu[j];
-                mu[j] = a[i][j] * lam[j];
-            }
-            if (i >= n || !on) continue;
-            const size_t at = (row0 + place(first + i)) * p.D + c;
-            if (!ends) {
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) hp[j] = to_f(ro[i].x[j]);
-            } else if (!kSeqs) {
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) hp[j] = h0_row[j];
-            } else if (p.h0) {
-                load_f<float, VEC>(p.h0 + (size_t)s * p.D + c, hp);
-            }
-            if (ends && p.dh0) store_vec<float, VEC>(p.dh0 + (size_t)s * p.D + c, mu);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j)
-                out[j] = mu[j] * (kWrite == GDR_WRITE_TIED ? hp[j] - to_f(rv[i].x[j]) : hp[j]);
-            store_vec<GT, VEC>(p.dg + at, out);
-            if constexpr (kWrite == GDR_WRITE_GATE) {
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) out[j] = lam[j] * to_f(rv[i].x[j]);
-                store_vec<GT, VEC>(p.dbeta + at, out);
-            }
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                if constexpr (kWrite == GDR_WRITE_GATE) out[j] = lam[j] * to_f(rb[i].x[j]);
-                else if constexpr (kWrite == GDR_WRITE_TIED) out[j] = -expm1f(to_f(rg[i].x[j])) * lam[j];
-                else out[j] = lam[j];
-            }
-            store_vec<IO, VEC>(p.dv + at, out);
-        }
+        sh.warp[k & 1][wid][lane] = run;
+    };
+
+    float carry[2] = {}, h0_row[2] = {};
+    if (!kSeqs) {
+        if (p.dh_final) load_state<kCopy>(p.dh_final + (size_t)row * D + c, carry, mine);
+        if (p.h0) load_state<kCopy>(p.h0 + (size_t)row * D + c, h0_row, mine);
     }
+
+    auto cl = cooperative_groups::this_cluster();
+    Run whole;
+    auto publish = [&](int k, Elements& e) {
+        join_block<kSeqs>(sh.warp[k & 1], wid, lane, e.before, whole);
+        if (cluster > 1) {
+            if (wid < cluster) *cl.map_shared_rank(&sh.block[k & 3][rank][lane], wid) = whole;
+            cl.barrier_arrive();
+        }
+    };
+    auto finish = [&](int k, const Elements& e, const Run& tile) {
+        float mu[2];
+        if (cluster == 1) {
+            mu[0] = carry[0];
+            mu[1] = carry[1];
+            run_apply<kSeqs>(tile, carry);
+        } else {
+            for (int r = 0; r < cluster; ++r) {
+                if (r == rank) { mu[0] = carry[0]; mu[1] = carry[1]; }
+                run_apply<kSeqs>(sh.block[k & 3][r][lane], carry);
+            }
+        }
+        run_apply<kSeqs>(e.before, mu);
+        const char* s = buf + (k % kStages) * St::kBytes;
+        const int first = place(k), n = min(kSeg, L - first);
+        const long long next = (long long)dir * D;
+        long long at = (long long)base + (long long)(origin + dir * first) * D + 2 * lane;
+#pragma unroll
+        for (int i = 0; i < kSeg; ++i, at += next) {
+            const bool ends = kSeqs ? (e.m.end >> i & 1u) : first + i == L - 1;
+            const int q = !kSeqs ? row : ends ? __shfl_sync(0xffffffffu, e.m.seq, i) : 0;
+            float lam[2], hp[2], out[2], v[2], w[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                lam[j] = kSeqs && (e.m.start >> i & 1u) ? e.d[i][j] : e.d[i][j] + mu[j];
+                mu[j] = e.a[i][j] * lam[j];
+            }
+            if (i >= n) continue;
+            Rows<IO, kSeg>::read(s + St::o, i, lane, hp);
+            if (ends) {
+                hp[0] = h0_row[0];
+                hp[1] = h0_row[1];
+                if (kSeqs && p.h0) load_state<kCopy>(p.h0 + (size_t)q * D + c, hp, mine);
+                if (p.dh0) store_pair<float, kCopy>(p.dh0 + (size_t)q * D + c, mu, mine);
+            }
+            if constexpr (kWrite != GDR_WRITE_PLAIN) Rows<IO, kSeg>::read(s + St::v, i, lane, v);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                out[j] = mu[j] * (kWrite == GDR_WRITE_TIED ? hp[j] - v[j] : hp[j]);
+            store_pair<GT, kCopy>(p.dg + at, out, mine);
+            if constexpr (kWrite == GDR_WRITE_GATE) {
+                Rows<GT, kSeg>::read(s + St::beta, i, lane, w);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) out[j] = lam[j] * v[j];
+                store_pair<GT, kCopy>(p.dbeta + at, out, mine);
+            } else if constexpr (kWrite == GDR_WRITE_TIED) {
+                Rows<GT, kSeg>::read(s, i, lane, w);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) w[j] = -expm1f(w[j]);
+            } else {
+                w[0] = w[1] = 1.f;
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) out[j] = kWrite == GDR_WRITE_PLAIN ? lam[j] : w[j] * lam[j];
+            store_pair<IO, kCopy>(p.dv + at, out, mine);
+        }
+    };
+
+    // the forward's walk (scan.cu)
+    auto turn = [&](int k, Elements& now, Elements& next) {
+        const Run tile = whole;
+        if (k + 1 < steps) {
+            form(k + 1, next);
+            __syncthreads();
+        }
+        if (cluster > 1) cl.barrier_wait();
+        if (k + 1 < steps) publish(k + 1, next);
+        finish(k, now, tile);
+    };
+    Elements even, odd;
+    form(0, even);
+    __syncthreads();
+    publish(0, even);
+    for (int k = 0; k < steps; k += 2) {
+        turn(k, even, odd);
+        if (k + 1 < steps) turn(k + 1, odd, even);
+    }
+    copy_wait<0>();
 }
 
-template <typename IO, typename GT, int kWrite, int VEC>
+template <typename IO, typename GT, int kWrite, Copy kCopy>
 gdr_status bwd_launch(const gdr_scan_args& a, const ScanPtrs& x, cudaStream_t st) {
     const bool seqs = scan_one_row(a, x.cu);
     BwdParams<IO, GT> p;
@@ -174,18 +248,23 @@ gdr_status bwd_launch(const gdr_scan_args& a, const ScanPtrs& x, cudaStream_t st
     p.q = Seqs{x.cu, a.n_seqs, a.T, a.B * a.T};
     p.D = a.D;
     p.L = seqs ? a.B * a.T : a.T;
-    p.slabs = (a.D + 32 * VEC - 1) / (32 * VEC);
+    p.slabs = (a.D + kSlab - 1) / kSlab;
     p.reverse = a.reverse;
     const long long units = (long long)p.slabs * (seqs ? 1 : a.B);
-    return seqs ? scan_launch(scan_bwd_kernel<IO, GT, kWrite, VEC, true>, p, units, p.L, kTile, st)
-                : scan_launch(scan_bwd_kernel<IO, GT, kWrite, VEC, false>, p, units, p.L, kTile, st);
+    const size_t smem = (size_t)kScanWarps * kStages * Stage<IO, GT, kWrite>::kBytes;
+    return seqs ? scan_launch(scan_bwd_kernel<IO, GT, kWrite, kCopy, true>, p, units, p.L, kTile, smem, st)
+                : scan_launch(scan_bwd_kernel<IO, GT, kWrite, kCopy, false>, p, units, p.L, kTile, smem, st);
 }
 
 struct Bwd {
     template <typename IO, typename GT, int kWrite>
     static gdr_status go(const gdr_scan_args& a, const ScanPtrs& x, cudaStream_t st) {
-        return a.D % 2 ? bwd_launch<IO, GT, kWrite, 1>(a, x, st)
-                       : bwd_launch<IO, GT, kWrite, 2>(a, x, st);
+        const Copy copy = scan_copy(a);
+        if (copy == kCopy16) return bwd_launch<IO, GT, kWrite, kCopy16>(a, x, st);
+        if constexpr (sizeof(IO) == sizeof(GT)) {
+            if (copy == kCopyPair) return bwd_launch<IO, GT, kWrite, kCopyPair>(a, x, st);
+        }
+        return bwd_launch<IO, GT, kWrite, kCopyOne>(a, x, st);
     }
 };
 
