@@ -27,28 +27,14 @@ struct FwdParams {
     int D, L, slabs, reverse;  // L: tokens of a row
 };
 
-// alpha and b of one element
-template <int kWrite>
-__device__ __forceinline__ void decay_write(float g, float v, float beta, float& a, float& b) {
-    if constexpr (kWrite == GDR_WRITE_TIED) {
-        const float em = expm1f(g);  // 1 - alpha without cancellation
-        a = 1.f + em;
-        b = -em * v;
-    } else {
-        a = expf(g);
-        b = kWrite == GDR_WRITE_GATE ? beta * v : v;
-    }
-}
-
 template <typename IO, typename GT, int kWrite>
 constexpr int stage_bytes = Rows<IO, seg_of<IO, GT>>::kBytes +
                             (kWrite == GDR_WRITE_GATE ? 2 : 1) * Rows<GT, seg_of<IO, GT>>::kBytes;
 
-// One tile's elements of a lane, from the forming of its run to the output.
+// A lane's elements of a tile, from the forming of its run to the output.
 template <int kSeg>
 struct Elements {
-    float a[kSeg][2], b[kSeg][2];
-    Run before;  // the block's runs before the warp's
+    F2 a[kSeg], b[kSeg];
     Marks m;
 };
 
@@ -71,164 +57,109 @@ scan_fwd_kernel(const FwdParams<IO, GT> p, const int cluster) {
     const int L = p.L, D = p.D;
     const int origin = p.reverse ? L - 1 : 0, dir = p.reverse ? -1 : 1;
 
+    scan_open(sh, cluster);
     if (kSeqs && blockIdx.x == 0) check_cu(p.q, p.status, tid, kScanThreads);
     if (kSeqs && rank == 0 && p.h_final) {  // empty sequences keep their state
         for (int s = wid; s < p.q.n; s += kScanWarps) {
             if (p.q.begin(s) != p.q.end(s)) continue;
-            float x[2] = {};
-            if (p.h0) load_state<kCopy>(p.h0 + (size_t)s * D + c, x, mine);
+            F2 x = f2(0.f);
+            if (p.h0) x = load_state<kCopy>(p.h0 + (size_t)s * D + c, mine);
             store_pair<float, kCopy>(p.h_final + (size_t)s * D + c, x, mine);
         }
     }
 
     const size_t base = (size_t)row * L * D + slab * kSlab;
-    char* const buf = stages + wid * kStages * kStage;
-    auto feed = [&](int first, int stage) {
-        char* s = buf + stage * kStage;
-        feed_rows<IO, kCopy, kSeg>(s, p.v + base, origin, dir, first, L, D, left, lane);
-        s += RowsIO::kBytes;
-        feed_rows<GT, kCopy, kSeg>(s, p.g + base, origin, dir, first, L, D, left, lane);
-        if constexpr (kWrite == GDR_WRITE_GATE)
-            feed_rows<GT, kCopy, kSeg>(s + RowsGT::kBytes, p.beta + base, origin, dir, first, L, D, left,
-                                 lane);
-    };
-
-    const int stride = cluster * kTile;
+    const int stride = cluster * kTile, first0 = rank * kTile + wid * kSeg;
     const int steps = (int)(((long long)L + stride - 1) / stride);
-    const int first0 = rank * kTile + wid * kSeg;
-    // places behind L may pass 2^31: a tile that starts there is empty
-    auto place = [&](int k) {
-        const long long f = first0 + (long long)k * stride;
-        return (int)(f < L ? f : L);
+    const long long hop = (long long)dir * stride * D;  // elements from a tile to the next
+    char* const buf = stages + wid * kStages * kStage;
+    Feed<IO, kCopy, kSeg> fv;
+    Feed<GT, kCopy, kSeg> fg, fb;
+    fv.open(p.v + base, origin, dir, first0, D, left, lane);
+    fg.open(p.g + base, origin, dir, first0, D, left, lane);
+    if constexpr (kWrite == GDR_WRITE_GATE) fb.open(p.beta + base, origin, dir, first0, D, left, lane);
+    // The tiles walk on past L by at most kStages steps: L is bounded so that no place overflows.
+    auto feed = [&](int k, int stage) {
+        char* s = buf + stage * kStage;
+        const int place = k < steps ? first0 + k * stride : L;
+        fv.tile(s, place, L, hop);
+        fg.tile(s + RowsIO::kBytes, place, L, hop);
+        if constexpr (kWrite == GDR_WRITE_GATE)
+            fb.tile(s + RowsIO::kBytes + RowsGT::kBytes, place, L, hop);
+        copy_commit();
     };
 #pragma unroll
-    for (int k = 0; k < kStages - 1; ++k) {
-        feed(place(k), k);
-        copy_commit();
-    }
+    for (int k = 0; k < kStages - 1; ++k) feed(k, k);
 
+    F2 carry = f2(0.f);
+    if (!kSeqs && p.h0) carry = load_state<kCopy>(p.h0 + (size_t)row * D + c, mine);
     Here here{0, 0};
     int stage = 0;  // of the next tile to be formed
-    // Forms the run of tile k and hands it to the block.
     auto form = [&](int k, Elements<kSeg>& e) {
         copy_wait<kStages - 2>();
         __syncwarp();
-        // the stage of the tile before: every lane has read it
-        feed(place(k + kStages - 1), stage == 0 ? kStages - 1 : stage - 1);
-        copy_commit();
+        // into the stage of the tile before: every lane has read it
+        feed(k + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
         const char* s = buf + stage * kStage;
         stage = stage == kStages - 1 ? 0 : stage + 1;
 #pragma unroll
         for (int i = 0; i < kSeg; ++i) {
-            float v[2], g[2], w[2] = {};
-            RowsIO::read(s, i, lane, v);
-            RowsGT::read(s + RowsIO::kBytes, i, lane, g);
+            const F2 v = RowsIO::read(s, i, lane), g = RowsGT::read(s + RowsIO::kBytes, i, lane);
+            e.a[i] = exp2ch(g);
             if constexpr (kWrite == GDR_WRITE_GATE)
-                RowsGT::read(s + RowsIO::kBytes + RowsGT::kBytes, i, lane, w);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) decay_write<kWrite>(g[j], v[j], w[j], e.a[i][j], e.b[i][j]);
+                e.b[i] = mul2(RowsGT::read(s + RowsIO::kBytes + RowsGT::kBytes, i, lane), v);
+            else if constexpr (kWrite == GDR_WRITE_TIED)
+                e.b[i] = mul2(one_minus(g, e.a[i]), v);
+            else
+                e.b[i] = v;
         }
         if constexpr (kSeqs) {
-            const int first = place(k);
+            const int first = first0 + k * stride;
             e.m = find_marks(p.q, here, origin, dir, first, min(kSeg, L - first), lane);
             if (e.m.start && p.h0) {  // b at a start takes the initial state in
 #pragma unroll
                 for (int i = 0; i < kSeg; ++i) {
                     if (!(e.m.start >> i & 1u)) continue;
                     const int q = __shfl_sync(0xffffffffu, e.m.seq, i);
-                    float x[2];
-                    load_state<kCopy>(p.h0 + (size_t)q * D + c, x, mine);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) e.b[i][j] = fmaf(e.a[i][j], x[j], e.b[i][j]);
+                    e.b[i] = fma2(e.a[i], load_state<kCopy>(p.h0 + (size_t)q * D + c, mine), e.b[i]);
                 }
             }
         }
-        Run run;
+        Run run{e.a[0], e.b[0]};
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            float A = e.a[0][j], H = e.b[0][j];
-#pragma unroll
-            for (int i = 1; i < kSeg; ++i) {
-                const float y = fmaf(e.a[i][j], H, e.b[i][j]);
-                H = kSeqs && (e.m.start >> i & 1u) ? e.b[i][j] : y;
-                A *= e.a[i][j];
-            }
-            run.A[j] = kSeqs && e.m.start ? kReset : A;
-            run.H[j] = H;
+        for (int i = 1; i < kSeg; ++i) {
+            const F2 y = fma2(e.a[i], run.H, e.b[i]);
+            run.H = kSeqs ? pick2(e.m.start >> i & 1u, e.b[i], y) : y;
+            run.A = mul2(run.A, e.a[i]);
         }
-        sh.warp[k & 1][wid][lane] = run;
+        if (kSeqs && e.m.start) run.A = f2(kReset);
+        sh.warp[k & 3][wid][lane] = run;
     };
 
-    float carry[2] = {};
-    if (!kSeqs && p.h0) load_state<kCopy>(p.h0 + (size_t)row * D + c, carry, mine);
-
-    auto cl = cooperative_groups::this_cluster();
-    Run whole;   // the block's tile, where the cluster is the block
-    // Joins the block's runs of tile k and, in a cluster, hands the result to every block.
-    auto publish = [&](int k, Elements<kSeg>& e) {
-        join_block<kSeqs>(sh.warp[k & 1], wid, lane, e.before, whole);
-        if (cluster > 1) {
-            if (wid < cluster) *cl.map_shared_rank(&sh.block[k & 3][rank][lane], wid) = whole;
-            cl.barrier_arrive();
-        }
-    };
-    // Finishes tile k: its states from the carry, which becomes the state behind the step.
-    auto finish = [&](int k, const Elements<kSeg>& e, const Run& tile) {
-        float h[2];
-        if (cluster == 1) {
-            h[0] = carry[0];
-            h[1] = carry[1];
-            run_apply<kSeqs>(tile, carry);
-        } else {
-            for (int r = 0; r < cluster; ++r) {
-                if (r == rank) { h[0] = carry[0]; h[1] = carry[1]; }
-                run_apply<kSeqs>(sh.block[k & 3][r][lane], carry);
-            }
-        }
-        run_apply<kSeqs>(e.before, h);
-        const int first = place(k), n = min(kSeg, L - first);
-        IO* out = p.o + base + (long long)(origin + dir * first) * D + 2 * lane;
-        const long long next = (long long)dir * D;
+    const long long next = (long long)dir * D;
+    IO* out = p.o + base + (origin + (long long)dir * first0) * D + 2 * lane;
+    auto finish = [&](int k, const Elements<kSeg>& e, F2 h) {
+        const int n = L - (first0 + k * stride);
+        IO* q = out;
+        out += hop;
 #pragma unroll
         for (int i = 0; i < kSeg; ++i) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float y = fmaf(e.a[i][j], h[j], e.b[i][j]);
-                h[j] = kSeqs && (e.m.start >> i & 1u) ? e.b[i][j] : y;
-            }
-            if (i < n) store_pair<IO, kCopy>(out, h, mine);
-            out += next;
+            const F2 y = fma2(e.a[i], h, e.b[i]);
+            h = kSeqs ? pick2(e.m.start >> i & 1u, e.b[i], y) : y;
+            if (i < n) store_pair<IO, kCopy>(q, h, mine);
+            q += next;
             if (kSeqs && (e.m.end >> i & 1u) && p.h_final) {
-                const int q = __shfl_sync(0xffffffffu, e.m.seq, i);
-                store_pair<float, kCopy>(p.h_final + (size_t)q * D + c, h, mine);
+                const int s = __shfl_sync(0xffffffffu, e.m.seq, i);
+                store_pair<float, kCopy>(p.h_final + (size_t)s * D + c, h, mine);
             }
         }
     };
-
-    // One step of the walk: tile k + 1's run goes out before tile k is finished.  The block
-    // barrier between form and publish also keeps the parities apart: a run is written again two
-    // tiles later, behind a barrier that every reader of the first has passed.
-    auto turn = [&](int k, Elements<kSeg>& now, Elements<kSeg>& next) {
-        const Run tile = whole;
-        if (k + 1 < steps) {
-            form(k + 1, next);
-            __syncthreads();
-        }
-        if (cluster > 1) cl.barrier_wait();
-        if (k + 1 < steps) publish(k + 1, next);
-        finish(k, now, tile);
-    };
-    Elements<kSeg> even, odd;
-    form(0, even);
-    __syncthreads();
-    publish(0, even);
-    for (int k = 0; k < steps; k += 2) {
-        turn(k, even, odd);
-        if (k + 1 < steps) turn(k + 1, odd, even);
-    }
-    copy_wait<0>();
+    const bool ok = scan_walk<kSeqs, Elements<kSeg>>(sh, steps, cluster, rank, wid, lane, carry, form,
+                                                     finish);
+    if (!ok && p.status) atomicCAS(p.status, (int)GDR_OK, (int)GDR_ERR_TIMEOUT);
     if (!kSeqs && p.h_final && rank == 0 && wid == 0)
         store_pair<float, kCopy>(p.h_final + (size_t)row * D + c, carry, mine);
+    scan_close(cluster);
 }
 
 template <typename IO, typename GT, int kWrite, Copy kCopy>
@@ -281,9 +212,11 @@ scan_step_kernel(const IO* __restrict__ v, const GT* __restrict__ g, const GT* _
     if constexpr (kWrite == GDR_WRITE_GATE) load_f<GT, VEC>(beta + at, fb);
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
-        float a, b;
-        decay_write<kWrite>(fg[j], fv[j], fb[j], a, b);
-        fh[j] = fmaf(a, fh[j], b);
+        const F2 g2 = f2(fg[j]), a = exp2ch(g2);
+        float b = fv[j];
+        if constexpr (kWrite == GDR_WRITE_GATE) b *= fb[j];
+        if constexpr (kWrite == GDR_WRITE_TIED) b *= one_minus(g2, a).lo();
+        fh[j] = fmaf(a.lo(), fh[j], b);
     }
     store_vec<float, VEC>(h_out + at, fh);
     store_vec<IO, VEC>(o + at, fh);

@@ -37,8 +37,7 @@ struct Stage {
 };
 
 struct Elements {
-    float a[kSeg][2], d[kSeg][2];  // alpha; dO, with dh_final at a sequence's last token
-    Run before;
+    F2 a[kSeg], d[kSeg];           // alpha; dO, with dh_final at a sequence's last token
     Marks m;                       // start: the last token of a sequence, end: its first
 };
 
@@ -58,175 +57,119 @@ scan_bwd_kernel(const BwdParams<IO, GT> p, const int cluster) {
     // the adjoint's order: the forward's, backwards
     const int origin = p.reverse ? 0 : L - 1, dir = p.reverse ? 1 : -1;
 
+    scan_open(sh, cluster);
     if (kSeqs && blockIdx.x == 0) check_cu(p.q, p.status, tid, kScanThreads);
     if (kSeqs && rank == 0 && p.dh0) {  // the state's gradient passes an empty sequence unchanged
         for (int s = wid; s < p.q.n; s += kScanWarps) {
             if (p.q.begin(s) != p.q.end(s)) continue;
-            float x[2] = {};
-            if (p.dh_final) load_state<kCopy>(p.dh_final + (size_t)s * D + c, x, mine);
+            F2 x = f2(0.f);
+            if (p.dh_final) x = load_state<kCopy>(p.dh_final + (size_t)s * D + c, mine);
             store_pair<float, kCopy>(p.dh0 + (size_t)s * D + c, x, mine);
         }
     }
 
     const size_t base = (size_t)row * L * D + slab * kSlab;
-    char* const buf = stages + wid * kStages * St::kBytes;
-    auto feed = [&](int first, int stage) {
-        char* s = buf + stage * St::kBytes;
-        feed_rows<GT, kCopy, kSeg>(s, p.g + base, origin, dir, first, L, D, left, lane);
-        feed_rows<IO, kCopy, kSeg>(s + St::dO, p.dO + base, origin, dir, first, L, D, left, lane);
-        feed_rows<IO, kCopy, kSeg>(s + St::o, p.o + base, origin, dir, first + 1, L, D, left, lane);
-        if constexpr (kWrite != GDR_WRITE_PLAIN)
-            feed_rows<IO, kCopy, kSeg>(s + St::v, p.v + base, origin, dir, first, L, D, left, lane);
-        if constexpr (kWrite == GDR_WRITE_GATE)
-            feed_rows<GT, kCopy, kSeg>(s + St::beta, p.beta + base, origin, dir, first, L, D, left,
-                                       lane);
-        copy_commit();
-    };
-
-    const int stride = cluster * kTile;
+    const int stride = cluster * kTile, first0 = rank * kTile + wid * kSeg;
     const int steps = (int)(((long long)L + stride - 1) / stride);
-    const int first0 = rank * kTile + wid * kSeg;
-    auto place = [&](int k) {
-        const long long f = first0 + (long long)k * stride;
-        return (int)(f < L ? f : L);
+    const long long hop = (long long)dir * stride * D;
+    char* const buf = stages + wid * kStages * St::kBytes;
+    Feed<GT, kCopy, kSeg> fg, fb;
+    Feed<IO, kCopy, kSeg> fd, fo, fv;
+    fg.open(p.g + base, origin, dir, first0, D, left, lane);
+    fd.open(p.dO + base, origin, dir, first0, D, left, lane);
+    fo.open(p.o + base, origin, dir, first0 + 1, D, left, lane);
+    if constexpr (kWrite != GDR_WRITE_PLAIN) fv.open(p.v + base, origin, dir, first0, D, left, lane);
+    if constexpr (kWrite == GDR_WRITE_GATE) fb.open(p.beta + base, origin, dir, first0, D, left, lane);
+    auto feed = [&](int k) {
+        char* s = buf + k % kStages * St::kBytes;
+        const int place = k < steps ? first0 + k * stride : L;
+        fg.tile(s, place, L, hop);
+        fd.tile(s + St::dO, place, L, hop);
+        fo.tile(s + St::o, place + 1, L, hop);
+        if constexpr (kWrite != GDR_WRITE_PLAIN) fv.tile(s + St::v, place, L, hop);
+        if constexpr (kWrite == GDR_WRITE_GATE) fb.tile(s + St::beta, place, L, hop);
+        copy_commit();
     };
     // a tile's stage is read until the tile is finished, a step after it was formed
 #pragma unroll
-    for (int k = 0; k < kStages - 2; ++k) feed(place(k), k);
+    for (int k = 0; k < kStages - 2; ++k) feed(k);
 
+    F2 carry = f2(0.f), h0_row = f2(0.f);
+    if (!kSeqs) {
+        if (p.dh_final) carry = load_state<kCopy>(p.dh_final + (size_t)row * D + c, mine);
+        if (p.h0) h0_row = load_state<kCopy>(p.h0 + (size_t)row * D + c, mine);
+    }
     Here here{0, 0};
     auto form = [&](int k, Elements& e) {
         copy_wait<kStages - 3>();
         __syncwarp();
-        feed(place(k + kStages - 2), (k + kStages - 2) % kStages);
-        const char* s = buf + (k % kStages) * St::kBytes;
+        feed(k + kStages - 2);
+        const char* s = buf + k % kStages * St::kBytes;
         if constexpr (kSeqs) {
-            const int first = place(k);
+            const int first = first0 + k * stride;
             e.m = find_marks(p.q, here, origin, dir, first, min(kSeg, L - first), lane);
         }
 #pragma unroll
         for (int i = 0; i < kSeg; ++i) {
-            float g[2];
-            Rows<GT, kSeg>::read(s, i, lane, g);
-            Rows<IO, kSeg>::read(s + St::dO, i, lane, e.d[i]);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) e.a[i][j] = expf(g[j]);
+            e.a[i] = exp2ch(Rows<GT, kSeg>::read(s, i, lane));
+            e.d[i] = Rows<IO, kSeg>::read(s + St::dO, i, lane);
             if (kSeqs && (e.m.start >> i & 1u) && p.dh_final) {
                 const int q = __shfl_sync(0xffffffffu, e.m.seq, i);
-                float x[2];
-                load_state<kCopy>(p.dh_final + (size_t)q * D + c, x, mine);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) e.d[i][j] += x[j];
+                e.d[i] = add2(e.d[i], load_state<kCopy>(p.dh_final + (size_t)q * D + c, mine));
             }
         }
-        Run run;
+        Run run{e.a[0], mul2(e.a[0], e.d[0])};
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            float A = 1.f, H = 0.f;
-#pragma unroll
-            for (int i = 0; i < kSeg; ++i) {
-                H = e.a[i][j] * (kSeqs && (e.m.start >> i & 1u) ? e.d[i][j] : e.d[i][j] + H);
-                A *= e.a[i][j];
-            }
-            run.A[j] = kSeqs && e.m.start ? kReset : A;
-            run.H[j] = H;
+        for (int i = 1; i < kSeg; ++i) {
+            const F2 y = add2(e.d[i], run.H);
+            run.H = mul2(e.a[i], kSeqs ? pick2(e.m.start >> i & 1u, e.d[i], y) : y);
+            run.A = mul2(run.A, e.a[i]);
         }
-        sh.warp[k & 1][wid][lane] = run;
+        if (kSeqs && e.m.start) run.A = f2(kReset);
+        sh.warp[k & 3][wid][lane] = run;
     };
 
-    float carry[2] = {}, h0_row[2] = {};
-    if (!kSeqs) {
-        if (p.dh_final) load_state<kCopy>(p.dh_final + (size_t)row * D + c, carry, mine);
-        if (p.h0) load_state<kCopy>(p.h0 + (size_t)row * D + c, h0_row, mine);
-    }
-
-    auto cl = cooperative_groups::this_cluster();
-    Run whole;
-    auto publish = [&](int k, Elements& e) {
-        join_block<kSeqs>(sh.warp[k & 1], wid, lane, e.before, whole);
-        if (cluster > 1) {
-            if (wid < cluster) *cl.map_shared_rank(&sh.block[k & 3][rank][lane], wid) = whole;
-            cl.barrier_arrive();
-        }
-    };
-    auto finish = [&](int k, const Elements& e, const Run& tile) {
-        float mu[2];
-        if (cluster == 1) {
-            mu[0] = carry[0];
-            mu[1] = carry[1];
-            run_apply<kSeqs>(tile, carry);
-        } else {
-            for (int r = 0; r < cluster; ++r) {
-                if (r == rank) { mu[0] = carry[0]; mu[1] = carry[1]; }
-                run_apply<kSeqs>(sh.block[k & 3][r][lane], carry);
-            }
-        }
-        run_apply<kSeqs>(e.before, mu);
-        const char* s = buf + (k % kStages) * St::kBytes;
-        const int first = place(k), n = min(kSeg, L - first);
-        const long long next = (long long)dir * D;
-        long long at = (long long)base + (long long)(origin + dir * first) * D + 2 * lane;
+    const long long next = (long long)dir * D;
+    long long out = (long long)base + (origin + (long long)dir * first0) * D + 2 * lane;
+    auto finish = [&](int k, const Elements& e, F2 mu) {
+        const char* s = buf + k % kStages * St::kBytes;
+        const int first = first0 + k * stride, n = L - first;
+        long long at = out;
+        out += hop;
 #pragma unroll
         for (int i = 0; i < kSeg; ++i, at += next) {
             const bool ends = kSeqs ? (e.m.end >> i & 1u) : first + i == L - 1;
             const int q = !kSeqs ? row : ends ? __shfl_sync(0xffffffffu, e.m.seq, i) : 0;
-            float lam[2], hp[2], out[2], v[2], w[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                lam[j] = kSeqs && (e.m.start >> i & 1u) ? e.d[i][j] : e.d[i][j] + mu[j];
-                mu[j] = e.a[i][j] * lam[j];
-            }
+            const F2 sum = add2(e.d[i], mu);
+            const F2 lam = kSeqs ? pick2(e.m.start >> i & 1u, e.d[i], sum) : sum;
+            mu = mul2(e.a[i], lam);
             if (i >= n) continue;
-            Rows<IO, kSeg>::read(s + St::o, i, lane, hp);
+            F2 hp = Rows<IO, kSeg>::read(s + St::o, i, lane);
             if (ends) {
-                hp[0] = h0_row[0];
-                hp[1] = h0_row[1];
-                if (kSeqs && p.h0) load_state<kCopy>(p.h0 + (size_t)q * D + c, hp, mine);
+                hp = h0_row;
+                if (kSeqs && p.h0) hp = load_state<kCopy>(p.h0 + (size_t)q * D + c, mine);
                 if (p.dh0) store_pair<float, kCopy>(p.dh0 + (size_t)q * D + c, mu, mine);
             }
-            if constexpr (kWrite != GDR_WRITE_PLAIN) Rows<IO, kSeg>::read(s + St::v, i, lane, v);
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                out[j] = mu[j] * (kWrite == GDR_WRITE_TIED ? hp[j] - v[j] : hp[j]);
-            store_pair<GT, kCopy>(p.dg + at, out, mine);
-            if constexpr (kWrite == GDR_WRITE_GATE) {
-                Rows<GT, kSeg>::read(s + St::beta, i, lane, w);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) out[j] = lam[j] * v[j];
-                store_pair<GT, kCopy>(p.dbeta + at, out, mine);
-            } else if constexpr (kWrite == GDR_WRITE_TIED) {
-                Rows<GT, kSeg>::read(s, i, lane, w);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) w[j] = -expm1f(w[j]);
+            if constexpr (kWrite == GDR_WRITE_PLAIN) {
+                store_pair<IO, kCopy>(p.dv + at, lam, mine);
             } else {
-                w[0] = w[1] = 1.f;
+                const F2 v = Rows<IO, kSeg>::read(s + St::v, i, lane);
+                if constexpr (kWrite == GDR_WRITE_GATE) {
+                    store_pair<GT, kCopy>(p.dbeta + at, mul2(lam, v), mine);
+                    store_pair<IO, kCopy>(
+                        p.dv + at, mul2(lam, Rows<GT, kSeg>::read(s + St::beta, i, lane)), mine);
+                } else {
+                    hp = add2(hp, f2(-v.lo(), -v.hi()));
+                    const F2 w = one_minus(Rows<GT, kSeg>::read(s, i, lane), e.a[i]);
+                    store_pair<IO, kCopy>(p.dv + at, mul2(w, lam), mine);
+                }
             }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) out[j] = kWrite == GDR_WRITE_PLAIN ? lam[j] : w[j] * lam[j];
-            store_pair<IO, kCopy>(p.dv + at, out, mine);
+            store_pair<GT, kCopy>(p.dg + at, mul2(mu, hp), mine);
         }
     };
-
-    // the forward's walk (scan.cu)
-    auto turn = [&](int k, Elements& now, Elements& next) {
-        const Run tile = whole;
-        if (k + 1 < steps) {
-            form(k + 1, next);
-            __syncthreads();
-        }
-        if (cluster > 1) cl.barrier_wait();
-        if (k + 1 < steps) publish(k + 1, next);
-        finish(k, now, tile);
-    };
-    Elements even, odd;
-    form(0, even);
-    __syncthreads();
-    publish(0, even);
-    for (int k = 0; k < steps; k += 2) {
-        turn(k, even, odd);
-        if (k + 1 < steps) turn(k + 1, odd, even);
-    }
-    copy_wait<0>();
+    const bool ok = scan_walk<kSeqs, Elements>(sh, steps, cluster, rank, wid, lane, carry, form, finish);
+    if (!ok && p.status) atomicCAS(p.status, (int)GDR_OK, (int)GDR_ERR_TIMEOUT);
+    scan_close(cluster);
 }
 
 template <typename IO, typename GT, int kWrite, Copy kCopy>

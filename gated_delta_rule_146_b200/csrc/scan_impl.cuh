@@ -20,64 +20,222 @@
 // do not pass, as they would through a product with zero.
 #pragma once
 
-#include <cooperative_groups.h>
-
 #include "layer.cuh"
+#include "tc_ptx.cuh"
 
 namespace gdr {
 
+using namespace tc;
+
 constexpr int kScanWarps = 8;
 constexpr int kScanThreads = 32 * kScanWarps;
-constexpr int kScanMaxCluster = 8;
+constexpr int kScanMaxCluster = 8;             // a warp hands the block's run to one block
 constexpr int kSlab = 64;                      // channels of a block
 constexpr float kReset = -1.f;
+constexpr uint64_t kScanWaitNs = 2000000000ull;
 
+// ---- a lane's two channels, in one 64-bit register pair -------------------------------------------
+struct F2 {
+    uint64_t v;
+    __device__ __forceinline__ float lo() const { return __uint_as_float((uint32_t)v); }
+    __device__ __forceinline__ float hi() const { return __uint_as_float((uint32_t)(v >> 32)); }
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ F2 f2(float x) { return f2(x, x); }
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 pick2(bool c, F2 a, F2 b) { return F2{c ? a.v : b.v}; }
+
+// max that lets NaN through
+__device__ __forceinline__ float max_nan(float x, float y) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+
+// e^g = 2^(g log2 e).  The product is rounded; what the rounding left out, e, and the low part of
+// log2 e multiply the result by 2^e = 1 + e ln 2 to first order (e is below 2^-17 in the range).
+// Below e^-150 the result is zero in either case, and the clamp keeps -inf out of the products.
+__device__ __forceinline__ F2 exp2ch(F2 g) {
+    const F2 x = f2(max_nan(g.lo(), -150.f), max_nan(g.hi(), -150.f));
+    const F2 t = mul2(x, f2(1.44269504f));
+    F2 e = fma2(x, f2(1.44269504f), f2(-t.lo(), -t.hi()));
+    e = fma2(x, f2(1.92596303e-8f), e);
+    const F2 m = f2(ex2(t.lo()), ex2(t.hi()));
+    return fma2(mul2(m, e), f2(0.693147181f), m);
+}
+
+// 1 - e^g given a = e^g: the series of e^g - 1 near zero (|g| < 1/2; the term left out is below
+// 2^-26 of the sum), the difference elsewhere.
+__device__ __forceinline__ F2 one_minus(F2 g, F2 a) {
+    F2 q = fma2(g, f2(1.f / 40320), f2(1.f / 5040));
+    q = fma2(q, g, f2(1.f / 720));
+    q = fma2(q, g, f2(1.f / 120));
+    q = fma2(q, g, f2(1.f / 24));
+    q = fma2(q, g, f2(1.f / 6));
+    q = fma2(q, g, f2(0.5f));
+    q = fma2(q, g, f2(1.f));
+    q = mul2(q, f2(-g.lo(), -g.hi()));
+    return f2(fabsf(g.lo()) < 0.5f ? q.lo() : 1.f - a.lo(), fabsf(g.hi()) < 0.5f ? q.hi() : 1.f - a.hi());
+}
+
+template <int kLeft> __device__ __forceinline__ void copy_wait();
+
+// ---- runs ----------------------------------------------------------------------------------------
 // The map of a run, for a lane's two channels.
 struct alignas(16) Run {
-    float A[2], H[2];
+    F2 A, H;
 };
 
+// x after the run
 template <bool kSeqs>
-__device__ __forceinline__ void run_apply(const Run& r, float (&x)[2]) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const float y = fmaf(r.A[j], x[j], r.H[j]);
-        x[j] = kSeqs && r.A[j] < 0.f ? r.H[j] : y;
-    }
+__device__ __forceinline__ F2 run_apply(const Run& r, F2 x) {
+    const F2 y = fma2(r.A, x, r.H);
+    return kSeqs ? pick2(r.A.lo() < 0.f, r.H, y) : y;
 }
 
-// f followed by r, into f
+// f followed by r
 template <bool kSeqs>
-__device__ __forceinline__ void run_join(Run& f, const Run& r) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const bool stop = kSeqs && r.A[j] < 0.f;
-        f.H[j] = stop ? r.H[j] : fmaf(r.A[j], f.H[j], r.H[j]);
-        f.A[j] = stop || (kSeqs && f.A[j] < 0.f) ? kReset : f.A[j] * r.A[j];
-    }
+__device__ __forceinline__ Run run_join(const Run& f, const Run& r) {
+    Run o;
+    o.H = run_apply<kSeqs>(r, f.H);
+    o.A = mul2(f.A, r.A);
+    if (kSeqs) o.A = pick2(r.A.lo() < 0.f || f.A.lo() < 0.f, f2(kReset), o.A);
+    return o;
 }
 
-__device__ __forceinline__ Run run_none() { return Run{{1.f, 1.f}, {0.f, 0.f}}; }
-
+// Runs handed over, by tile modulo four.  Between a tile's being written and its being read lies
+// a barrier, and a slot is written again only behind another one that every reader has passed.
+// The same holds between blocks: a block sends tile k + 1 once it has every block's tile k, and a
+// block sends that once all its warps have finished tile k - 2.
 struct ScanShared {
-    Run warp[2][kScanWarps][32];         // runs of the block's warps, by tile parity
-    // runs of the cluster's blocks, by tile modulo four.  A block writes tile k + 1 once every
-    // block has handed over tile k, which it does before it reads tile k - 1: the slot written
-    // is neither of these
+    Run warp[4][kScanWarps][32];
     Run block[4][kScanMaxCluster][32];
+    uint64_t full[4];   // bytes of block[] that have come
 };
 
-// Joins the block's runs of one tile (all written, behind a block barrier): the map of the
-// warps before this one, and that of the whole tile.
+// Joins the block's runs of tile k (written, behind a block barrier) and sends the result to
+// block `to` of the cluster.
 template <bool kSeqs>
-__device__ __forceinline__ void join_block(const Run (&warp)[kScanWarps][32], int wid, int lane,
-                                           Run& before, Run& all) {
-    all = run_none();
+__device__ __forceinline__ void send_run(ScanShared& sh, int k, int rank, int to, int lane) {
+    const Run(&r)[kScanWarps][32] = sh.warp[k & 3];
+    Run all = r[0][lane];
 #pragma unroll
-    for (int w = 0; w < kScanWarps; ++w) {
-        if (w == wid) before = all;
-        run_join<kSeqs>(all, warp[w][lane]);
+    for (int w = 1; w < kScanWarps; ++w) all = run_join<kSeqs>(all, r[w][lane]);
+    const uint32_t dst = cluster_map(smem_u32(&sh.block[k & 3][rank][lane]), to);
+    const uint32_t bar = cluster_map(smem_u32(&sh.full[k & 3]), to);
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];"
+                 ::"r"(dst), "f"(all.A.lo()), "f"(all.A.hi()), "f"(all.H.lo()), "f"(all.H.hi()), "r"(bar)
+                 : "memory");
+}
+
+// Waits, for two seconds at most, until every block's run of tile k is here.
+__device__ __forceinline__ bool runs_here(ScanShared& sh, int k) {
+    const uint32_t bar = smem_u32(&sh.full[k & 3]), parity = (uint32_t)(k >> 2) & 1u;
+    auto ready = [&](uint32_t ns) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok) : "r"(bar), "r"(parity), "r"(ns) : "memory");
+        return ok != 0;
+    };
+    if (ready(1000u)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (!ready(1000000u))
+        if (globaltimer_ns() - t0 > kScanWaitNs) return false;
+    return true;
+}
+
+// The state before the warp's run of tile k, from the carry before the step's first token, which
+// becomes the state behind its last.
+template <bool kSeqs>
+__device__ __forceinline__ F2 join_runs(const ScanShared& sh, int k, int cluster, int rank, int wid,
+                                        int lane, F2& carry) {
+    F2 x = carry;
+    if (cluster == 1) {
+#pragma unroll
+        for (int w = 0; w < kScanWarps; ++w) {
+            if (w == wid) x = carry;
+            carry = run_apply<kSeqs>(sh.warp[k & 3][w][lane], carry);
+        }
+        return x;
     }
+#pragma unroll
+    for (int r = 0; r < kScanMaxCluster; ++r) {
+        if (r == rank) x = carry;
+        if (r < cluster) carry = run_apply<kSeqs>(sh.block[k & 3][r][lane], carry);
+    }
+#pragma unroll
+    for (int w = 0; w < kScanWarps - 1; ++w)
+        if (w < wid) x = run_apply<kSeqs>(sh.warp[k & 3][w][lane], x);
+    return x;
+}
+
+// The walk over a row's tiles.  E holds a lane's elements of a tile; form(k, E) makes them and
+// writes the warp's run, finish(k, E, x) uses them with the state x before the run.  `dead`: a
+// wait ran out; the walk goes on without waiting, so that all threads meet at the barriers.
+template <bool kSeqs, typename E, typename Form, typename Finish>
+__device__ __forceinline__ bool scan_walk(ScanShared& sh, int steps, int cluster, int rank, int wid,
+                                          int lane, F2& carry, Form form, Finish finish) {
+    bool dead = false;
+    auto publish = [&](int k) {
+        if (cluster == 1) return;
+        if (threadIdx.x == 0) mbar_expect_tx(&sh.full[k & 3], (uint32_t)cluster * 32 * sizeof(Run));
+        if (wid < cluster) send_run<kSeqs>(sh, k, rank, wid, lane);
+    };
+    // tile k + 1's runs go out before tile k is finished
+    auto turn = [&](int k, E& now, E& next) {
+        if (k + 1 < steps) {
+            form(k + 1, next);
+            __syncthreads();
+        }
+        if (cluster > 1 && !dead) dead = !runs_here(sh, k);
+        if (k + 1 < steps) publish(k + 1);
+        finish(k, now, join_runs<kSeqs>(sh, k, cluster, rank, wid, lane, carry));
+    };
+    E even, odd;
+    form(0, even);
+    __syncthreads();
+    publish(0);
+    for (int k = 0; k < steps; k += 2) {
+        turn(k, even, odd);
+        if (k + 1 < steps) turn(k + 1, odd, even);
+    }
+    return !dead;
+}
+
+// The blocks of a cluster start together, their barriers ready, and end together, so that nothing
+// is sent to a block that is gone.
+__device__ __forceinline__ void scan_open(ScanShared& sh, int cluster) {
+    if (cluster == 1) return;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 4; ++i) mbar_init(&sh.full[i], 1);
+        mbar_init_fence();
+    }
+    cluster_sync_all();
+}
+__device__ __forceinline__ void scan_close(int cluster) {
+    copy_wait<0>();
+    if (cluster > 1) cluster_sync_all();
 }
 
 // ---- feeding -----------------------------------------------------------------------------------
@@ -105,91 +263,95 @@ __device__ __forceinline__ void copy_wait() {
 template <typename E, int kSeg>
 struct Rows {
     static constexpr int kBytes = kSeg * kSlab * (int)sizeof(E);
-    static __device__ __forceinline__ void read(const char* p, int i, int lane, float (&f)[2]) {
+    static __device__ __forceinline__ F2 read(const char* p, int i, int lane) {
         const char* q = p + i * kSlab * (int)sizeof(E) + lane * 2 * (int)sizeof(E);
         if constexpr (sizeof(E) == 2) {
             const uint32_t r = *reinterpret_cast<const uint32_t*>(q);
-            f[0] = __uint_as_float(r << 16);
-            f[1] = __uint_as_float(r & 0xffff0000u);
+            return f2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
         } else {
-            const float2 r = *reinterpret_cast<const float2*>(q);
-            f[0] = r.x;
-            f[1] = r.y;
+            return F2{*reinterpret_cast<const uint64_t*>(q)};
         }
     }
 };
 
-// Copies places [first, first + kSeg) of a row's order into p; places at or behind L are zero.
-// src: the slab's first channel of the row's first token; place 0 is token `origin`, and the
-// order goes up or (dir = -1) down the tokens.
+// Copies a warp's rows of one tensor, tile after tile.  Place 0 of a row's order is token
+// `origin`, and the order goes up or (dir = -1) down the tokens; places at or behind L are zero.
 template <typename E, Copy kCopy, int kSeg>
-__device__ __forceinline__ void feed_rows(char* p, const E* src, int origin, int dir, int first,
-                                          int L, int D, int left, int lane) {
-    if constexpr (kCopy == kCopy16) {
-        constexpr int kChunks = kSlab * (int)sizeof(E) / 16;  // of a row
-        constexpr int kRows = 32 / kChunks;                   // rows of one pass of the warp
-        constexpr int kEls = 16 / (int)sizeof(E);
-        const int row = lane / kChunks, col = (lane % kChunks) * kEls;
-        const E* at = src + (long long)(origin + dir * (first + row)) * D + col;
-        const long long next = (long long)dir * kRows * D;
-        uint32_t dst = (uint32_t)__cvta_generic_to_shared(p) + (uint32_t)lane * 16;
+struct Feed {
+    static constexpr int kEls = kCopy == kCopy16 ? 16 / (int)sizeof(E) : 2;
+    static constexpr int kPerRow = kSlab / kEls;              // lanes of a row
+    static constexpr int kRows = 32 / kPerRow;                // rows of one pass of the warp
+    static_assert(kSeg % kRows == 0, "a pass copies whole rows of a run");
+    const E* at;        // the lane's part of its first row of the next tile
+    long long pass;     // elements from a pass to the next
+    uint32_t dst;       // the lane's place in a stage
+    int row, left;
+
+    // src: the slab's first channel of the row's first token; `first`: the place of the warp's
+    // first row; left: channels of the slab
+    __device__ __forceinline__ void open(const E* src, int origin, int dir, long long first, int D,
+                                         int channels, int lane) {
+        row = lane / kPerRow;
+        const int col = lane % kPerRow * kEls;
+        left = channels - col;
+        at = src + (origin + dir * (first + row)) * D + col;
+        pass = (long long)dir * kRows * D;
+        dst = (uint32_t)(row * kSlab + col) * (uint32_t)sizeof(E);
+    }
+    // `place`: the tile's first row of this warp; hop: elements to the next tile
+    __device__ __forceinline__ void tile(char* stage, int place, int L, long long hop) {
+        const E* p = at;
+        at += hop;
+        if constexpr (kCopy == kCopyOne) {
+            E r[kSeg / kRows][2];
 #pragma unroll
-        for (int m = 0; m < kSeg / kRows; ++m) {
-            const bool in = col < left && first + row + m * kRows < L;
-            copy_async<16>(dst + m * 512, in ? at : src, in);
-            at += next;
-        }
-    } else if constexpr (kCopy == kCopyPair) {
-        const E* at = src + (long long)(origin + dir * first) * D + 2 * lane;
-        const long long next = (long long)dir * D;
-        uint32_t dst = (uint32_t)__cvta_generic_to_shared(p) + (uint32_t)(lane * 2 * sizeof(E));
+            for (int m = 0; m < kSeg / kRows; ++m) {
 #pragma unroll
-        for (int i = 0; i < kSeg; ++i) {
-            const bool in = 2 * lane < left && first + i < L;
-            copy_async<2 * (int)sizeof(E)>(dst + i * kSlab * (int)sizeof(E), in ? at : src, in);
-            at += next;
-        }
-    } else {
-        const E* at = src + (long long)(origin + dir * first) * D + 2 * lane;
-        const long long next = (long long)dir * D;
-        E r[kSeg][2];
+                for (int j = 0; j < 2; ++j)
+                    r[m][j] = j < left && place + row + m * kRows < L ? p[j] : from_f<E>(0.f);
+                p += pass;
+            }
+            E* q = reinterpret_cast<E*>(stage + dst);
 #pragma unroll
-        for (int i = 0; i < kSeg; ++i) {
+            for (int m = 0; m < kSeg / kRows; ++m) {
+                q[m * kRows * kSlab] = r[m][0];
+                q[m * kRows * kSlab + 1] = r[m][1];
+            }
+        } else {
+            const uint32_t q = smem_u32(stage) + dst;
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                r[i][j] = 2 * lane + j < left && first + i < L ? at[j] : from_f<E>(0.f);
-            at += next;
-        }
-        E* q = reinterpret_cast<E*>(p);
-#pragma unroll
-        for (int i = 0; i < kSeg; ++i) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) q[i * kSlab + 2 * lane + j] = r[i][j];
+            for (int m = 0; m < kSeg / kRows; ++m) {
+                copy_async<kEls * (int)sizeof(E)>(q + m * kRows * kSlab * (int)sizeof(E), p,
+                                                  left > 0 && place + row + m * kRows < L);
+                p += pass;
+            }
         }
     }
-}
+};
 
 // Writes a lane's two channels of one token (left: channels from the lane's first on).
 template <typename E, Copy kCopy>
-__device__ __forceinline__ void store_pair(E* p, const float (&f)[2], int left) {
+__device__ __forceinline__ void store_pair(E* p, F2 f, int left) {
     if constexpr (kCopy != kCopyOne) {
-        if (left > 0) store_vec<E, 2>(p, f);
+        const float x[2] = {f.lo(), f.hi()};
+        if (left > 0) store_vec<E, 2>(p, x);
     } else {
-        if (left > 0) p[0] = from_f<E>(f[0]);
-        if (left > 1) p[1] = from_f<E>(f[1]);
+        if (left > 0) p[0] = from_f<E>(f.lo());
+        if (left > 1) p[1] = from_f<E>(f.hi());
     }
 }
 
 // A lane's two channels of a state row.
 template <Copy kCopy>
-__device__ __forceinline__ void load_state(const float* p, float (&f)[2], int left) {
-    f[0] = f[1] = 0.f;
+__device__ __forceinline__ F2 load_state(const float* p, int left) {
+    float f[2] = {0.f, 0.f};
     if constexpr (kCopy != kCopyOne) {
         if (left > 0) load_f<float, 2>(p, f);
     } else {
         if (left > 0) f[0] = p[0];
         if (left > 1) f[1] = p[1];
     }
+    return f2(f[0], f[1]);
 }
 
 // ---- sequences of a row ------------------------------------------------------------------------
