@@ -39,12 +39,13 @@ struct Elements {
 };
 
 // kSeqs: one row holds all sequences, whose starts reset the state; else a row is a sequence.
-template <typename IO, typename GT, int kWrite, Copy kCopy, bool kSeqs>
-__global__ void __launch_bounds__(kScanThreads, 2)
+template <typename IO, typename GT, int kWrite, Copy kCopy, bool kSeqs, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, kWarps == 8 ? 2 : 1)
 scan_fwd_kernel(const FwdParams<IO, GT> p, const int cluster) {
-    extern __shared__ __align__(128) char stages[];
-    __shared__ ScanShared sh;
-    constexpr int kSeg = seg_of<IO, GT>, kTile = kScanWarps * kSeg;
+    extern __shared__ __align__(128) char smem[];
+    ScanShared<kWarps>& sh = *reinterpret_cast<ScanShared<kWarps>*>(smem);
+    char* const stages = smem + sizeof(sh);
+    constexpr int kSeg = seg_of<IO, GT>, kTile = kWarps * kSeg;
     constexpr int kStage = stage_bytes<IO, GT, kWrite>;
     using RowsIO = Rows<IO, kSeg>;
     using RowsGT = Rows<GT, kSeg>;
@@ -57,10 +58,10 @@ scan_fwd_kernel(const FwdParams<IO, GT> p, const int cluster) {
     const int L = p.L, D = p.D;
     const int origin = p.reverse ? L - 1 : 0, dir = p.reverse ? -1 : 1;
 
-    scan_open(sh, cluster);
-    if (kSeqs && blockIdx.x == 0) check_cu(p.q, p.status, tid, kScanThreads);
+    scan_open(sh.full, cluster);
+    if (kSeqs && blockIdx.x == 0) check_cu(p.q, p.status, tid, 32 * kWarps);
     if (kSeqs && rank == 0 && p.h_final) {  // empty sequences keep their state
-        for (int s = wid; s < p.q.n; s += kScanWarps) {
+        for (int s = wid; s < p.q.n; s += kWarps) {
             if (p.q.begin(s) != p.q.end(s)) continue;
             F2 x = f2(0.f);
             if (p.h0) x = load_state<kCopy>(p.h0 + (size_t)s * D + c, mine);
@@ -179,10 +180,18 @@ gdr_status fwd_launch(const gdr_scan_args& a, const ScanPtrs& x, cudaStream_t st
     p.slabs = (a.D + kSlab - 1) / kSlab;
     p.reverse = a.reverse;
     const long long units = (long long)p.slabs * (seqs ? 1 : a.B);
-    const int tile = kScanWarps * seg_of<IO, GT>;
-    const size_t smem = (size_t)kScanWarps * kStages * stage_bytes<IO, GT, kWrite>;
-    return seqs ? scan_launch(scan_fwd_kernel<IO, GT, kWrite, kCopy, true>, p, units, p.L, tile, smem, st)
-                : scan_launch(scan_fwd_kernel<IO, GT, kWrite, kCopy, false>, p, units, p.L, tile, smem, st);
+    const ScanPlan plan = scan_plan(units, kCopy == kCopy16);
+    auto launch = [&](auto kernel, int warps) {
+        const size_t smem = (size_t)warps * kStages * stage_bytes<IO, GT, kWrite> + scan_shared_bytes(warps);
+        return scan_launch(kernel, p, units, plan.cluster, warps, smem, st);
+    };
+    if constexpr (kCopy == kCopy16) {
+        if (plan.wide)
+            return seqs ? launch(scan_fwd_kernel<IO, GT, kWrite, kCopy, true, 16>, 16)
+                        : launch(scan_fwd_kernel<IO, GT, kWrite, kCopy, false, 16>, 16);
+    }
+    return seqs ? launch(scan_fwd_kernel<IO, GT, kWrite, kCopy, true, 8>, 8)
+                : launch(scan_fwd_kernel<IO, GT, kWrite, kCopy, false, 8>, 8);
 }
 
 struct Fwd {
@@ -242,12 +251,6 @@ struct Step {
 };
 
 }  // namespace
-
-int scan_cluster(long long units, long long tiles) {
-    int c = 1;
-    while (c < kScanMaxCluster && units * c < 2 * 148 && tiles >= 2 * c) c *= 2;
-    return c;
-}
 
 gdr_status launch_scan_fwd(const gdr_scan_args& a, const ScanPtrs& x, cudaStream_t st) {
     if (a.B * (long long)a.T == 0) {  // every state stays

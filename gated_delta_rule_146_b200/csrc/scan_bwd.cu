@@ -12,9 +12,8 @@ namespace gdr {
 
 namespace {
 
-constexpr int kStages = 4;
-constexpr int kSeg = 4;                    // tokens of a warp's run
-constexpr int kTile = kScanWarps * kSeg;
+constexpr int kSeg = 4;      // tokens of a warp's run
+constexpr int kStages = 3;
 
 template <typename IO, typename GT>
 struct BwdParams {
@@ -27,26 +26,33 @@ struct BwdParams {
     int D, L, slabs, reverse;
 };
 
-// Where a warp's tokens of each tensor lie in a stage: g, dO, o of the token before, v, beta.
+// A warp's tokens in shared memory, in two rings: g and dO of a tile are read when its run is
+// formed, o of the token before, v and beta a step later, when it is finished.
 template <typename IO, typename GT, int kWrite>
-struct Stage {
+struct Ring {
     static constexpr int kG = Rows<GT, kSeg>::kBytes, kI = Rows<IO, kSeg>::kBytes;
-    static constexpr int dO = kG, o = dO + kI, v = o + kI, beta = v + kI;
-    static constexpr int kBytes = v + (kWrite == GDR_WRITE_PLAIN ? 0 : kI) +
-                                  (kWrite == GDR_WRITE_GATE ? kG : 0);
+    static constexpr int kEarly = kG + kI;
+    static constexpr int v = kI, beta = v + kI;  // behind o
+    static constexpr int kLate = kI + (kWrite == GDR_WRITE_PLAIN ? 0 : kI) +
+                                 (kWrite == GDR_WRITE_GATE ? kG : 0);
+    static constexpr int kBytes = kStages * (kEarly + kLate);
 };
 
+template <int kWrite>
 struct Elements {
     F2 a[kSeg], d[kSeg];           // alpha; dO, with dh_final at a sequence's last token
+    F2 w[kWrite == GDR_WRITE_TIED ? kSeg : 1];
     Marks m;                       // start: the last token of a sequence, end: its first
 };
 
-template <typename IO, typename GT, int kWrite, Copy kCopy, bool kSeqs>
-__global__ void __launch_bounds__(kScanThreads, 2)
+template <typename IO, typename GT, int kWrite, Copy kCopy, bool kSeqs, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, kWarps == 8 ? 2 : 1)
 scan_bwd_kernel(const BwdParams<IO, GT> p, const int cluster) {
-    extern __shared__ __align__(128) char stages[];
-    __shared__ ScanShared sh;
-    using St = Stage<IO, GT, kWrite>;
+    extern __shared__ __align__(128) char smem[];
+    ScanShared<kWarps>& sh = *reinterpret_cast<ScanShared<kWarps>*>(smem);
+    char* const stages = smem + sizeof(sh);
+    using R = Ring<IO, GT, kWrite>;
+    constexpr int kTile = kWarps * kSeg;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int rank = blockIdx.x % cluster;
     const int unit = blockIdx.x / cluster;
@@ -57,10 +63,10 @@ scan_bwd_kernel(const BwdParams<IO, GT> p, const int cluster) {
     // the adjoint's order: the forward's, backwards
     const int origin = p.reverse ? 0 : L - 1, dir = p.reverse ? 1 : -1;
 
-    scan_open(sh, cluster);
-    if (kSeqs && blockIdx.x == 0) check_cu(p.q, p.status, tid, kScanThreads);
+    scan_open(sh.full, cluster);
+    if (kSeqs && blockIdx.x == 0) check_cu(p.q, p.status, tid, 32 * kWarps);
     if (kSeqs && rank == 0 && p.dh0) {  // the state's gradient passes an empty sequence unchanged
-        for (int s = wid; s < p.q.n; s += kScanWarps) {
+        for (int s = wid; s < p.q.n; s += kWarps) {
             if (p.q.begin(s) != p.q.end(s)) continue;
             F2 x = f2(0.f);
             if (p.dh_final) x = load_state<kCopy>(p.dh_final + (size_t)s * D + c, mine);
@@ -72,7 +78,8 @@ scan_bwd_kernel(const BwdParams<IO, GT> p, const int cluster) {
     const int stride = cluster * kTile, first0 = rank * kTile + wid * kSeg;
     const int steps = (int)(((long long)L + stride - 1) / stride);
     const long long hop = (long long)dir * stride * D;
-    char* const buf = stages + wid * kStages * St::kBytes;
+    char* const early = stages + wid * R::kBytes;
+    char* const late = early + kStages * R::kEarly;
     Feed<GT, kCopy, kSeg> fg, fb;
     Feed<IO, kCopy, kSeg> fd, fo, fv;
     fg.open(p.g + base, origin, dir, first0, D, left, lane);
@@ -80,19 +87,24 @@ scan_bwd_kernel(const BwdParams<IO, GT> p, const int cluster) {
     fo.open(p.o + base, origin, dir, first0 + 1, D, left, lane);
     if constexpr (kWrite != GDR_WRITE_PLAIN) fv.open(p.v + base, origin, dir, first0, D, left, lane);
     if constexpr (kWrite == GDR_WRITE_GATE) fb.open(p.beta + base, origin, dir, first0, D, left, lane);
-    auto feed = [&](int k) {
-        char* s = buf + k % kStages * St::kBytes;
-        const int place = k < steps ? first0 + k * stride : L;
-        fg.tile(s, place, L, hop);
-        fd.tile(s + St::dO, place, L, hop);
-        fo.tile(s + St::o, place + 1, L, hop);
-        if constexpr (kWrite != GDR_WRITE_PLAIN) fv.tile(s + St::v, place, L, hop);
-        if constexpr (kWrite == GDR_WRITE_GATE) fb.tile(s + St::beta, place, L, hop);
-        copy_commit();
+    auto place_of = [&](int k) { return k < steps ? first0 + k * stride : L; };
+    auto feed_early = [&](int k) {
+        char* s = early + k % kStages * R::kEarly;
+        fg.tile(s, place_of(k), L, hop);
+        fd.tile(s + R::kG, place_of(k), L, hop);
     };
-    // a tile's stage is read until the tile is finished, a step after it was formed
-#pragma unroll
-    for (int k = 0; k < kStages - 2; ++k) feed(k);
+    auto feed_late = [&](int k) {
+        char* s = late + k % kStages * R::kLate;
+        fo.tile(s, place_of(k) + 1, L, hop);
+        if constexpr (kWrite != GDR_WRITE_PLAIN) fv.tile(s + R::v, place_of(k), L, hop);
+        if constexpr (kWrite == GDR_WRITE_GATE) fb.tile(s + R::beta, place_of(k), L, hop);
+    };
+    // copy group k: the first ring's tile k and the second's tile k - 1
+    feed_early(0);
+    copy_commit();
+    feed_early(1);
+    feed_late(0);
+    copy_commit();
 
     F2 carry = f2(0.f), h0_row = f2(0.f);
     if (!kSeqs) {
@@ -100,19 +112,24 @@ scan_bwd_kernel(const BwdParams<IO, GT> p, const int cluster) {
         if (p.h0) h0_row = load_state<kCopy>(p.h0 + (size_t)row * D + c, mine);
     }
     Here here{0, 0};
-    auto form = [&](int k, Elements& e) {
-        copy_wait<kStages - 3>();
+    auto form = [&](int k, Elements<kWrite>& e) {
+        copy_wait<1>();
         __syncwarp();
-        feed(k + kStages - 2);
-        const char* s = buf + k % kStages * St::kBytes;
+        // into the stages of tiles k - 1 and k - 2, which every lane has read
+        feed_early(k + 2);
+        feed_late(k + 1);
+        copy_commit();
+        const char* s = early + k % kStages * R::kEarly;
         if constexpr (kSeqs) {
             const int first = first0 + k * stride;
             e.m = find_marks(p.q, here, origin, dir, first, min(kSeg, L - first), lane);
         }
 #pragma unroll
         for (int i = 0; i < kSeg; ++i) {
-            e.a[i] = exp2ch(Rows<GT, kSeg>::read(s, i, lane));
-            e.d[i] = Rows<IO, kSeg>::read(s + St::dO, i, lane);
+            const F2 g = Rows<GT, kSeg>::read(s, i, lane);
+            e.a[i] = exp2ch(g);
+            if constexpr (kWrite == GDR_WRITE_TIED) e.w[i] = one_minus(g, e.a[i]);
+            e.d[i] = Rows<IO, kSeg>::read(s + R::kG, i, lane);
             if (kSeqs && (e.m.start >> i & 1u) && p.dh_final) {
                 const int q = __shfl_sync(0xffffffffu, e.m.seq, i);
                 e.d[i] = add2(e.d[i], load_state<kCopy>(p.dh_final + (size_t)q * D + c, mine));
@@ -131,8 +148,12 @@ scan_bwd_kernel(const BwdParams<IO, GT> p, const int cluster) {
 
     const long long next = (long long)dir * D;
     long long out = (long long)base + (origin + (long long)dir * first0) * D + 2 * lane;
-    auto finish = [&](int k, const Elements& e, F2 mu) {
-        const char* s = buf + k % kStages * St::kBytes;
+    auto finish = [&](int k, const Elements<kWrite>& e, F2 mu) {
+        if (k + 1 == steps) {  // no tile was formed behind this one: its second ring may be on the way
+            copy_wait<0>();
+            __syncwarp();
+        }
+        const char* s = late + k % kStages * R::kLate;
         const int first = first0 + k * stride, n = L - first;
         long long at = out;
         out += hop;
@@ -144,7 +165,7 @@ scan_bwd_kernel(const BwdParams<IO, GT> p, const int cluster) {
             const F2 lam = kSeqs ? pick2(e.m.start >> i & 1u, e.d[i], sum) : sum;
             mu = mul2(e.a[i], lam);
             if (i >= n) continue;
-            F2 hp = Rows<IO, kSeg>::read(s + St::o, i, lane);
+            F2 hp = Rows<IO, kSeg>::read(s, i, lane);
             if (ends) {
                 hp = h0_row;
                 if (kSeqs && p.h0) hp = load_state<kCopy>(p.h0 + (size_t)q * D + c, mine);
@@ -153,21 +174,20 @@ scan_bwd_kernel(const BwdParams<IO, GT> p, const int cluster) {
             if constexpr (kWrite == GDR_WRITE_PLAIN) {
                 store_pair<IO, kCopy>(p.dv + at, lam, mine);
             } else {
-                const F2 v = Rows<IO, kSeg>::read(s + St::v, i, lane);
+                const F2 v = Rows<IO, kSeg>::read(s + R::v, i, lane);
                 if constexpr (kWrite == GDR_WRITE_GATE) {
                     store_pair<GT, kCopy>(p.dbeta + at, mul2(lam, v), mine);
                     store_pair<IO, kCopy>(
-                        p.dv + at, mul2(lam, Rows<GT, kSeg>::read(s + St::beta, i, lane)), mine);
+                        p.dv + at, mul2(lam, Rows<GT, kSeg>::read(s + R::beta, i, lane)), mine);
                 } else {
                     hp = add2(hp, f2(-v.lo(), -v.hi()));
-                    const F2 w = one_minus(Rows<GT, kSeg>::read(s, i, lane), e.a[i]);
-                    store_pair<IO, kCopy>(p.dv + at, mul2(w, lam), mine);
+                    store_pair<IO, kCopy>(p.dv + at, mul2(e.w[i], lam), mine);
                 }
             }
             store_pair<GT, kCopy>(p.dg + at, mul2(mu, hp), mine);
         }
     };
-    const bool ok = scan_walk<kSeqs, Elements>(sh, steps, cluster, rank, wid, lane, carry, form, finish);
+    const bool ok = scan_walk<kSeqs, Elements<kWrite>>(sh, steps, cluster, rank, wid, lane, carry, form, finish);
     if (!ok && p.status) atomicCAS(p.status, (int)GDR_OK, (int)GDR_ERR_TIMEOUT);
     scan_close(cluster);
 }
@@ -194,9 +214,20 @@ gdr_status bwd_launch(const gdr_scan_args& a, const ScanPtrs& x, cudaStream_t st
     p.slabs = (a.D + kSlab - 1) / kSlab;
     p.reverse = a.reverse;
     const long long units = (long long)p.slabs * (seqs ? 1 : a.B);
-    const size_t smem = (size_t)kScanWarps * kStages * Stage<IO, GT, kWrite>::kBytes;
-    return seqs ? scan_launch(scan_bwd_kernel<IO, GT, kWrite, kCopy, true>, p, units, p.L, kTile, smem, st)
-                : scan_launch(scan_bwd_kernel<IO, GT, kWrite, kCopy, false>, p, units, p.L, kTile, smem, st);
+    // 16 warps' rings fit an SM's shared memory in bf16 only
+    constexpr bool kMayWide = kCopy == kCopy16 && sizeof(IO) + sizeof(GT) == 4;
+    const ScanPlan plan = scan_plan(units, kMayWide);
+    auto launch = [&](auto kernel, int warps) {
+        return scan_launch(kernel, p, units, plan.cluster, warps,
+                           (size_t)warps * Ring<IO, GT, kWrite>::kBytes + scan_shared_bytes(warps), st);
+    };
+    if constexpr (kMayWide) {
+        if (plan.wide)
+            return seqs ? launch(scan_bwd_kernel<IO, GT, kWrite, kCopy, true, 16>, 16)
+                        : launch(scan_bwd_kernel<IO, GT, kWrite, kCopy, false, 16>, 16);
+    }
+    return seqs ? launch(scan_bwd_kernel<IO, GT, kWrite, kCopy, true, 8>, 8)
+                : launch(scan_bwd_kernel<IO, GT, kWrite, kCopy, false, 8>, 8);
 }
 
 struct Bwd {

@@ -4,8 +4,8 @@
 //
 // A recurrence x <- a x + b over a run of tokens is the map x -> A x + H (A the product of the
 // decays, H the run's result from zero), and maps compose.  A block owns a slab of 64 channels
-// of one row, two per lane, and walks it in tiles of kScanWarps * kSeg tokens: a warp takes
-// kSeg tokens and forms its run's (A, H); the block's warps join theirs through shared memory,
+// of one row, two per lane, and walks it in tiles of kWarps * kSeg tokens: a warp takes kSeg
+// tokens and forms its run's (A, H); the block's warps join theirs through shared memory,
 // in order.  Where rows and channels give too few blocks, the blocks of a cluster take
 // neighbouring tiles at once and join through distributed shared memory.  There is no other wait
 // between blocks, no workspace, and every join has a fixed order.
@@ -27,8 +27,6 @@ namespace gdr {
 
 using namespace tc;
 
-constexpr int kScanWarps = 8;
-constexpr int kScanThreads = 32 * kScanWarps;
 constexpr int kScanMaxCluster = 8;             // a warp hands the block's run to one block
 constexpr int kSlab = 64;                      // channels of a block
 constexpr float kReset = -1.f;
@@ -71,15 +69,15 @@ __device__ __forceinline__ float max_nan(float x, float y) {
 }
 
 // e^g = 2^(g log2 e).  The product is rounded; what the rounding left out, e, and the low part of
-// log2 e multiply the result by 2^e = 1 + e ln 2 to first order (e is below 2^-17 in the range).
+// log2 e multiply the result by 2^e = 1 + e ln 2 to first order (e is below 2^-16 in the range).
 // Below e^-150 the result is zero in either case, and the clamp keeps -inf out of the products.
 __device__ __forceinline__ F2 exp2ch(F2 g) {
     const F2 x = f2(max_nan(g.lo(), -150.f), max_nan(g.hi(), -150.f));
     const F2 t = mul2(x, f2(1.44269504f));
-    F2 e = fma2(x, f2(1.44269504f), f2(-t.lo(), -t.hi()));
-    e = fma2(x, f2(1.92596303e-8f), e);
+    F2 e = fma2(x, f2(-1.44269504f), t);  // -e
+    e = fma2(x, f2(-1.92596303e-8f), e);
     const F2 m = f2(ex2(t.lo()), ex2(t.hi()));
-    return fma2(mul2(m, e), f2(0.693147181f), m);
+    return fma2(mul2(m, e), f2(-0.693147181f), m);
 }
 
 // 1 - e^g given a = e^g: the series of e^g - 1 near zero (|g| < 1/2; the term left out is below
@@ -92,8 +90,8 @@ __device__ __forceinline__ F2 one_minus(F2 g, F2 a) {
     q = fma2(q, g, f2(1.f / 6));
     q = fma2(q, g, f2(0.5f));
     q = fma2(q, g, f2(1.f));
-    q = mul2(q, f2(-g.lo(), -g.hi()));
-    return f2(fabsf(g.lo()) < 0.5f ? q.lo() : 1.f - a.lo(), fabsf(g.hi()) < 0.5f ? q.hi() : 1.f - a.hi());
+    q = mul2(q, g);
+    return f2(fabsf(g.lo()) < 0.5f ? -q.lo() : 1.f - a.lo(), fabsf(g.hi()) < 0.5f ? -q.hi() : 1.f - a.hi());
 }
 
 template <int kLeft> __device__ __forceinline__ void copy_wait();
@@ -125,20 +123,24 @@ __device__ __forceinline__ Run run_join(const Run& f, const Run& r) {
 // a barrier, and a slot is written again only behind another one that every reader has passed.
 // The same holds between blocks: a block sends tile k + 1 once it has every block's tile k, and a
 // block sends that once all its warps have finished tile k - 2.
-struct ScanShared {
-    Run warp[4][kScanWarps][32];
+template <int kWarps>
+struct alignas(128) ScanShared {
+    Run warp[4][kWarps][32];
     Run block[4][kScanMaxCluster][32];
-    uint64_t full[4];   // bytes of block[] that have come
+    alignas(128) uint64_t full[4];   // bytes of block[] that have come
 };
+inline size_t scan_shared_bytes(int warps) {
+    return warps == 16 ? sizeof(ScanShared<16>) : sizeof(ScanShared<8>);
+}
 
 // Joins the block's runs of tile k (written, behind a block barrier) and sends the result to
 // block `to` of the cluster.
-template <bool kSeqs>
-__device__ __forceinline__ void send_run(ScanShared& sh, int k, int rank, int to, int lane) {
-    const Run(&r)[kScanWarps][32] = sh.warp[k & 3];
+template <bool kSeqs, int kWarps>
+__device__ __forceinline__ void send_run(ScanShared<kWarps>& sh, int k, int rank, int to, int lane) {
+    const Run(&r)[kWarps][32] = sh.warp[k & 3];
     Run all = r[0][lane];
 #pragma unroll
-    for (int w = 1; w < kScanWarps; ++w) all = run_join<kSeqs>(all, r[w][lane]);
+    for (int w = 1; w < kWarps; ++w) all = run_join<kSeqs>(all, r[w][lane]);
     const uint32_t dst = cluster_map(smem_u32(&sh.block[k & 3][rank][lane]), to);
     const uint32_t bar = cluster_map(smem_u32(&sh.full[k & 3]), to);
     asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];"
@@ -147,8 +149,8 @@ __device__ __forceinline__ void send_run(ScanShared& sh, int k, int rank, int to
 }
 
 // Waits, for two seconds at most, until every block's run of tile k is here.
-__device__ __forceinline__ bool runs_here(ScanShared& sh, int k) {
-    const uint32_t bar = smem_u32(&sh.full[k & 3]), parity = (uint32_t)(k >> 2) & 1u;
+__device__ __forceinline__ bool runs_here(uint64_t (&full)[4], int k) {
+    const uint32_t bar = smem_u32(&full[k & 3]), parity = (uint32_t)(k >> 2) & 1u;
     auto ready = [&](uint32_t ns) {
         uint32_t ok;
         asm volatile(
@@ -167,13 +169,13 @@ __device__ __forceinline__ bool runs_here(ScanShared& sh, int k) {
 
 // The state before the warp's run of tile k, from the carry before the step's first token, which
 // becomes the state behind its last.
-template <bool kSeqs>
-__device__ __forceinline__ F2 join_runs(const ScanShared& sh, int k, int cluster, int rank, int wid,
+template <bool kSeqs, int kWarps>
+__device__ __forceinline__ F2 join_runs(const ScanShared<kWarps>& sh, int k, int cluster, int rank, int wid,
                                         int lane, F2& carry) {
     F2 x = carry;
     if (cluster == 1) {
 #pragma unroll
-        for (int w = 0; w < kScanWarps; ++w) {
+        for (int w = 0; w < kWarps; ++w) {
             if (w == wid) x = carry;
             carry = run_apply<kSeqs>(sh.warp[k & 3][w][lane], carry);
         }
@@ -185,7 +187,7 @@ __device__ __forceinline__ F2 join_runs(const ScanShared& sh, int k, int cluster
         if (r < cluster) carry = run_apply<kSeqs>(sh.block[k & 3][r][lane], carry);
     }
 #pragma unroll
-    for (int w = 0; w < kScanWarps - 1; ++w)
+    for (int w = 0; w < kWarps - 1; ++w)
         if (w < wid) x = run_apply<kSeqs>(sh.warp[k & 3][w][lane], x);
     return x;
 }
@@ -193,8 +195,8 @@ __device__ __forceinline__ F2 join_runs(const ScanShared& sh, int k, int cluster
 // The walk over a row's tiles.  E holds a lane's elements of a tile; form(k, E) makes them and
 // writes the warp's run, finish(k, E, x) uses them with the state x before the run.  `dead`: a
 // wait ran out; the walk goes on without waiting, so that all threads meet at the barriers.
-template <bool kSeqs, typename E, typename Form, typename Finish>
-__device__ __forceinline__ bool scan_walk(ScanShared& sh, int steps, int cluster, int rank, int wid,
+template <bool kSeqs, typename E, int kWarps, typename Form, typename Finish>
+__device__ __forceinline__ bool scan_walk(ScanShared<kWarps>& sh, int steps, int cluster, int rank, int wid,
                                           int lane, F2& carry, Form form, Finish finish) {
     bool dead = false;
     auto publish = [&](int k) {
@@ -208,7 +210,7 @@ __device__ __forceinline__ bool scan_walk(ScanShared& sh, int steps, int cluster
             form(k + 1, next);
             __syncthreads();
         }
-        if (cluster > 1 && !dead) dead = !runs_here(sh, k);
+        if (cluster > 1 && !dead) dead = !runs_here(sh.full, k);
         if (k + 1 < steps) publish(k + 1);
         finish(k, now, join_runs<kSeqs>(sh, k, cluster, rank, wid, lane, carry));
     };
@@ -225,10 +227,10 @@ __device__ __forceinline__ bool scan_walk(ScanShared& sh, int steps, int cluster
 
 // The blocks of a cluster start together, their barriers ready, and end together, so that nothing
 // is sent to a block that is gone.
-__device__ __forceinline__ void scan_open(ScanShared& sh, int cluster) {
+__device__ __forceinline__ void scan_open(uint64_t (&full)[4], int cluster) {
     if (cluster == 1) return;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 4; ++i) mbar_init(&sh.full[i], 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&full[i], 1);
         mbar_init_fence();
     }
     cluster_sync_all();
@@ -404,20 +406,32 @@ inline Copy scan_copy(const gdr_scan_args& a) {
     return a.D % (f32 ? 4 : 8) == 0 ? kCopy16 : a.D % 2 == 0 && !mixed ? kCopyPair : kCopyOne;
 }
 
-// Blocks of a cluster: as few as fill the GPU (units: slabs times rows; tiles of a row).
-int scan_cluster(long long units, long long tiles);
+// How a call's units (slabs times rows) are laid out.  Many units: a block of 8 warps each, two
+// on an SM.  Few: blocks of 16 warps, one on an SM, and clusters of as many as the GPU holds at
+// once (its parts hold 16 SMs' worth of the larger clusters).
+struct ScanPlan {
+    int cluster;
+    bool wide;   // 16 warps
+};
+inline ScanPlan scan_plan(long long units, bool may_wide) {
+    ScanPlan p{1, false};
+    if (units >= 148) return p;
+    p.wide = may_wide;
+    const long long most = may_wide ? 128 : 256;
+    while (p.cluster < kScanMaxCluster && units * p.cluster * 2 <= most) p.cluster *= 2;
+    return p;
+}
 
 template <typename P>
-gdr_status scan_launch(void (*kernel)(P, int), const P& p, long long units, int L, int tile,
+gdr_status scan_launch(void (*kernel)(P, int), const P& p, long long units, int cluster, int warps,
                        size_t smem, cudaStream_t st) {
-    const int cluster = scan_cluster(units, ((long long)L + tile - 1) / tile);
     if (units * cluster > 0x7fffffffLL) return GDR_ERR_UNSUPPORTED;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
         cudaSuccess)
         return GDR_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(units * cluster));
-    cfg.blockDim = dim3(kScanThreads);
+    cfg.blockDim = dim3(32 * warps);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
