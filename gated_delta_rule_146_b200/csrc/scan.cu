@@ -39,11 +39,13 @@ struct Elements {
 };
 
 // kSeqs: one row holds all sequences, whose starts reset the state; else a row is a sequence.
-template <typename IO, typename GT, int kWrite, Copy kCopy, bool kSeqs, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps, kWarps == 8 ? 2 : 1)
+template <typename IO, typename GT, int kWrite, Copy kCopy, bool kSeqs, bool kCluster,
+          int kWarps>
+__global__ void __launch_bounds__(32 * (kWarps + 2 * kCluster), kCluster ? 1 : 2)
 scan_fwd_kernel(const FwdParams<IO, GT> p, const int cluster) {
     extern __shared__ __align__(128) char smem[];
-    ScanShared<kWarps>& sh = *reinterpret_cast<ScanShared<kWarps>*>(smem);
+    using Shared = ScanShared<kWarps, kCluster>;
+    Shared& sh = *reinterpret_cast<Shared*>(smem);
     char* const stages = smem + sizeof(sh);
     constexpr int kSeg = seg_of<IO, GT>, kTile = kWarps * kSeg;
     constexpr int kStage = stage_bytes<IO, GT, kWrite>;
@@ -58,10 +60,12 @@ scan_fwd_kernel(const FwdParams<IO, GT> p, const int cluster) {
     const int L = p.L, D = p.D;
     const int origin = p.reverse ? L - 1 : 0, dir = p.reverse ? -1 : 1;
 
-    scan_open(sh.full, cluster);
-    if (kSeqs && blockIdx.x == 0) check_cu(p.q, p.status, tid, 32 * kWarps);
+    F2 carry = f2(0.f);  // the folder's; read before any block can write h_final
+    if (!kSeqs && (!kCluster || wid == kWarps) && p.h0) carry = load_state<kCopy>(p.h0 + (size_t)row * D + c, mine);
+    scan_open<kCluster>(sh.full);
+    if (kSeqs && blockIdx.x == 0) check_cu(p.q, p.status, tid, 32 * (kWarps + 2 * kCluster));
     if (kSeqs && rank == 0 && p.h_final) {  // empty sequences keep their state
-        for (int s = wid; s < p.q.n; s += kWarps) {
+        for (int s = wid; s < p.q.n; s += kWarps + 2 * kCluster) {
             if (p.q.begin(s) != p.q.end(s)) continue;
             F2 x = f2(0.f);
             if (p.h0) x = load_state<kCopy>(p.h0 + (size_t)s * D + c, mine);
@@ -89,14 +93,24 @@ scan_fwd_kernel(const FwdParams<IO, GT> p, const int cluster) {
             fb.tile(s + RowsIO::kBytes + RowsGT::kBytes, place, L, hop);
         copy_commit();
     };
+    if constexpr (kCluster) if (wid >= kWarps) {
+        if (wid > kWarps) {
+            scan_publish<kSeqs>(sh, steps, cluster, rank, lane);
+        } else {
+            const bool ok = scan_fold<kSeqs>(sh, steps, cluster, rank, lane, carry);
+            if (!ok && p.status && lane == 0) atomicCAS(p.status, (int)GDR_OK, (int)GDR_ERR_TIMEOUT);
+            if (!kSeqs && p.h_final && rank == 0)
+                store_pair<float, kCopy>(p.h_final + (size_t)row * D + c, carry, mine);
+        }
+        scan_close<kCluster>();
+        return;
+    }
 #pragma unroll
     for (int k = 0; k < kStages - 1; ++k) feed(k, k);
 
-    F2 carry = f2(0.f);
-    if (!kSeqs && p.h0) carry = load_state<kCopy>(p.h0 + (size_t)row * D + c, mine);
     Here here{0, 0};
     int stage = 0;  // of the next tile to be formed
-    auto form = [&](int k, Elements<kSeg>& e) {
+    auto form = [&](int k, Elements<kSeg>& e) -> Run {
         copy_wait<kStages - 2>();
         __syncwarp();
         // into the stage of the tile before: every lane has read it
@@ -134,7 +148,7 @@ scan_fwd_kernel(const FwdParams<IO, GT> p, const int cluster) {
             run.A = mul2(run.A, e.a[i]);
         }
         if (kSeqs && e.m.start) run.A = f2(kReset);
-        sh.warp[k & 3][wid][lane] = run;
+        return run;
     };
 
     const long long next = (long long)dir * D;
@@ -155,12 +169,15 @@ scan_fwd_kernel(const FwdParams<IO, GT> p, const int cluster) {
             }
         }
     };
-    const bool ok = scan_walk<kSeqs, Elements<kSeg>>(sh, steps, cluster, rank, wid, lane, carry, form,
-                                                     finish);
-    if (!ok && p.status) atomicCAS(p.status, (int)GDR_OK, (int)GDR_ERR_TIMEOUT);
-    if (!kSeqs && p.h_final && rank == 0 && wid == 0)
-        store_pair<float, kCopy>(p.h_final + (size_t)row * D + c, carry, mine);
-    scan_close(cluster);
+    if constexpr (kCluster) {
+        scan_work<Elements<kSeg>>(sh, steps, wid, lane, form, finish);
+    } else {
+        scan_walk<kSeqs, Elements<kSeg>>(sh, steps, wid, lane, carry, form, finish);
+        if (!kSeqs && p.h_final && wid == 0)
+            store_pair<float, kCopy>(p.h_final + (size_t)row * D + c, carry, mine);
+    }
+    copy_wait<0>();
+    scan_close<kCluster>();
 }
 
 template <typename IO, typename GT, int kWrite, Copy kCopy>
@@ -180,18 +197,22 @@ gdr_status fwd_launch(const gdr_scan_args& a, const ScanPtrs& x, cudaStream_t st
     p.slabs = (a.D + kSlab - 1) / kSlab;
     p.reverse = a.reverse;
     const long long units = (long long)p.slabs * (seqs ? 1 : a.B);
-    const ScanPlan plan = scan_plan(units, kCopy == kCopy16);
-    auto launch = [&](auto kernel, int warps) {
-        const size_t smem = (size_t)warps * kStages * stage_bytes<IO, GT, kWrite> + scan_shared_bytes(warps);
-        return scan_launch(kernel, p, units, plan.cluster, warps, smem, st);
+    const int cluster = kCopy == kCopyOne ? 0 : scan_cluster(units);
+    constexpr int kWide = 16;
+    auto launch = [&](auto kernel, int warps, int threads, size_t shared) {
+        const size_t smem = (size_t)warps * kStages * stage_bytes<IO, GT, kWrite> + shared;
+        return scan_launch(kernel, p, units, cluster ? cluster : 1, threads, smem, st);
     };
-    if constexpr (kCopy == kCopy16) {
-        if (plan.wide)
-            return seqs ? launch(scan_fwd_kernel<IO, GT, kWrite, kCopy, true, 16>, 16)
-                        : launch(scan_fwd_kernel<IO, GT, kWrite, kCopy, false, 16>, 16);
+    if constexpr (kCopy != kCopyOne) {
+        if (cluster) {
+            constexpr int kThreads = 32 * (kWide + 2);
+            constexpr size_t kShared = sizeof(ScanShared<kWide, true>);
+            return seqs ? launch(scan_fwd_kernel<IO, GT, kWrite, kCopy, true, true, kWide>, kWide, kThreads, kShared)
+                        : launch(scan_fwd_kernel<IO, GT, kWrite, kCopy, false, true, kWide>, kWide, kThreads, kShared);
+        }
     }
-    return seqs ? launch(scan_fwd_kernel<IO, GT, kWrite, kCopy, true, 8>, 8)
-                : launch(scan_fwd_kernel<IO, GT, kWrite, kCopy, false, 8>, 8);
+    return seqs ? launch(scan_fwd_kernel<IO, GT, kWrite, kCopy, true, false, 8>, 8, 256, sizeof(ScanShared<8, false>))
+                : launch(scan_fwd_kernel<IO, GT, kWrite, kCopy, false, false, 8>, 8, 256, sizeof(ScanShared<8, false>));
 }
 
 struct Fwd {

@@ -45,11 +45,13 @@ struct Elements {
     Marks m;                       // start: the last token of a sequence, end: its first
 };
 
-template <typename IO, typename GT, int kWrite, Copy kCopy, bool kSeqs, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps, kWarps == 8 ? 2 : 1)
+template <typename IO, typename GT, int kWrite, Copy kCopy, bool kSeqs, bool kCluster,
+          int kWarps>
+__global__ void __launch_bounds__(32 * (kWarps + 2 * kCluster), kCluster ? 1 : 2)
 scan_bwd_kernel(const BwdParams<IO, GT> p, const int cluster) {
     extern __shared__ __align__(128) char smem[];
-    ScanShared<kWarps>& sh = *reinterpret_cast<ScanShared<kWarps>*>(smem);
+    using Shared = ScanShared<kWarps, kCluster>;
+    Shared& sh = *reinterpret_cast<Shared*>(smem);
     char* const stages = smem + sizeof(sh);
     using R = Ring<IO, GT, kWrite>;
     constexpr int kTile = kWarps * kSeg;
@@ -63,10 +65,13 @@ scan_bwd_kernel(const BwdParams<IO, GT> p, const int cluster) {
     // the adjoint's order: the forward's, backwards
     const int origin = p.reverse ? 0 : L - 1, dir = p.reverse ? 1 : -1;
 
-    scan_open(sh.full, cluster);
-    if (kSeqs && blockIdx.x == 0) check_cu(p.q, p.status, tid, 32 * kWarps);
+    F2 carry = f2(0.f), h0_row = f2(0.f);  // the folder's, the workers'
+    if (!kSeqs && (!kCluster || wid == kWarps) && p.dh_final)
+        carry = load_state<kCopy>(p.dh_final + (size_t)row * D + c, mine);
+    scan_open<kCluster>(sh.full);
+    if (kSeqs && blockIdx.x == 0) check_cu(p.q, p.status, tid, 32 * (kWarps + 2 * kCluster));
     if (kSeqs && rank == 0 && p.dh0) {  // the state's gradient passes an empty sequence unchanged
-        for (int s = wid; s < p.q.n; s += kWarps) {
+        for (int s = wid; s < p.q.n; s += kWarps + 2 * kCluster) {
             if (p.q.begin(s) != p.q.end(s)) continue;
             F2 x = f2(0.f);
             if (p.dh_final) x = load_state<kCopy>(p.dh_final + (size_t)s * D + c, mine);
@@ -99,6 +104,16 @@ scan_bwd_kernel(const BwdParams<IO, GT> p, const int cluster) {
         if constexpr (kWrite != GDR_WRITE_PLAIN) fv.tile(s + R::v, place_of(k), L, hop);
         if constexpr (kWrite == GDR_WRITE_GATE) fb.tile(s + R::beta, place_of(k), L, hop);
     };
+    if constexpr (kCluster) if (wid >= kWarps) {
+        if (wid > kWarps) {
+            scan_publish<kSeqs>(sh, steps, cluster, rank, lane);
+        } else {
+            const bool ok = scan_fold<kSeqs>(sh, steps, cluster, rank, lane, carry);
+            if (!ok && p.status && lane == 0) atomicCAS(p.status, (int)GDR_OK, (int)GDR_ERR_TIMEOUT);
+        }
+        scan_close<kCluster>();
+        return;
+    }
     // copy group k: the first ring's tile k and the second's tile k - 1
     feed_early(0);
     copy_commit();
@@ -106,13 +121,9 @@ scan_bwd_kernel(const BwdParams<IO, GT> p, const int cluster) {
     feed_late(0);
     copy_commit();
 
-    F2 carry = f2(0.f), h0_row = f2(0.f);
-    if (!kSeqs) {
-        if (p.dh_final) carry = load_state<kCopy>(p.dh_final + (size_t)row * D + c, mine);
-        if (p.h0) h0_row = load_state<kCopy>(p.h0 + (size_t)row * D + c, mine);
-    }
+    if (!kSeqs && p.h0) h0_row = load_state<kCopy>(p.h0 + (size_t)row * D + c, mine);
     Here here{0, 0};
-    auto form = [&](int k, Elements<kWrite>& e) {
+    auto form = [&](int k, Elements<kWrite>& e) -> Run {
         copy_wait<1>();
         __syncwarp();
         // into the stages of tiles k - 1 and k - 2, which every lane has read
@@ -143,7 +154,7 @@ scan_bwd_kernel(const BwdParams<IO, GT> p, const int cluster) {
             run.A = mul2(run.A, e.a[i]);
         }
         if (kSeqs && e.m.start) run.A = f2(kReset);
-        sh.warp[k & 3][wid][lane] = run;
+        return run;
     };
 
     const long long next = (long long)dir * D;
@@ -187,9 +198,13 @@ scan_bwd_kernel(const BwdParams<IO, GT> p, const int cluster) {
             store_pair<GT, kCopy>(p.dg + at, mul2(mu, hp), mine);
         }
     };
-    const bool ok = scan_walk<kSeqs, Elements<kWrite>>(sh, steps, cluster, rank, wid, lane, carry, form, finish);
-    if (!ok && p.status) atomicCAS(p.status, (int)GDR_OK, (int)GDR_ERR_TIMEOUT);
-    scan_close(cluster);
+    if constexpr (kCluster) {
+        scan_work<Elements<kWrite>>(sh, steps, wid, lane, form, finish);
+    } else {
+        scan_walk<kSeqs, Elements<kWrite>>(sh, steps, wid, lane, carry, form, finish);
+    }
+    copy_wait<0>();
+    scan_close<kCluster>();
 }
 
 template <typename IO, typename GT, int kWrite, Copy kCopy>
@@ -214,20 +229,23 @@ gdr_status bwd_launch(const gdr_scan_args& a, const ScanPtrs& x, cudaStream_t st
     p.slabs = (a.D + kSlab - 1) / kSlab;
     p.reverse = a.reverse;
     const long long units = (long long)p.slabs * (seqs ? 1 : a.B);
+    const int cluster = kCopy == kCopyOne ? 0 : scan_cluster(units);
     // 16 warps' rings fit an SM's shared memory in bf16 only
-    constexpr bool kMayWide = kCopy == kCopy16 && sizeof(IO) + sizeof(GT) == 4;
-    const ScanPlan plan = scan_plan(units, kMayWide);
-    auto launch = [&](auto kernel, int warps) {
-        return scan_launch(kernel, p, units, plan.cluster, warps,
-                           (size_t)warps * Ring<IO, GT, kWrite>::kBytes + scan_shared_bytes(warps), st);
+    constexpr int kWide = sizeof(IO) + sizeof(GT) == 4 ? 16 : 8;
+    auto launch = [&](auto kernel, int warps, int threads, size_t shared) {
+        const size_t smem = (size_t)warps * Ring<IO, GT, kWrite>::kBytes + shared;
+        return scan_launch(kernel, p, units, cluster ? cluster : 1, threads, smem, st);
     };
-    if constexpr (kMayWide) {
-        if (plan.wide)
-            return seqs ? launch(scan_bwd_kernel<IO, GT, kWrite, kCopy, true, 16>, 16)
-                        : launch(scan_bwd_kernel<IO, GT, kWrite, kCopy, false, 16>, 16);
+    if constexpr (kCopy != kCopyOne) {
+        if (cluster) {
+            constexpr int kThreads = 32 * (kWide + 2);
+            constexpr size_t kShared = sizeof(ScanShared<kWide, true>);
+            return seqs ? launch(scan_bwd_kernel<IO, GT, kWrite, kCopy, true, true, kWide>, kWide, kThreads, kShared)
+                        : launch(scan_bwd_kernel<IO, GT, kWrite, kCopy, false, true, kWide>, kWide, kThreads, kShared);
+        }
     }
-    return seqs ? launch(scan_bwd_kernel<IO, GT, kWrite, kCopy, true, 8>, 8)
-                : launch(scan_bwd_kernel<IO, GT, kWrite, kCopy, false, 8>, 8);
+    return seqs ? launch(scan_bwd_kernel<IO, GT, kWrite, kCopy, true, false, 8>, 8, 256, sizeof(ScanShared<8, false>))
+                : launch(scan_bwd_kernel<IO, GT, kWrite, kCopy, false, false, 8>, 8, 256, sizeof(ScanShared<8, false>));
 }
 
 struct Bwd {

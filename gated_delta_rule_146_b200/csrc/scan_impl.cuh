@@ -10,10 +10,13 @@
 // neighbouring tiles at once and join through distributed shared memory.  There is no other wait
 // between blocks, no workspace, and every join has a fixed order.
 //
-// The walk is a pipeline.  A warp's tokens arrive by asynchronous copies, kStages - 1 tiles
-// ahead, into shared memory of its own; the runs of tile k + 1 are formed and handed over before
-// the elements of tile k are finished, so that neither the block's barrier nor the cluster's is
-// waited for right after it was reached.
+// The walk is a pipeline.  A warp's tokens arrive by asynchronous copies, two tiles ahead, into
+// shared memory of its own, and it forms the run of tile k + 1 before it finishes tile k.  In a
+// single block every warp then carries the state along the runs by itself: two blocks on an SM
+// cover each other's barriers.  In a cluster the way to the other blocks is long, and the work
+// around it is taken off the workers: one warp, the publisher, joins the block's runs and sends
+// them to all blocks; another, the folder, carries the state along and leaves every worker the
+// state before its run.
 //
 // A run that holds the start of a sequence ignores what comes in.  Its A is kReset (decays are
 // never negative) and the join selects H, so that infinities and NaN of the sequence before
@@ -94,8 +97,6 @@ __device__ __forceinline__ F2 one_minus(F2 g, F2 a) {
     return f2(fabsf(g.lo()) < 0.5f ? -q.lo() : 1.f - a.lo(), fabsf(g.hi()) < 0.5f ? -q.hi() : 1.f - a.hi());
 }
 
-template <int kLeft> __device__ __forceinline__ void copy_wait();
-
 // ---- runs ----------------------------------------------------------------------------------------
 // The map of a run, for a lane's two channels.
 struct alignas(16) Run {
@@ -119,38 +120,57 @@ __device__ __forceinline__ Run run_join(const Run& f, const Run& r) {
     return o;
 }
 
-// Runs handed over, by tile modulo four.  Between a tile's being written and its being read lies
-// a barrier, and a slot is written again only behind another one that every reader has passed.
-// The same holds between blocks: a block sends tile k + 1 once it has every block's tile k, and a
-// block sends that once all its warps have finished tile k - 2.
-template <int kWarps>
+// Runs go by tile parity: a warp forms tile k + 2 behind a barrier that all readers of tile k's
+// runs have passed (in a cluster: once it has the state of tile k, and the folder has read them by
+// then).  Blocks' runs go by tile modulo four: a block sends tile j when its workers have the
+// states of tile j - 2, for which every block has sent tile j - 2, and so has folded tile j - 4.
+template <int kWarps, bool kCluster>
 struct alignas(128) ScanShared {
-    Run warp[4][kWarps][32];
-    Run block[4][kScanMaxCluster][32];
+    Run run[2][kWarps][32];
+    F2 before[kCluster ? 2 : 1][kCluster ? kWarps : 1][32];
+    Run block[kCluster ? 4 : 1][kScanMaxCluster][32];
     alignas(128) uint64_t full[4];   // bytes of block[] that have come
 };
-inline size_t scan_shared_bytes(int warps) {
-    return warps == 16 ? sizeof(ScanShared<16>) : sizeof(ScanShared<8>);
+
+// A single block's walk over the row's tiles.  E holds a lane's elements of a tile; form(k, e)
+// makes them and returns the run, finish(k, e, x) uses them with the state x before it.  `carry`
+// goes from the state before the row's first token to the one behind its last.
+template <bool kSeqs, typename E, int kWarps, typename Form, typename Finish>
+__device__ __forceinline__ void scan_walk(ScanShared<kWarps, false>& sh, int steps, int wid, int lane,
+                                          F2& carry, Form form, Finish finish) {
+    auto turn = [&](int k, E& now, E& next) {
+        if (k + 1 < steps) sh.run[(k + 1) & 1][wid][lane] = form(k + 1, next);
+        F2 x = carry;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w == wid) x = carry;
+            carry = run_apply<kSeqs>(sh.run[k & 1][w][lane], carry);
+        }
+        finish(k, now, x);
+        __syncthreads();
+    };
+    E even, odd;
+    sh.run[0][wid][lane] = form(0, even);
+    __syncthreads();
+    for (int k = 0; k < steps; k += 2) {
+        turn(k, even, odd);
+        if (k + 1 < steps) turn(k + 1, odd, even);
+    }
 }
 
-// Joins the block's runs of tile k (written, behind a block barrier) and sends the result to
-// block `to` of the cluster.
-template <bool kSeqs, int kWarps>
-__device__ __forceinline__ void send_run(ScanShared<kWarps>& sh, int k, int rank, int to, int lane) {
-    const Run(&r)[kWarps][32] = sh.warp[k & 3];
-    Run all = r[0][lane];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) all = run_join<kSeqs>(all, r[w][lane]);
-    const uint32_t dst = cluster_map(smem_u32(&sh.block[k & 3][rank][lane]), to);
-    const uint32_t bar = cluster_map(smem_u32(&sh.full[k & 3]), to);
-    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];"
-                 ::"r"(dst), "f"(all.A.lo()), "f"(all.A.hi()), "f"(all.H.lo()), "f"(all.H.hi()), "r"(bar)
-                 : "memory");
+// The blocks' named barriers: tile k's runs are formed (kFormed + parity), the states before them
+// are there (kFolded + parity).
+enum { kFormed = 1, kFolded = 3 };
+__device__ __forceinline__ void bar_arrive(int id, int threads) {
+    asm volatile("barrier.cta.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 // Waits, for two seconds at most, until every block's run of tile k is here.
-__device__ __forceinline__ bool runs_here(uint64_t (&full)[4], int k) {
-    const uint32_t bar = smem_u32(&full[k & 3]), parity = (uint32_t)(k >> 2) & 1u;
+__device__ __forceinline__ bool runs_here(uint64_t* bar_, uint32_t parity) {
+    const uint32_t bar = smem_u32(bar_);
     auto ready = [&](uint32_t ns) {
         uint32_t ok;
         asm volatile(
@@ -167,77 +187,101 @@ __device__ __forceinline__ bool runs_here(uint64_t (&full)[4], int k) {
     return true;
 }
 
-// The state before the warp's run of tile k, from the carry before the step's first token, which
-// becomes the state behind its last.
-template <bool kSeqs, int kWarps>
-__device__ __forceinline__ F2 join_runs(const ScanShared<kWarps>& sh, int k, int cluster, int rank, int wid,
-                                        int lane, F2& carry) {
-    F2 x = carry;
-    if (cluster == 1) {
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w == wid) x = carry;
-            carry = run_apply<kSeqs>(sh.warp[k & 3][w][lane], carry);
-        }
-        return x;
-    }
-#pragma unroll
-    for (int r = 0; r < kScanMaxCluster; ++r) {
-        if (r == rank) x = carry;
-        if (r < cluster) carry = run_apply<kSeqs>(sh.block[k & 3][r][lane], carry);
-    }
-#pragma unroll
-    for (int w = 0; w < kWarps - 1; ++w)
-        if (w < wid) x = run_apply<kSeqs>(sh.warp[k & 3][w][lane], x);
-    return x;
-}
-
-// The walk over a row's tiles.  E holds a lane's elements of a tile; form(k, E) makes them and
-// writes the warp's run, finish(k, E, x) uses them with the state x before the run.  `dead`: a
-// wait ran out; the walk goes on without waiting, so that all threads meet at the barriers.
-template <bool kSeqs, typename E, int kWarps, typename Form, typename Finish>
-__device__ __forceinline__ bool scan_walk(ScanShared<kWarps>& sh, int steps, int cluster, int rank, int wid,
-                                          int lane, F2& carry, Form form, Finish finish) {
-    bool dead = false;
-    auto publish = [&](int k) {
-        if (cluster == 1) return;
-        if (threadIdx.x == 0) mbar_expect_tx(&sh.full[k & 3], (uint32_t)cluster * 32 * sizeof(Run));
-        if (wid < cluster) send_run<kSeqs>(sh, k, rank, wid, lane);
+// A worker's walk in a cluster.
+template <typename E, int kWarps, typename Form, typename Finish>
+__device__ __forceinline__ void scan_work(ScanShared<kWarps, true>& sh, int steps, int wid, int lane,
+                                          Form form, Finish finish) {
+    const int formed = blockDim.x, folded = 32 * (kWarps + 1);
+    auto give = [&](int k, E& e) {
+        sh.run[k & 1][wid][lane] = form(k, e);
+        bar_arrive(kFormed + (k & 1), formed);
     };
-    // tile k + 1's runs go out before tile k is finished
     auto turn = [&](int k, E& now, E& next) {
-        if (k + 1 < steps) {
-            form(k + 1, next);
-            __syncthreads();
-        }
-        if (cluster > 1 && !dead) dead = !runs_here(sh.full, k);
-        if (k + 1 < steps) publish(k + 1);
-        finish(k, now, join_runs<kSeqs>(sh, k, cluster, rank, wid, lane, carry));
+        if (k + 1 < steps) give(k + 1, next);
+        bar_sync(kFolded + (k & 1), folded);
+        finish(k, now, sh.before[k & 1][wid][lane]);
     };
     E even, odd;
-    form(0, even);
-    __syncthreads();
-    publish(0);
+    give(0, even);
     for (int k = 0; k < steps; k += 2) {
         turn(k, even, odd);
         if (k + 1 < steps) turn(k + 1, odd, even);
     }
-    return !dead;
+}
+
+// The folder's walk.  False if a wait ran out; the walk then goes on without waiting, so that all
+// threads meet at the barriers.
+template <bool kSeqs, int kWarps>
+__device__ __forceinline__ bool scan_fold(ScanShared<kWarps, true>& sh, int steps, int cluster, int rank,
+                                          int lane, F2& carry) {
+    bool ok = true;
+    for (int k = 0; k < steps; ++k) {
+        const int par = k & 1;
+        bar_sync(kFormed + par, blockDim.x);
+        uint64_t* full = &sh.full[k & 3];
+        if (lane == 0) mbar_expect_tx(full, (uint32_t)cluster * 32 * sizeof(Run));
+        // the maps from the block's first token to every worker, while the other blocks' runs come
+        Run to[kWarps];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) to[w] = sh.run[par][w][lane];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) to[w] = run_join<kSeqs>(to[w - 1], to[w]);
+        if (ok) ok = runs_here(full, (uint32_t)(k >> 2) & 1u);
+        ok = __all_sync(0xffffffffu, ok);
+        F2 x = carry;
+        Run blocks[kScanMaxCluster];
+#pragma unroll
+        for (int r = 0; r < kScanMaxCluster; ++r) blocks[r] = sh.block[k & 3][r][lane];
+#pragma unroll
+        for (int r = 0; r < kScanMaxCluster; ++r) {
+            if (r == rank) x = carry;
+            if (r < cluster) carry = run_apply<kSeqs>(blocks[r], carry);
+        }
+        sh.before[par][0][lane] = x;
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) sh.before[par][w][lane] = run_apply<kSeqs>(to[w - 1], x);
+        bar_arrive(kFolded + par, 32 * (kWarps + 1));
+    }
+    return ok;
+}
+
+// The publisher's walk: joins the block's runs of every tile and sends them to all blocks.
+template <bool kSeqs, int kWarps>
+__device__ __forceinline__ void scan_publish(ScanShared<kWarps, true>& sh, int steps, int cluster, int rank,
+                                             int lane) {
+    for (int k = 0; k < steps; ++k) {
+        bar_sync(kFormed + (k & 1), blockDim.x);
+        const Run(&r)[kWarps][32] = sh.run[k & 1];
+        Run all = r[0][lane];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) all = run_join<kSeqs>(all, r[w][lane]);
+        const uint32_t to = smem_u32(&sh.block[k & 3][rank][lane]), bar = smem_u32(&sh.full[k & 3]);
+        for (int b = 0; b < cluster; ++b)
+            asm volatile(
+                "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];"
+                ::"r"(cluster_map(to, b)), "f"(all.A.lo()), "f"(all.A.hi()), "f"(all.H.lo()),
+                "f"(all.H.hi()), "r"(cluster_map(bar, b))
+                : "memory");
+    }
 }
 
 // The blocks of a cluster start together, their barriers ready, and end together, so that nothing
 // is sent to a block that is gone.
-__device__ __forceinline__ void scan_open(uint64_t (&full)[4], int cluster) {
-    if (cluster == 1) return;
+template <bool kCluster>
+__device__ __forceinline__ void scan_open(uint64_t (&full)[4]) {
+    if (!kCluster) return;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 4; ++i) mbar_init(&full[i], 1);
         mbar_init_fence();
     }
+    __syncwarp();
     cluster_sync_all();
 }
-__device__ __forceinline__ void scan_close(int cluster) {
-    copy_wait<0>();
-    if (cluster > 1) cluster_sync_all();
+template <bool kCluster>
+__device__ __forceinline__ void scan_close() {
+    if (!kCluster) return;
+    __syncwarp();
+    cluster_sync_all();
 }
 
 // ---- feeding -----------------------------------------------------------------------------------
@@ -406,24 +450,21 @@ inline Copy scan_copy(const gdr_scan_args& a) {
     return a.D % (f32 ? 4 : 8) == 0 ? kCopy16 : a.D % 2 == 0 && !mixed ? kCopyPair : kCopyOne;
 }
 
-// How a call's units (slabs times rows) are laid out.  Many units: a block of 8 warps each, two
-// on an SM.  Few: blocks of 16 warps, one on an SM, and clusters of as many as the GPU holds at
-// once (its parts hold 16 SMs' worth of the larger clusters).
-struct ScanPlan {
-    int cluster;
-    bool wide;   // 16 warps
-};
-inline ScanPlan scan_plan(long long units, bool may_wide) {
-    ScanPlan p{1, false};
-    if (units >= 148) return p;
-    p.wide = may_wide;
-    const long long most = may_wide ? 128 : 256;
-    while (p.cluster < kScanMaxCluster && units * p.cluster * 2 <= most) p.cluster *= 2;
-    return p;
+// How a call's units (slabs times rows) are laid out.  Many: a block each, two on an SM.  Few: a
+// cluster each, of as many blocks as the GPU holds at once, one on an SM.  (The blocks of a cluster
+// are in one part of the GPU: the occupancy query counts 74 clusters of 2, 45 of 3, 33 of 4, 26
+// of 5, 22 of 6 and 15 of 7 or 8.)
+// 0: single blocks.
+inline int scan_cluster(long long units) {
+    static const unsigned char most[kScanMaxCluster + 1] = {0, 148, 74, 45, 33, 26, 22, 15, 15};
+    if (units > 74) return units <= 148 ? 1 : 0;
+    int c = kScanMaxCluster;
+    while (units > most[c]) --c;
+    return c;
 }
 
 template <typename P>
-gdr_status scan_launch(void (*kernel)(P, int), const P& p, long long units, int cluster, int warps,
+gdr_status scan_launch(void (*kernel)(P, int), const P& p, long long units, int cluster, int threads,
                        size_t smem, cudaStream_t st) {
     if (units * cluster > 0x7fffffffLL) return GDR_ERR_UNSUPPORTED;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
@@ -431,7 +472,7 @@ gdr_status scan_launch(void (*kernel)(P, int), const P& p, long long units, int 
         return GDR_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(units * cluster));
-    cfg.blockDim = dim3(32 * warps);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
