@@ -46,7 +46,7 @@ scan_fwd_kernel(const FwdParams<IO, GT> p, const int cluster) {
     extern __shared__ __align__(128) char smem[];
     using Shared = ScanShared<kWarps, kCluster>;
     Shared& sh = *reinterpret_cast<Shared*>(smem);
-    char* const stages = smem + sizeof(sh);
+    char* const stages = smem + sizeof(sh) + (kSeqs ? kCuBytes : 0);
     constexpr int kSeg = seg_of<IO, GT>, kTile = kWarps * kSeg;
     constexpr int kStage = stage_bytes<IO, GT, kWrite>;
     using RowsIO = Rows<IO, kSeg>;
@@ -62,11 +62,13 @@ scan_fwd_kernel(const FwdParams<IO, GT> p, const int cluster) {
 
     F2 carry = f2(0.f);  // the folder's; read before any block can write h_final
     if (!kSeqs && (!kCluster || wid == kWarps) && p.h0) carry = load_state<kCopy>(p.h0 + (size_t)row * D + c, mine);
+    Seqs seqs = p.q;
+    if constexpr (kSeqs) seqs = share_cu(p.q, reinterpret_cast<int32_t*>(smem + sizeof(sh)));
     scan_open<kCluster>(sh.full);
     if (kSeqs && blockIdx.x == 0) check_cu(p.q, p.status, tid, 32 * (kWarps + 2 * kCluster));
     if (kSeqs && rank == 0 && p.h_final) {  // empty sequences keep their state
-        for (int s = wid; s < p.q.n; s += kWarps + 2 * kCluster) {
-            if (p.q.begin(s) != p.q.end(s)) continue;
+        for (int s = wid; s < seqs.n; s += kWarps + 2 * kCluster) {
+            if (seqs.begin(s) != seqs.end(s)) continue;
             F2 x = f2(0.f);
             if (p.h0) x = load_state<kCopy>(p.h0 + (size_t)s * D + c, mine);
             store_pair<float, kCopy>(p.h_final + (size_t)s * D + c, x, mine);
@@ -117,6 +119,10 @@ scan_fwd_kernel(const FwdParams<IO, GT> p, const int cluster) {
         feed(k + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
         const char* s = buf + stage * kStage;
         stage = stage == kStages - 1 ? 0 : stage + 1;
+        if constexpr (kSeqs) {
+            const int first = first0 + k * stride;
+            e.m = find_marks(seqs, here, origin, dir, first, min(kSeg, L - first), lane);
+        }
 #pragma unroll
         for (int i = 0; i < kSeg; ++i) {
             const F2 v = RowsIO::read(s, i, lane), g = RowsGT::read(s + RowsIO::kBytes, i, lane);
@@ -128,26 +134,27 @@ scan_fwd_kernel(const FwdParams<IO, GT> p, const int cluster) {
             else
                 e.b[i] = v;
         }
-        if constexpr (kSeqs) {
-            const int first = first0 + k * stride;
-            e.m = find_marks(p.q, here, origin, dir, first, min(kSeg, L - first), lane);
-            if (e.m.start && p.h0) {  // b at a start takes the initial state in
+        if (kSeqs && e.m.start && p.h0) {  // b at a start takes the initial state in
 #pragma unroll
-                for (int i = 0; i < kSeg; ++i) {
-                    if (!(e.m.start >> i & 1u)) continue;
-                    const int q = __shfl_sync(0xffffffffu, e.m.seq, i);
-                    e.b[i] = fma2(e.a[i], load_state<kCopy>(p.h0 + (size_t)q * D + c, mine), e.b[i]);
-                }
+            for (int i = 0; i < kSeg; ++i) {
+                if (!(e.m.start >> i & 1u)) continue;
+                const int q = __shfl_sync(0xffffffffu, e.m.seq, i);
+                e.b[i] = fma2(e.a[i], load_state<kCopy>(p.h0 + (size_t)q * D + c, mine), e.b[i]);
             }
         }
         Run run{e.a[0], e.b[0]};
+        if (!kSeqs || !e.m.start) {
 #pragma unroll
-        for (int i = 1; i < kSeg; ++i) {
-            const F2 y = fma2(e.a[i], run.H, e.b[i]);
-            run.H = kSeqs ? pick2(e.m.start >> i & 1u, e.b[i], y) : y;
-            run.A = mul2(run.A, e.a[i]);
+            for (int i = 1; i < kSeg; ++i) {
+                run.H = fma2(e.a[i], run.H, e.b[i]);
+                run.A = mul2(run.A, e.a[i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 1; i < kSeg; ++i)
+                run.H = pick2(e.m.start >> i & 1u, e.b[i], fma2(e.a[i], run.H, e.b[i]));
+            run.A = f2(kReset);
         }
-        if (kSeqs && e.m.start) run.A = f2(kReset);
         return run;
     };
 
@@ -157,12 +164,19 @@ scan_fwd_kernel(const FwdParams<IO, GT> p, const int cluster) {
         const int n = L - (first0 + k * stride);
         IO* q = out;
         out += hop;
+        if (n >= kSeg && !(kSeqs && e.m.any())) {
 #pragma unroll
-        for (int i = 0; i < kSeg; ++i) {
+            for (int i = 0; i < kSeg; ++i, q += next) {
+                h = fma2(e.a[i], h, e.b[i]);
+                store_pair<IO, kCopy>(q, h, mine);
+            }
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < kSeg; ++i, q += next) {
             const F2 y = fma2(e.a[i], h, e.b[i]);
             h = kSeqs ? pick2(e.m.start >> i & 1u, e.b[i], y) : y;
             if (i < n) store_pair<IO, kCopy>(q, h, mine);
-            q += next;
             if (kSeqs && (e.m.end >> i & 1u) && p.h_final) {
                 const int s = __shfl_sync(0xffffffffu, e.m.seq, i);
                 store_pair<float, kCopy>(p.h_final + (size_t)s * D + c, h, mine);
@@ -200,7 +214,8 @@ gdr_status fwd_launch(const gdr_scan_args& a, const ScanPtrs& x, cudaStream_t st
     const int cluster = kCopy == kCopyOne ? 0 : scan_cluster(units);
     constexpr int kWide = 16;
     auto launch = [&](auto kernel, int warps, int threads, size_t shared) {
-        const size_t smem = (size_t)warps * kStages * stage_bytes<IO, GT, kWrite> + shared;
+        const size_t smem = (size_t)warps * kStages * stage_bytes<IO, GT, kWrite> + shared +
+                            (seqs ? kCuBytes : 0);
         return scan_launch(kernel, p, units, cluster ? cluster : 1, threads, smem, st);
     };
     if constexpr (kCopy != kCopyOne) {

@@ -52,7 +52,7 @@ scan_bwd_kernel(const BwdParams<IO, GT> p, const int cluster) {
     extern __shared__ __align__(128) char smem[];
     using Shared = ScanShared<kWarps, kCluster>;
     Shared& sh = *reinterpret_cast<Shared*>(smem);
-    char* const stages = smem + sizeof(sh);
+    char* const stages = smem + sizeof(sh) + (kSeqs ? kCuBytes : 0);
     using R = Ring<IO, GT, kWrite>;
     constexpr int kTile = kWarps * kSeg;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -68,11 +68,13 @@ scan_bwd_kernel(const BwdParams<IO, GT> p, const int cluster) {
     F2 carry = f2(0.f), h0_row = f2(0.f);  // the folder's, the workers'
     if (!kSeqs && (!kCluster || wid == kWarps) && p.dh_final)
         carry = load_state<kCopy>(p.dh_final + (size_t)row * D + c, mine);
+    Seqs seqs = p.q;
+    if constexpr (kSeqs) seqs = share_cu(p.q, reinterpret_cast<int32_t*>(smem + sizeof(sh)));
     scan_open<kCluster>(sh.full);
     if (kSeqs && blockIdx.x == 0) check_cu(p.q, p.status, tid, 32 * (kWarps + 2 * kCluster));
     if (kSeqs && rank == 0 && p.dh0) {  // the state's gradient passes an empty sequence unchanged
-        for (int s = wid; s < p.q.n; s += kWarps + 2 * kCluster) {
-            if (p.q.begin(s) != p.q.end(s)) continue;
+        for (int s = wid; s < seqs.n; s += kWarps + 2 * kCluster) {
+            if (seqs.begin(s) != seqs.end(s)) continue;
             F2 x = f2(0.f);
             if (p.dh_final) x = load_state<kCopy>(p.dh_final + (size_t)s * D + c, mine);
             store_pair<float, kCopy>(p.dh0 + (size_t)s * D + c, x, mine);
@@ -93,13 +95,13 @@ scan_bwd_kernel(const BwdParams<IO, GT> p, const int cluster) {
     if constexpr (kWrite != GDR_WRITE_PLAIN) fv.open(p.v + base, origin, dir, first0, D, left, lane);
     if constexpr (kWrite == GDR_WRITE_GATE) fb.open(p.beta + base, origin, dir, first0, D, left, lane);
     auto place_of = [&](int k) { return k < steps ? first0 + k * stride : L; };
-    auto feed_early = [&](int k) {
-        char* s = early + k % kStages * R::kEarly;
+    auto feed_early = [&](int k, int stage) {
+        char* s = early + stage * R::kEarly;
         fg.tile(s, place_of(k), L, hop);
         fd.tile(s + R::kG, place_of(k), L, hop);
     };
-    auto feed_late = [&](int k) {
-        char* s = late + k % kStages * R::kLate;
+    auto feed_late = [&](int k, int stage) {
+        char* s = late + stage * R::kLate;
         fo.tile(s, place_of(k) + 1, L, hop);
         if constexpr (kWrite != GDR_WRITE_PLAIN) fv.tile(s + R::v, place_of(k), L, hop);
         if constexpr (kWrite == GDR_WRITE_GATE) fb.tile(s + R::beta, place_of(k), L, hop);
@@ -115,25 +117,28 @@ scan_bwd_kernel(const BwdParams<IO, GT> p, const int cluster) {
         return;
     }
     // copy group k: the first ring's tile k and the second's tile k - 1
-    feed_early(0);
+    feed_early(0, 0);
     copy_commit();
-    feed_early(1);
-    feed_late(0);
+    feed_early(1, 1);
+    feed_late(0, 0);
     copy_commit();
 
     if (!kSeqs && p.h0) h0_row = load_state<kCopy>(p.h0 + (size_t)row * D + c, mine);
     Here here{0, 0};
+    int stage = 0, last = 0;  // of the next tile to be formed, and to be finished
     auto form = [&](int k, Elements<kWrite>& e) -> Run {
         copy_wait<1>();
         __syncwarp();
         // into the stages of tiles k - 1 and k - 2, which every lane has read
-        feed_early(k + 2);
-        feed_late(k + 1);
+        const int second = stage == kStages - 1 ? 0 : stage + 1;
+        feed_early(k + 2, stage == 0 ? kStages - 1 : stage - 1);
+        feed_late(k + 1, second);
         copy_commit();
-        const char* s = early + k % kStages * R::kEarly;
+        const char* s = early + stage * R::kEarly;
+        stage = second;
         if constexpr (kSeqs) {
             const int first = first0 + k * stride;
-            e.m = find_marks(p.q, here, origin, dir, first, min(kSeg, L - first), lane);
+            e.m = find_marks(seqs, here, origin, dir, first, min(kSeg, L - first), lane);
         }
 #pragma unroll
         for (int i = 0; i < kSeg; ++i) {
@@ -147,13 +152,18 @@ scan_bwd_kernel(const BwdParams<IO, GT> p, const int cluster) {
             }
         }
         Run run{e.a[0], mul2(e.a[0], e.d[0])};
+        if (!kSeqs || !e.m.start) {
 #pragma unroll
-        for (int i = 1; i < kSeg; ++i) {
-            const F2 y = add2(e.d[i], run.H);
-            run.H = mul2(e.a[i], kSeqs ? pick2(e.m.start >> i & 1u, e.d[i], y) : y);
-            run.A = mul2(run.A, e.a[i]);
+            for (int i = 1; i < kSeg; ++i) {
+                run.H = mul2(e.a[i], add2(e.d[i], run.H));
+                run.A = mul2(run.A, e.a[i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 1; i < kSeg; ++i)
+                run.H = mul2(e.a[i], pick2(e.m.start >> i & 1u, e.d[i], add2(e.d[i], run.H)));
+            run.A = f2(kReset);
         }
-        if (kSeqs && e.m.start) run.A = f2(kReset);
         return run;
     };
 
@@ -164,24 +174,13 @@ scan_bwd_kernel(const BwdParams<IO, GT> p, const int cluster) {
             copy_wait<0>();
             __syncwarp();
         }
-        const char* s = late + k % kStages * R::kLate;
+        const char* s = late + last * R::kLate;
+        last = last == kStages - 1 ? 0 : last + 1;
         const int first = first0 + k * stride, n = L - first;
         long long at = out;
         out += hop;
-#pragma unroll
-        for (int i = 0; i < kSeg; ++i, at += next) {
-            const bool ends = kSeqs ? (e.m.end >> i & 1u) : first + i == L - 1;
-            const int q = !kSeqs ? row : ends ? __shfl_sync(0xffffffffu, e.m.seq, i) : 0;
-            const F2 sum = add2(e.d[i], mu);
-            const F2 lam = kSeqs ? pick2(e.m.start >> i & 1u, e.d[i], sum) : sum;
-            mu = mul2(e.a[i], lam);
-            if (i >= n) continue;
-            F2 hp = Rows<IO, kSeg>::read(s, i, lane);
-            if (ends) {
-                hp = h0_row;
-                if (kSeqs && p.h0) hp = load_state<kCopy>(p.h0 + (size_t)q * D + c, mine);
-                if (p.dh0) store_pair<float, kCopy>(p.dh0 + (size_t)q * D + c, mu, mine);
-            }
+        // the gradients of token i of the run, at element `at`, h of the token before being hp
+        auto element = [&](int i, F2 lam, F2 hp) {
             if constexpr (kWrite == GDR_WRITE_PLAIN) {
                 store_pair<IO, kCopy>(p.dv + at, lam, mine);
             } else {
@@ -196,6 +195,31 @@ scan_bwd_kernel(const BwdParams<IO, GT> p, const int cluster) {
                 }
             }
             store_pair<GT, kCopy>(p.dg + at, mul2(mu, hp), mine);
+        };
+        if (kSeqs ? n >= kSeg && !e.m.any() : n > kSeg) {  // no sequence ends here
+#pragma unroll
+            for (int i = 0; i < kSeg; ++i, at += next) {
+                const F2 lam = add2(e.d[i], mu);
+                mu = mul2(e.a[i], lam);
+                element(i, lam, Rows<IO, kSeg>::read(s, i, lane));
+            }
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < kSeg; ++i, at += next) {
+            const bool ends = kSeqs ? (e.m.end >> i & 1u) : first + i == L - 1;
+            const int q = !kSeqs ? row : ends ? __shfl_sync(0xffffffffu, e.m.seq, i) : 0;
+            const F2 sum = add2(e.d[i], mu);
+            const F2 lam = kSeqs ? pick2(e.m.start >> i & 1u, e.d[i], sum) : sum;
+            mu = mul2(e.a[i], lam);
+            if (i >= n) continue;
+            F2 hp = Rows<IO, kSeg>::read(s, i, lane);
+            if (ends) {
+                hp = h0_row;
+                if (kSeqs && p.h0) hp = load_state<kCopy>(p.h0 + (size_t)q * D + c, mine);
+                if (p.dh0) store_pair<float, kCopy>(p.dh0 + (size_t)q * D + c, mu, mine);
+            }
+            element(i, lam, hp);
         }
     };
     if constexpr (kCluster) {
@@ -233,7 +257,8 @@ gdr_status bwd_launch(const gdr_scan_args& a, const ScanPtrs& x, cudaStream_t st
     // 16 warps' rings fit an SM's shared memory in bf16 only
     constexpr int kWide = sizeof(IO) + sizeof(GT) == 4 ? 16 : 8;
     auto launch = [&](auto kernel, int warps, int threads, size_t shared) {
-        const size_t smem = (size_t)warps * Ring<IO, GT, kWrite>::kBytes + shared;
+        const size_t smem = (size_t)warps * Ring<IO, GT, kWrite>::kBytes + shared +
+                            (seqs ? kCuBytes : 0);
         return scan_launch(kernel, p, units, cluster ? cluster : 1, threads, smem, st);
     };
     if constexpr (kCopy != kCopyOne) {

@@ -402,11 +402,26 @@ __device__ __forceinline__ F2 load_state(const float* p, int left) {
 
 // ---- sequences of a row ------------------------------------------------------------------------
 
+// Bounds of up to this many sequences are kept in shared memory.
+constexpr int kCuShared = 1024;
+constexpr size_t kCuBytes = sizeof(int32_t) * (kCuShared + 32);
+
+// The call's sequences, with their bounds in shared memory if they fit.  All threads of the block.
+__device__ __forceinline__ Seqs share_cu(Seqs q, int32_t* room) {
+    if (q.cu && q.n <= kCuShared) {
+        for (int s = threadIdx.x; s <= q.n; s += blockDim.x) room[s] = q.cu[s];
+        q.cu = room;
+    }
+    __syncthreads();
+    return q;
+}
+
 // Which of a warp's tokens start or end a sequence, in the kernel's order, and (in lane i) the
 // sequence of token i.
 struct Marks {
     unsigned start, end;
     int seq;
+    __device__ __forceinline__ bool any() const { return (start | end) != 0; }
 };
 
 // The sequence met last, so that runs inside one sequence need no search.
