@@ -2,10 +2,12 @@
 //
 //     p_t = bias + sum_{j < W} w[W-1-j] x_{t-j},   y_t = act(p_t)
 //
-// A thread owns VEC neighbouring channels and walks a run of tokens with the last W inputs in
-// registers, so that every input is read once (and W - 1 more at the start of each run, which
-// the cache serves).  The activation is one exponential and one division per element; HBM bounds
-// all three kernels: 4 bytes per token and channel forward and 6 backward, in bf16.
+// A thread owns N neighbouring channels (8 bytes of a row) and walks a run of tokens with the last
+// W inputs in registers, so that every input is read once (and W - 1 more at the start of each
+// run, which the cache serves).  Tokens are loaded in batches, the next batch before one is used.
+// Channels go in pairs through packed fp32 arithmetic, and the activation costs one exponential
+// and one reciprocal: with an IEEE division the forward took 2.5 times as long as its bytes.  HBM
+// bounds all three kernels: 4 bytes per token and channel forward and 6 backward, in bf16.
 //
 // The backward forms p again from x.  dx_t gathers dp of the W - 1 tokens behind it, so a run
 // reads that far ahead; the gradients of weights and bias are summed over the run in registers,
@@ -29,7 +31,7 @@ struct ConvParams {
     int* status;
     Seqs q;
     int D, act, reverse;
-    int run;                  // tokens of a warp's run
+    int run, slabs;           // tokens of a warp's run, slabs of channels
 };
 
 // The tokens of one sequence in scan order: place 0 is its first token there.
@@ -46,116 +48,186 @@ __device__ __forceinline__ void run_places(const Span& sp, int t0, int t1, int& 
     i1 = sp.reverse ? sp.e - lo : hi - sp.b;
 }
 
-// x at place i of a sequence, from its state where i < 0
-template <typename IO, int W, int VEC>
-__device__ __forceinline__ void load_place(const ConvParams<IO>& p, const Span& sp, int s, int i,
-                                           int c, float (&f)[VEC]) {
+// N channels as they lie in memory.  kWhole: rows are whole vectors of N; else element by element,
+// `left` channels from the thread's first one on.
+template <typename IO, int N, bool kWhole>
+__device__ __forceinline__ Vec<IO, N> fetch(const IO* p, int left) {
+    if constexpr (kWhole) return load_vec<IO, N>(p);
+    Vec<IO, N> v;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) f[j] = 0.f;
-    if (i >= 0) load_f<IO, VEC>(p.x + (size_t)sp.token(i) * p.D + c, f);
-    else if (p.state) load_f<IO, VEC>(p.state + ((size_t)s * (W - 1) + (W - 1 + i)) * p.D + c, f);
+    for (int j = 0; j < N; ++j) v.x[j] = j < left ? p[j] : from_f<IO>(0.f);
+    return v;
+}
+template <typename IO, int N, bool kWhole>
+__device__ __forceinline__ void put(IO* p, const F2 (&f)[N / 2], int left) {
+    Vec<IO, N> v;
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) set_pair(v, j, f[j]);
+    if constexpr (kWhole) {
+        store_raw(p, v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (j < left) p[j] = v.x[j];
+    }
+}
+template <typename IO, int N>
+__device__ __forceinline__ void pairs(const Vec<IO, N>& v, F2 (&f)[N / 2]) {
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) f[j] = pair_of(v, j);
 }
 
-template <int W, int VEC>
-__device__ __forceinline__ void load_weights(const float* w, const float* bias, int c,
-                                             float (&wr)[W][VEC], float (&br)[VEC]) {
+// x at place i of a sequence, from its state where i < 0
+template <typename IO, int W, int N, bool kWhole>
+__device__ __forceinline__ void fetch_place(const ConvParams<IO>& p, const Span& sp, int s, int i,
+                                            int c, F2 (&f)[N / 2]) {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
+    for (int j = 0; j < N / 2; ++j) f[j] = f2(0.f);
+    if (i >= 0)
+        pairs(fetch<IO, N, kWhole>(p.x + (size_t)sp.token(i) * p.D + c, p.D - c), f);
+    else if (p.state)
+        pairs(fetch<IO, N, kWhole>(p.state + ((size_t)s * (W - 1) + (W - 1 + i)) * p.D + c, p.D - c), f);
+}
+
+template <int W, int N>
+__device__ __forceinline__ void load_weights(const float* w, const float* bias, int c, int D,
+                                             F2 (&wr)[W][N / 2], F2 (&br)[N / 2]) {
+    auto at = [&](int ch, int k) { return ch < D ? __ldg(w + (size_t)ch * W + k) : 0.f; };
+    auto b = [&](int ch) { return bias && ch < D ? __ldg(bias + ch) : 0.f; };
 #pragma unroll
-        for (int k = 0; k < W; ++k) wr[k][j] = __ldg(w + (size_t)(c + j) * W + k);
-        br[j] = bias ? __ldg(bias + c + j) : 0.f;
+    for (int j = 0; j < N / 2; ++j) {
+#pragma unroll
+        for (int k = 0; k < W; ++k) wr[k][j] = f2(at(c + 2 * j, k), at(c + 2 * j + 1, k));
+        br[j] = f2(b(c + 2 * j), b(c + 2 * j + 1));
     }
 }
 
-template <typename IO, int W, int VEC>
+// The block's warp and slab: slabs vary fastest, so that blocks that run together read whole rows.
+struct Where {
+    long long warp, warps, tokens_block;
+    int slab;
+    __device__ __forceinline__ Where(int slabs, int wid) {
+        tokens_block = blockIdx.x / slabs;
+        slab = blockIdx.x % slabs;
+        warp = tokens_block * kConvWarps + wid;
+        warps = (long long)(gridDim.x / slabs) * kConvWarps;
+    }
+};
+
+template <typename IO, int W, int N, bool kWhole>
 __global__ void __launch_bounds__(kConvThreads)
 conv_fwd_kernel(const ConvParams<IO> p) {
+    constexpr int P = N / 2, kBatch = 8;
     const int lane = threadIdx.x, wid = threadIdx.y;
-    const int c = (blockIdx.y * 32 + lane) * VEC;
-    if (blockIdx.x == 0 && blockIdx.y == 0)
-        check_cu(p.q, p.status, wid * 32 + lane, kConvThreads);
-    if (c >= p.D) return;
-    const long long warp = (long long)blockIdx.x * kConvWarps + wid;
-    const long long warps = (long long)gridDim.x * kConvWarps;
+    const Where me(p.slabs, wid);
+    const int c = (me.slab * 32 + lane) * N, left = p.D - c;
+    if (blockIdx.x == 0) check_cu(p.q, p.status, wid * 32 + lane, kConvThreads);
+    if (left <= 0) return;
 
     if (p.state_out) {  // the last W - 1 inputs of every sequence
-        for (long long s = warp; s < p.q.n; s += warps) {
+        for (long long s = me.warp; s < p.q.n; s += me.warps) {
             const Span sp{p.q.begin((int)s), p.q.end((int)s), p.reverse};
             const int len = max(sp.e - sp.b, 0);
 #pragma unroll
             for (int k = 0; k < W - 1; ++k) {
-                float f[VEC];
-                load_place<IO, W, VEC>(p, sp, (int)s, len - (W - 1) + k, c, f);
-                store_vec<IO, VEC>(p.state_out + ((size_t)s * (W - 1) + k) * p.D + c, f);
+                F2 f[P];
+                fetch_place<IO, W, N, kWhole>(p, sp, (int)s, len - (W - 1) + k, c, f);
+                put<IO, N, kWhole>(p.state_out + ((size_t)s * (W - 1) + k) * p.D + c, f, left);
             }
         }
     }
-    const long long first = warp * p.run;
+    const long long first = me.warp * p.run;
     if (first >= p.q.total) return;
     const int t0 = (int)first, t1 = (int)min((long long)p.q.total, first + p.run);
 
-    float w[W][VEC], bias[VEC];
-    load_weights<W, VEC>(p.w, p.bias, c, w, bias);
+    F2 w[W][P], bias[P];
+    load_weights<W, N>(p.w, p.bias, c, p.D, w, bias);
+    const long long hop = p.reverse ? -(long long)p.D : p.D;
     for (int s = p.q.of(t0); s < p.q.n; ++s) {
         const Span sp{p.q.begin(s), p.q.end(s), p.reverse};
         if (sp.b >= t1) break;
         int i0, i1;
         run_places(sp, t0, t1, i0, i1);
         if (i0 >= i1) continue;
-        float x[W][VEC];  // x[k]: place i - (W - 1) + k
+        F2 x[W - 1][P];  // places i - (W - 1) .. i - 1
 #pragma unroll
-        for (int k = 1; k < W; ++k)
-            load_place<IO, W, VEC>(p, sp, s, i0 - W + k, c, x[k]);
-#pragma unroll 4
-        for (int i = i0; i < i1; ++i) {
-            const size_t at = (size_t)sp.token(i) * p.D + c;
+        for (int k = 0; k < W - 1; ++k)
+            fetch_place<IO, W, N, kWhole>(p, sp, s, i0 - (W - 1) + k, c, x[k]);
+        const IO* in = p.x + (size_t)sp.token(i0) * p.D + c;
+        IO* out = p.y + (size_t)sp.token(i0) * p.D + c;
+        auto step = [&](const Vec<IO, N>& v) {
+            F2 now[P], y[P];
+            pairs(v, now);
 #pragma unroll
-            for (int k = 0; k + 1 < W; ++k) {
+            for (int j = 0; j < P; ++j) {
+                F2 a = fma2(w[W - 1][j], now[j], bias[j]);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) x[k][j] = x[k + 1][j];
+                for (int k = 0; k < W - 1; ++k) a = fma2(w[k][j], x[k][j], a);
+                y[j] = act2(a, p.act);
+#pragma unroll
+                for (int k = 0; k < W - 2; ++k) x[k][j] = x[k + 1][j];
+                x[W - 2][j] = now[j];
             }
-            load_f<IO, VEC>(p.x + at, x[W - 1]);
-            float y[VEC];
+            put<IO, N, kWhole>(out, y, left);
+            out += hop;
+        };
+        int i = i0;
+        if (i + kBatch <= i1) {
+            Vec<IO, N> next[kBatch];
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                float a = bias[j];
+            for (int u = 0; u < kBatch; ++u) next[u] = fetch<IO, N, kWhole>(in + u * hop, left);
+            for (; i + kBatch <= i1; i += kBatch) {
+                Vec<IO, N> now[kBatch];
 #pragma unroll
-                for (int k = 0; k < W; ++k) a = fmaf(w[k][j], x[k][j], a);
-                y[j] = act_f(a, p.act);
+                for (int u = 0; u < kBatch; ++u) now[u] = next[u];
+                in += kBatch * hop;
+                if (i + 2 * kBatch <= i1) {
+#pragma unroll
+                    for (int u = 0; u < kBatch; ++u) next[u] = fetch<IO, N, kWhole>(in + u * hop, left);
+                }
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) step(now[u]);
             }
-            store_vec<IO, VEC>(p.y + at, y);
         }
+        for (; i < i1; ++i, in += hop) step(fetch<IO, N, kWhole>(in, left));
     }
 }
 
-template <typename IO, int W, int VEC>
+template <typename IO, int W, int N, bool kWhole>
 __global__ void __launch_bounds__(kConvThreads)
 conv_bwd_kernel(const ConvParams<IO> p) {
-    __shared__ float sh[kConvWarps][32 * VEC];
+    constexpr int P = N / 2, kBatch = 4;
+    __shared__ float sh[kConvWarps][32 * N];
     const int lane = threadIdx.x, wid = threadIdx.y;
-    const int c = (blockIdx.y * 32 + lane) * VEC;
-    const bool on = c < p.D;
-    if (blockIdx.x == 0 && blockIdx.y == 0)
-        check_cu(p.q, p.status, wid * 32 + lane, kConvThreads);
-    const long long warp = (long long)blockIdx.x * kConvWarps + wid;
-    const long long warps = (long long)gridDim.x * kConvWarps;
-    if (p.dstate && on) {  // nothing reads an empty sequence's state
-        for (long long s = warp; s < p.q.n; s += warps) {
+    const Where me(p.slabs, wid);
+    const int c = (me.slab * 32 + lane) * N, left = p.D - c;
+    if (blockIdx.x == 0) check_cu(p.q, p.status, wid * 32 + lane, kConvThreads);
+    if (p.dstate && left > 0) {  // nothing reads an empty sequence's state
+        for (long long s = me.warp; s < p.q.n; s += me.warps) {
             if (p.q.begin((int)s) < p.q.end((int)s)) continue;
-            const float z[VEC] = {};
+            F2 z[P];
+#pragma unroll
+            for (int j = 0; j < P; ++j) z[j] = f2(0.f);
 #pragma unroll
             for (int k = 0; k < W - 1; ++k)
-                store_vec<IO, VEC>(p.dstate + ((size_t)s * (W - 1) + k) * p.D + c, z);
+                put<IO, N, kWhole>(p.dstate + ((size_t)s * (W - 1) + k) * p.D + c, z, left);
         }
     }
-    const long long first = warp * p.run;
+    const long long first = me.warp * p.run;
     const int t0 = (int)min((long long)p.q.total, first);
     const int t1 = (int)min((long long)p.q.total, first + p.run);
 
-    float dw[W][VEC] = {}, db[VEC] = {};
-    if (on && t0 < t1) {
-        float w[W][VEC], bias[VEC];
-        load_weights<W, VEC>(p.w, p.bias, c, w, bias);
+    F2 dw[W][P], db[P];
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+        db[j] = f2(0.f);
+#pragma unroll
+        for (int k = 0; k < W; ++k) dw[k][j] = f2(0.f);
+    }
+    if (left > 0 && t0 < t1) {
+        F2 w[W][P], bias[P];
+        load_weights<W, N>(p.w, p.bias, c, p.D, w, bias);
+        const long long hop = p.reverse ? -(long long)p.D : p.D;
         for (int s = p.q.of(t0); s < p.q.n; ++s) {
             const Span sp{p.q.begin(s), p.q.end(s), p.reverse};
             if (sp.b >= t1) break;
@@ -163,81 +235,114 @@ conv_bwd_kernel(const ConvParams<IO> p) {
             run_places(sp, t0, t1, i0, i1);
             if (i0 >= i1) continue;
             const int len = sp.e - sp.b;
-            float x[W][VEC], dp[W][VEC];  // places i - (W - 1) .. i
+            F2 x[W - 1][P], dp[W - 1][P];  // places i - (W - 1) .. i - 1
 #pragma unroll
-            for (int k = 1; k < W; ++k) {
-                load_place<IO, W, VEC>(p, sp, s, i0 - W + k, c, x[k]);
+            for (int k = 0; k < W - 1; ++k) {
+                fetch_place<IO, W, N, kWhole>(p, sp, s, i0 - (W - 1) + k, c, x[k]);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) dp[k][j] = 0.f;
+                for (int j = 0; j < P; ++j) dp[k][j] = f2(0.f);
             }
-            // each step brings dp of place i in and dx of place i - (W - 1) out: places ahead
-            // of the run's end complete its last tokens, zeros behind the sequence's
-            const int first_out = i0 == 0 ? -(W - 1) : i0;
-#pragma unroll 2
-            for (int i = i0; i < i1 + W - 1; ++i) {
+            // A step brings dp of place i in and dx of place i - (W - 1) out; `own`: the run's
+            // token, which counts for dw and db; past: behind the sequence's end, where dp is zero.
+            F2 dx[P];
+            auto step = [&](const Vec<IO, N>& vx, const Vec<IO, N>& vdy, bool own, bool past) {
+                F2 xi[P], d[P];
+                pairs(vx, xi);
+                pairs(vdy, d);
 #pragma unroll
-                for (int k = 0; k + 1 < W; ++k) {
+                for (int j = 0; j < P; ++j) {
+                    F2 a = fma2(w[W - 1][j], xi[j], bias[j]), v, g;
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) { x[k][j] = x[k + 1][j]; dp[k][j] = dp[k + 1][j]; }
-                }
-                if (i < len) {
-                    const size_t at = (size_t)sp.token(i) * p.D + c;
-                    float dy[VEC];
-                    load_f<IO, VEC>(p.x + at, x[W - 1]);
-                    load_f<IO, VEC>(p.dy + at, dy);
+                    for (int k = 0; k < W - 1; ++k) a = fma2(w[k][j], x[k][j], a);
+                    act2_both(a, p.act, v, g);
+                    d[j] = past ? f2(0.f) : mul2(d[j], g);
+                    if (own) {
+                        db[j] = add2(db[j], d[j]);
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        float a = bias[j], v, d;
-#pragma unroll
-                        for (int k = 0; k < W; ++k) a = fmaf(w[k][j], x[k][j], a);
-                        act_both(a, p.act, v, d);
-                        dp[W - 1][j] = dy[j] * d;
+                        for (int k = 0; k < W - 1; ++k) dw[k][j] = fma2(d[j], x[k][j], dw[k][j]);
+                        dw[W - 1][j] = fma2(d[j], xi[j], dw[W - 1][j]);
                     }
-                    if (i < i1) {
+                    // dx_out = sum_k w[W-1-k] dp_{out + k}
+                    F2 sum = mul2(w[0][j], d[j]);
 #pragma unroll
-                        for (int j = 0; j < VEC; ++j) {
-                            db[j] += dp[W - 1][j];
+                    for (int k = 0; k < W - 1; ++k) sum = fma2(w[W - 1 - k][j], dp[k][j], sum);
+                    dx[j] = sum;
 #pragma unroll
-                            for (int k = 0; k < W; ++k) dw[k][j] = fmaf(dp[W - 1][j], x[k][j], dw[k][j]);
+                    for (int k = 0; k < W - 2; ++k) { x[k][j] = x[k + 1][j]; dp[k][j] = dp[k + 1][j]; }
+                    x[W - 2][j] = xi[j];
+                    dp[W - 2][j] = d[j];
+                }
+            };
+            auto any = [&](int i) {
+                const bool past = i >= len;
+                Vec<IO, N> vx{}, vdy{};
+                if (!past) {
+                    const size_t at = (size_t)sp.token(i) * p.D + c;
+                    vx = fetch<IO, N, kWhole>(p.x + at, left);
+                    vdy = fetch<IO, N, kWhole>(p.dy + at, left);
+                }
+                step(vx, vdy, i < i1, past);
+                const int out = i - (W - 1);
+                if (out < i0 && i0 > 0) return;  // another run's
+                if (out >= 0)
+                    put<IO, N, kWhole>(p.dx + (size_t)sp.token(out) * p.D + c, dx, left);
+                else if (p.dstate)
+                    put<IO, N, kWhole>(p.dstate + ((size_t)s * (W - 1) + (W - 1 + out)) * p.D + c, dx, left);
+            };
+            int i = i0;
+            for (; i < min(i0 + W - 1, i1); ++i) any(i);
+            if (i + kBatch <= i1) {  // the run's own tokens, dx of its own tokens
+                const size_t at = (size_t)sp.token(i) * p.D + c;
+                const IO *ix = p.x + at, *idy = p.dy + at;
+                IO* out = p.dx + (size_t)sp.token(i - (W - 1)) * p.D + c;
+                Vec<IO, N> nx[kBatch], ny[kBatch];
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    nx[u] = fetch<IO, N, kWhole>(ix + u * hop, left);
+                    ny[u] = fetch<IO, N, kWhole>(idy + u * hop, left);
+                }
+                for (; i + kBatch <= i1; i += kBatch) {
+                    Vec<IO, N> cx[kBatch], cy[kBatch];
+#pragma unroll
+                    for (int u = 0; u < kBatch; ++u) { cx[u] = nx[u]; cy[u] = ny[u]; }
+                    ix += kBatch * hop;
+                    idy += kBatch * hop;
+                    if (i + 2 * kBatch <= i1) {
+#pragma unroll
+                        for (int u = 0; u < kBatch; ++u) {
+                            nx[u] = fetch<IO, N, kWhole>(ix + u * hop, left);
+                            ny[u] = fetch<IO, N, kWhole>(idy + u * hop, left);
                         }
                     }
-                } else {
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) dp[W - 1][j] = 0.f;
+                    for (int u = 0; u < kBatch; ++u) {
+                        step(cx[u], cy[u], true, false);
+                        put<IO, N, kWhole>(out, dx, left);
+                        out += hop;
+                    }
                 }
-                const int out = i - (W - 1);
-                if (out < first_out) continue;
-                float dx[VEC];
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    dx[j] = 0.f;  // dx_out = sum_j w[W-1-j] dp_{out + j}
-#pragma unroll
-                    for (int k = 0; k < W; ++k) dx[j] = fmaf(w[W - 1 - k][j], dp[k][j], dx[j]);
-                }
-                if (out >= 0) store_vec<IO, VEC>(p.dx + (size_t)sp.token(out) * p.D + c, dx);
-                else if (p.dstate)
-                    store_vec<IO, VEC>(p.dstate + ((size_t)s * (W - 1) + (W - 1 + out)) * p.D + c, dx);
             }
+            for (; i < i1 + W - 1; ++i) any(i);
         }
     }
     // the block's runs, then one row of partial sums a block
+#pragma unroll
     for (int k = 0; k <= W; ++k) {
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            float v = db[j];
-#pragma unroll
-            for (int kk = 0; kk < W; ++kk) v = kk == k ? dw[kk][j] : v;
-            sh[wid][lane * VEC + j] = v;
+        for (int j = 0; j < P; ++j) {
+            const F2 v = k < W ? dw[k < W ? k : 0][j] : db[j];
+            sh[wid][lane * N + 2 * j] = v.lo();
+            sh[wid][lane * N + 2 * j + 1] = v.hi();
         }
         __syncthreads();
-        for (int i = wid * 32 + lane; i < 32 * VEC; i += kConvThreads) {
-            const int ch = blockIdx.y * 32 * VEC + i;
+        for (int i = wid * 32 + lane; i < 32 * N; i += kConvThreads) {
+            const int ch = me.slab * 32 * N + i;
             if (ch >= p.D) break;
             float v = 0.f;
 #pragma unroll
             for (int g = 0; g < kConvWarps; ++g) v += sh[g][i];
-            p.part[((size_t)blockIdx.x * (W + 1) + k) * p.D + ch] = v;
+            p.part[((size_t)me.tokens_block * (W + 1) + k) * p.D + ch] = v;
         }
     }
 }
@@ -262,80 +367,77 @@ conv_reduce_kernel(const float* __restrict__ part, int rows, int D, float* __res
     else if (dbias) dbias[c] = v;
 }
 
-template <typename IO, int W, int VEC>
+template <typename IO, int W, int N, bool kWhole>
 __global__ void __launch_bounds__(128)
 conv_step_kernel(const IO* __restrict__ x, const float* __restrict__ w,
                  const float* __restrict__ bias, const IO* state, IO* state_out,
                  IO* __restrict__ y, int D, int act) {
-    const int c = (blockIdx.x * 128 + threadIdx.x) * VEC;
-    if (c >= D) return;
-    const size_t n = blockIdx.y + (size_t)blockIdx.z * gridDim.y;
-    float win[W][VEC], wr[W][VEC], b[VEC], out[VEC];
+    constexpr int P = N / 2;
+    const int c = (blockIdx.x * 128 + threadIdx.x) * N, left = D - c;
+    if (left <= 0) return;
+    const size_t n = blockIdx.y;
     const IO* st = state + n * (W - 1) * D + c;
-    // the state may be updated in place: all of it is read before any of it is written
+    // the state may be updated in place: all of it is read before any of it is written, and not
+    // through the read-only path
+    F2 win[W][P], wr[W][P], b[P];
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) {
+        Vec<IO, N> v;
+        if constexpr (kWhole) {
+            using R = typename RawOf<sizeof(IO) * N>::T;
+            const R r = *reinterpret_cast<const R*>(st + (size_t)k * D);
+            memcpy(&v, &r, sizeof(R));
+        } else {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) win[k][j] = 0.f;
-        Vec<IO, VEC> v;
-        using R = typename RawOf<sizeof(IO) * VEC>::T;
-        const R r = *reinterpret_cast<const R*>(st + (size_t)k * D);
-        memcpy(&v, &r, sizeof(R));
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) win[k][j] = to_f(v.x[j]);
+            for (int j = 0; j < N; ++j) v.x[j] = j < left ? st[(size_t)k * D + j] : from_f<IO>(0.f);
+        }
+        pairs(v, win[k]);
     }
-    load_f<IO, VEC>(x + n * D + c, win[W - 1]);
-    load_weights<W, VEC>(w, bias, c, wr, b);
+    pairs(fetch<IO, N, kWhole>(x + n * D + c, left), win[W - 1]);
+    load_weights<W, N>(w, bias, c, D, wr, b);
+    F2 out[P];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-        float a = b[j];
+    for (int j = 0; j < P; ++j) {
+        F2 a = fma2(wr[W - 1][j], win[W - 1][j], b[j]);
 #pragma unroll
-        for (int k = 0; k < W; ++k) a = fmaf(wr[k][j], win[k][j], a);
-        out[j] = act_f(a, act);
+        for (int k = 0; k < W - 1; ++k) a = fma2(wr[k][j], win[k][j], a);
+        out[j] = act2(a, act);
     }
-    store_vec<IO, VEC>(y + n * D + c, out);
+    put<IO, N, kWhole>(y + n * D + c, out, left);
     IO* so = state_out + n * (W - 1) * D + c;
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) store_vec<IO, VEC>(so + (size_t)k * D, win[k + 1]);
+    for (int k = 0; k < W - 1; ++k) put<IO, N, kWhole>(so + (size_t)k * D, win[k + 1], left);
 }
 
 // ---- launching ---------------------------------------------------------------------------------
 
-// Channels of a thread: 8 bytes where rows are whole 8-byte words, else one element.
-int conv_vec(const gdr_conv_args& a) {
-    const int v = a.io_dtype == GDR_BF16 ? 4 : 2;
-    return a.D % v ? 1 : v;
-}
-
-// Tokens of a warp's run: long enough that the W - 1 extra tokens read at its ends cost little,
-// short enough that the warps fill the GPU.
-int conv_run(const gdr_conv_args& a, int vec, int most) {
-    const long long slabs = (a.D + 32 * vec - 1) / (32 * vec);
-    const long long tokens = (long long)a.B * a.T;
-    long long run = tokens * slabs / (148 * 32);
-    return (int)(run < 8 ? 8 : run > most ? most : run);
-}
+// Channels of a thread: four where rows are whole vectors of four, else two.
+int conv_channels(const gdr_conv_args& a) { return a.D % 4 ? 2 : 4; }
 
 struct ConvGrid {
-    int vec, run;
-    unsigned blocks, slabs;
+    int run;                 // tokens of a warp's run
+    unsigned slabs, blocks;  // blocks over the tokens
 };
 
-ConvGrid conv_grid(const gdr_conv_args& a, int most) {
+// A run is long enough that the W - 1 extra tokens read at its ends cost little, and short enough
+// that `warps` of them fill the GPU.
+ConvGrid conv_grid(const gdr_conv_args& a, int warps, int most) {
     ConvGrid g;
-    g.vec = conv_vec(a);
-    g.run = conv_run(a, g.vec, most);
+    const int per_slab = 32 * conv_channels(a);
+    const long long tokens = (long long)a.B * a.T;
+    g.slabs = (unsigned)((a.D + per_slab - 1) / per_slab);
+    const long long run = (tokens * g.slabs + warps - 1) / warps;
+    g.run = (int)(run < 8 ? 8 : run > most ? most : run);
     const long long per = (long long)g.run * kConvWarps;
-    g.blocks = (unsigned)(((long long)a.B * a.T + per - 1) / per);
+    g.blocks = (unsigned)((tokens + per - 1) / per);
     if (g.blocks == 0) g.blocks = 1;
-    g.slabs = (unsigned)((a.D + 32 * g.vec - 1) / (32 * g.vec));
     return g;
 }
-
-constexpr int kFwdRun = 64, kBwdRun = 256;
+ConvGrid fwd_grid(const gdr_conv_args& a) { return conv_grid(a, 148 * 32, 64); }
+ConvGrid bwd_grid(const gdr_conv_args& a) { return conv_grid(a, 148 * 16, 256); }
 
 template <typename IO>
-ConvParams<IO> conv_params(const gdr_conv_args& a, const ConvPtrs& x, int run) {
+ConvParams<IO> conv_params(const gdr_conv_args& a, const ConvPtrs& x, const ConvGrid& g) {
     ConvParams<IO> p;
     p.x = static_cast<const IO*>(x.x);
     p.state = static_cast<const IO*>(x.state);
@@ -352,38 +454,39 @@ ConvParams<IO> conv_params(const gdr_conv_args& a, const ConvPtrs& x, int run) {
     p.D = a.D;
     p.act = a.activation;
     p.reverse = a.reverse;
-    p.run = run;
+    p.run = g.run;
+    p.slabs = (int)g.slabs;
     return p;
 }
 
 struct ConvFwd {
-    template <typename IO, int W, int VEC>
+    template <typename IO, int W, int N, bool kWhole>
     static void go(const gdr_conv_args& a, const ConvPtrs& x, cudaStream_t st) {
-        const ConvGrid g = conv_grid(a, kFwdRun);
-        conv_fwd_kernel<IO, W, VEC><<<dim3(g.blocks, g.slabs), dim3(32, kConvWarps), 0, st>>>(
-            conv_params<IO>(a, x, g.run));
+        const ConvGrid g = fwd_grid(a);
+        conv_fwd_kernel<IO, W, N, kWhole><<<g.blocks * g.slabs, dim3(32, kConvWarps), 0, st>>>(
+            conv_params<IO>(a, x, g));
     }
 };
 
 struct ConvBwd {
-    template <typename IO, int W, int VEC>
+    template <typename IO, int W, int N, bool kWhole>
     static void go(const gdr_conv_args& a, const ConvPtrs& x, cudaStream_t st) {
-        const ConvGrid g = conv_grid(a, kBwdRun);
-        conv_bwd_kernel<IO, W, VEC><<<dim3(g.blocks, g.slabs), dim3(32, kConvWarps), 0, st>>>(
-            conv_params<IO>(a, x, g.run));
+        const ConvGrid g = bwd_grid(a);
+        conv_bwd_kernel<IO, W, N, kWhole><<<g.blocks * g.slabs, dim3(32, kConvWarps), 0, st>>>(
+            conv_params<IO>(a, x, g));
         conv_reduce_kernel<W><<<dim3((a.D + 31) / 32, W + 1), 256, 0, st>>>(
             x.ws, (int)g.blocks, a.D, x.dw, x.dbias);
     }
 };
 
 struct ConvStep {
-    template <typename IO, int W, int VEC>
+    template <typename IO, int W, int N, bool kWhole>
     static void go(const gdr_conv_args& a, const ConvPtrs& x, cudaStream_t st) {
-        const unsigned bx = (unsigned)((a.D + 128 * VEC - 1) / (128 * VEC));
+        const unsigned bx = (unsigned)((a.D + 128 * N - 1) / (128 * N));
         for (int n0 = 0; n0 < a.B; n0 += 65535) {  // a grid's second dimension ends at 65535
             const int n = a.B - n0 < 65535 ? a.B - n0 : 65535;
             const size_t row = (size_t)n0 * a.D, srow = row * (W - 1);
-            conv_step_kernel<IO, W, VEC><<<dim3(bx, n), 128, 0, st>>>(
+            conv_step_kernel<IO, W, N, kWhole><<<dim3(bx, n), 128, 0, st>>>(
                 static_cast<const IO*>(x.x) + row, x.w, x.bias,
                 static_cast<const IO*>(x.state) + srow, static_cast<IO*>(x.state_out) + srow,
                 static_cast<IO*>(x.y) + row, a.D, a.activation);
@@ -391,32 +494,33 @@ struct ConvStep {
     }
 };
 
-template <typename Op, typename IO, int VEC>
+template <typename Op, typename IO, int W>
+void conv_vectors(const gdr_conv_args& a, const ConvPtrs& x, cudaStream_t st) {
+    if (a.D % 4 == 0) Op::template go<IO, W, 4, true>(a, x, st);
+    else if (a.D % 2 == 0) Op::template go<IO, W, 2, true>(a, x, st);
+    else Op::template go<IO, W, 2, false>(a, x, st);
+}
+
+template <typename Op, typename IO>
 void conv_width(const gdr_conv_args& a, const ConvPtrs& x, cudaStream_t st) {
     switch (a.width) {
-        case 2: Op::template go<IO, 2, VEC>(a, x, st); break;
-        case 3: Op::template go<IO, 3, VEC>(a, x, st); break;
-        default: Op::template go<IO, 4, VEC>(a, x, st);
+        case 2: conv_vectors<Op, IO, 2>(a, x, st); break;
+        case 3: conv_vectors<Op, IO, 3>(a, x, st); break;
+        default: conv_vectors<Op, IO, 4>(a, x, st);
     }
 }
 
 template <typename Op>
 gdr_status conv_dispatch(const gdr_conv_args& a, const ConvPtrs& x, cudaStream_t st) {
-    const bool one = conv_vec(a) == 1;
-    if (a.io_dtype == GDR_BF16) {
-        if (one) conv_width<Op, __nv_bfloat16, 1>(a, x, st);
-        else conv_width<Op, __nv_bfloat16, 4>(a, x, st);
-    } else {
-        if (one) conv_width<Op, float, 1>(a, x, st);
-        else conv_width<Op, float, 2>(a, x, st);
-    }
+    if (a.io_dtype == GDR_BF16) conv_width<Op, __nv_bfloat16>(a, x, st);
+    else conv_width<Op, float>(a, x, st);
     return cudaGetLastError() == cudaSuccess ? GDR_OK : GDR_ERR_CUDA;
 }
 
 }  // namespace
 
 size_t conv_bwd_workspace(const gdr_conv_args& a) {
-    const ConvGrid g = conv_grid(a, kBwdRun);
+    const ConvGrid g = bwd_grid(a);
     return align_up(sizeof(float) * (size_t)g.blocks * (a.width + 1) * a.D, 256);
 }
 

@@ -3,8 +3,11 @@
 #pragma once
 
 #include "common.cuh"
+#include "tc_ptx.cuh"
 
 namespace gdr {
+
+using tc::ex2;
 
 // ---- sequences ------------------------------------------------------------------------------
 // The tokens of a call lie on one axis of `total` rows: B rows of T tokens one after the other,
@@ -93,26 +96,121 @@ __device__ __forceinline__ void load_f(const E* p, float (&f)[N]) {
     for (int i = 0; i < N; ++i) f[i] = to_f(v.x[i]);
 }
 
-// ---- activations -------------------------------------------------------------------------------
-// sigmoid from the side that does not overflow: e^-|x| is in (0, 1].
-__device__ __forceinline__ float sigmoid_f(float x) {
-    const float e = expf(-fabsf(x));
-    const float r = 1.f / (1.f + e);
-    return x >= 0.f ? r : e * r;
+// ---- two channels in one 64-bit register pair ---------------------------------------------------
+struct F2 {
+    uint64_t v;
+    __device__ __forceinline__ float lo() const { return __uint_as_float((uint32_t)v); }
+    __device__ __forceinline__ float hi() const { return __uint_as_float((uint32_t)(v >> 32)); }
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ F2 f2(float x) { return f2(x, x); }
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 pick2(bool c, F2 a, F2 b) { return F2{c ? a.v : b.v}; }
+
+// max that lets NaN through
+__device__ __forceinline__ float max_nan(float x, float y) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
 }
 
-__device__ __forceinline__ float act_f(float x, int act) {
+__device__ __forceinline__ float min_nan(float x, float y) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float rcp_ftz(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// e^x = 2^(x log2 e).  The product is rounded; what the rounding left out, e, and the low part of
+// log2 e multiply the result by 2^e = 1 + e ln 2 to first order (e is below 2^-16 in the range).
+// x has to be finite, and below 88.
+__device__ __forceinline__ F2 exp_in_range(F2 x) {
+    const F2 t = mul2(x, f2(1.44269504f));
+    F2 e = fma2(x, f2(-1.44269504f), t);  // -e
+    e = fma2(x, f2(-1.92596303e-8f), e);
+    const F2 m = f2(ex2(t.lo()), ex2(t.hi()));
+    return fma2(mul2(m, e), f2(-0.693147181f), m);
+}
+
+// e^g for g <= 0 and above as far as it stays finite.  Below e^-150 the result is zero in either
+// case, and the clamp keeps -inf out of the products.
+__device__ __forceinline__ F2 exp2ch(F2 g) {
+    return exp_in_range(f2(max_nan(g.lo(), -150.f), max_nan(g.hi(), -150.f)));
+}
+
+// ---- activations -------------------------------------------------------------------------------
+// sigmoid(x) = 1 / (1 + e^-x).  At the lower clamp e^-x is above 2^126, whose reciprocal the
+// hardware flushes to zero: so it is for all x below, and x sigmoid(x) is -0 (NaN for -inf, as
+// -inf times 0 is).  Exponential and reciprocal are off by one step of fp32 each.
+__device__ __forceinline__ F2 sigmoid2(F2 x) {
+    const F2 c = f2(min_nan(max_nan(-x.lo(), -88.f), 87.7f), min_nan(max_nan(-x.hi(), -88.f), 87.7f));
+    const F2 s = add2(exp_in_range(c), f2(1.f));
+    return f2(rcp_ftz(s.lo()), rcp_ftz(s.hi()));
+}
+
+__device__ __forceinline__ F2 act2(F2 x, int act) {
     if (act == GDR_ACT_NONE) return x;
-    const float s = sigmoid_f(x);
-    return act == GDR_ACT_SILU ? x * s : s;
+    const F2 s = sigmoid2(x);
+    return act == GDR_ACT_SILU ? mul2(x, s) : s;
 }
 
 // act(x) and act'(x)
-__device__ __forceinline__ void act_both(float x, int act, float& a, float& d) {
-    if (act == GDR_ACT_NONE) { a = x; d = 1.f; return; }
-    const float s = sigmoid_f(x);
-    if (act == GDR_ACT_SILU) { a = x * s; d = s * (1.f + x * (1.f - s)); }
-    else { a = s; d = s * (1.f - s); }
+__device__ __forceinline__ void act2_both(F2 x, int act, F2& a, F2& d) {
+    if (act == GDR_ACT_NONE) { a = x; d = f2(1.f); return; }
+    const F2 s = sigmoid2(x), rest = fma2(s, f2(-1.f), f2(1.f));
+    if (act == GDR_ACT_SILU) {
+        a = mul2(x, s);
+        d = mul2(s, fma2(x, rest, f2(1.f)));
+    } else {
+        a = s;
+        d = mul2(s, rest);
+    }
+}
+
+// The pair at word i of N neighbouring elements, and the way back.
+template <typename E, int N>
+__device__ __forceinline__ F2 pair_of(const Vec<E, N>& v, int i) {
+    if constexpr (sizeof(E) == 2) {
+        uint32_t r;
+        memcpy(&r, &v.x[2 * i], 4);
+        return f2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
+    } else {
+        return f2(v.x[2 * i], v.x[2 * i + 1]);
+    }
+}
+template <typename E, int N>
+__device__ __forceinline__ void set_pair(Vec<E, N>& v, int i, F2 f) {
+    v.x[2 * i] = from_f<E>(f.lo());
+    v.x[2 * i + 1] = from_f<E>(f.hi());
+}
+template <typename E, int N>
+__device__ __forceinline__ void store_raw(E* p, const Vec<E, N>& v) {
+    using R = typename RawOf<sizeof(E) * N>::T;
+    R r;
+    memcpy(&r, &v, sizeof(R));
+    *reinterpret_cast<R*>(p) = r;
 }
 
 // ---- launchers (host) ----------------------------------------------------------------------------

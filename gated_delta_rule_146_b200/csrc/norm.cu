@@ -52,62 +52,48 @@ Deal deal(const gdr_norm_args& a, int groups, int per_slot) {
 }
 
 template <typename S>
-__device__ __forceinline__ void token_stats(const float (&x)[S::NV][S::VEC], int l, int d,
-                                            int center, float eps, float& mean, float& rstd) {
+__device__ __forceinline__ void token_stats(const Pairs<S>& x, int l, int d, int center, float eps,
+                                            float& mean, float& rstd) {
     const float inv = 1.f / d;
-    mean = 0.f;
-    if (center) {
-        float s = 0.f;
-#pragma unroll
-        for (int k = 0; k < S::NV; ++k) {
-#pragma unroll
-            for (int j = 0; j < S::VEC; ++j) s += x[k][j];
-        }
-        mean = group_sum<S::LPG>(s) * inv;
-    }
-    float v = 0.f;
-#pragma unroll
-    for (int k = 0; k < S::NV; ++k) {
-        const bool in = (k * S::LPG + l) * S::VEC < d;
-#pragma unroll
-        for (int j = 0; j < S::VEC; ++j) {
-            const float t = x[k][j] - mean;
-            v = in ? fmaf(t, t, v) : v;
-        }
-    }
-    rstd = 1.f / sqrtf(group_sum<S::LPG>(v) * inv + eps);
+    mean = center ? group_sum<S::LPG>(lane_sum<S>(x)) * inv : 0.f;
+    rstd = 1.f / sqrtf(group_sum<S::LPG>(lane_squares<S>(x, mean, l, d)) * inv + eps);
 }
 
 template <typename S>
 __global__ void __launch_bounds__(kNormThreads)
 norm_token_fwd(const NormParams<typename S::IO> p, int used, long long slots) {
+    constexpr int kAhead = S::NV == 1 ? 2 : 1;   // rows loaded ahead of the one in work
     const int g = threadIdx.x / S::LPG, l = threadIdx.x % S::LPG;
     const long long slot = (long long)blockIdx.x * used + g;
     const bool on = g < used && slot < slots;
     const int head = (int)(slot % p.H);
-    float w[S::NV][S::VEC], b[S::NV][S::VEC];
-    load_affine<S>(p.w, 1.f, head, l, p.d, p.shared, w);
-    load_affine<S>(p.b, 0.f, head, l, p.d, p.shared, b);
+    const Pairs<S> w = load_affine<S>(p.w, 1.f, head, l, p.d, p.shared);
+    const Pairs<S> b = load_affine<S>(p.b, 0.f, head, l, p.d, p.shared);
     const bool gate = p.z != nullptr;
+    Raw<S> x[kAhead], z[kAhead];
+    auto fetch = [&](long long r0, int i) {
+        const bool in = on && r0 + g < p.rows;
+        const size_t at = (size_t)(in ? r0 + g : 0) * p.d;
+        x[i] = load_row<S>(p.x + at, l, p.d, in);
+        if (gate) z[i] = load_row<S>(p.z + at, l, p.d, in);
+    };
     // every lane takes part in the group sums until the block's last row
-    for (long long r0 = (long long)blockIdx.x * used; r0 < p.rows; r0 += slots) {
-        const long long r = r0 + g;
-        const bool in = on && r < p.rows;
-        const size_t at = (size_t)(in ? r : 0) * p.d;
-        float x[S::NV][S::VEC], z[S::NV][S::VEC], y[S::NV][S::VEC];
-        load_row<S>(p.x + at, l, p.d, in, x);
-        if (gate) load_row<S>(p.z + at, l, p.d, in, z);
-        float mean, rstd;
-        token_stats<S>(x, l, p.d, p.center, p.eps, mean, rstd);
-        if (!in) continue;
+    const long long first = (long long)blockIdx.x * used;
 #pragma unroll
-        for (int k = 0; k < S::NV; ++k) {
+    for (int i = 0; i < kAhead; ++i) fetch(first + i * slots, i);
+    for (long long r0 = first; r0 < p.rows; r0 += kAhead * slots) {
 #pragma unroll
-            for (int j = 0; j < S::VEC; ++j)
-                y[k][j] = norm_out((x[k][j] - mean) * rstd, w[k][j], b[k][j], gate,
-                                   gate ? z[k][j] : 0.f, p.act);
+        for (int i = 0; i < kAhead; ++i) {
+            const long long r = r0 + i * slots;
+            const Pairs<S> f = widen<S>(x[i]);
+            const Raw<S> zz = z[i];
+            fetch(r + kAhead * slots, i);
+            float mean, rstd;
+            token_stats<S>(f, l, p.d, p.center, p.eps, mean, rstd);
+            if (on && r + g < p.rows)
+                store_row<S>(p.y + (size_t)(r + g) * p.d, l, p.d,
+                             norm_rows<S>(f, w, b, gate, zz, mean, rstd, p.act));
         }
-        store_row<S>(p.y + at, l, p.d, y);
     }
 }
 
@@ -118,54 +104,35 @@ norm_token_bwd(const NormParams<typename S::IO> p, int used, long long slots) {
     const long long slot = (long long)blockIdx.x * used + g;
     const bool on = g < used && slot < slots;
     const int head = (int)(slot % p.H);
-    float w[S::NV][S::VEC], b[S::NV][S::VEC];
-    float dw[S::NV][S::VEC] = {}, db[S::NV][S::VEC] = {};
-    load_affine<S>(p.w, 1.f, head, l, p.d, p.shared, w);
-    load_affine<S>(p.b, 0.f, head, l, p.d, p.shared, b);
+    const Pairs<S> w = load_affine<S>(p.w, 1.f, head, l, p.d, p.shared);
+    const Pairs<S> b = load_affine<S>(p.b, 0.f, head, l, p.d, p.shared);
+    Pairs<S> dw = fill<S>(0.f), db = fill<S>(0.f);
     const bool gate = p.z != nullptr;
     const float inv = 1.f / p.d;
-    for (long long r0 = (long long)blockIdx.x * used; r0 < p.rows; r0 += slots) {
-        const long long r = r0 + g;
-        const bool in = on && r < p.rows;
-        const size_t at = (size_t)(in ? r : 0) * p.d;
-        float x[S::NV][S::VEC], z[S::NV][S::VEC], dy[S::NV][S::VEC];
-        load_row<S>(p.x + at, l, p.d, in, x);
-        load_row<S>(p.dy + at, l, p.d, in, dy);
-        if (gate) load_row<S>(p.z + at, l, p.d, in, z);
+    Raw<S> x, dy, z;
+    auto fetch = [&](long long r0) {
+        const bool in = on && r0 + g < p.rows;
+        const size_t at = (size_t)(in ? r0 + g : 0) * p.d;
+        x = load_row<S>(p.x + at, l, p.d, in);
+        dy = load_row<S>(p.dy + at, l, p.d, in);
+        if (gate) z = load_row<S>(p.z + at, l, p.d, in);
+    };
+    const long long first = (long long)blockIdx.x * used;
+    fetch(first);
+    for (long long r0 = first; r0 < p.rows; r0 += slots) {
+        const Raw<S> cx = x, cdy = dy, cz = z;
+        fetch(r0 + slots);
         float mean, rstd;
-        token_stats<S>(x, l, p.d, p.center, p.eps, mean, rstd);
-        float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-        for (int k = 0; k < S::NV; ++k) {
-            const bool c = (k * S::LPG + l) * S::VEC < p.d && in;
-#pragma unroll
-            for (int j = 0; j < S::VEC; ++j) {
-                const float n = (x[k][j] - mean) * rstd;
-                float dz = 0.f;
-                const float du = norm_du(n, w[k][j], b[k][j], gate, gate ? z[k][j] : 0.f,
-                                         dy[k][j], p.act, dz);
-                x[k][j] = n;
-                z[k][j] = dz;
-                const float q = du * w[k][j];
-                dy[k][j] = q;
-                if (!c) continue;
-                dw[k][j] = fmaf(du, n, dw[k][j]);
-                db[k][j] += du;
-                s1 += q;
-                s2 = fmaf(q, n, s2);
-            }
+        token_stats<S>(widen<S>(cx), l, p.d, p.center, p.eps, mean, rstd);
+        if (!on || r0 + g >= p.rows) rstd = 0.f;  // zeros throughout: nothing for the sums
+        const Back<S> o = back_rows<S, true>(cx, cdy, cz, gate, w, b, mean, rstd, p.act, dw, db);
+        const float mq = p.center ? group_sum<S::LPG>(o.s1) * inv : 0.f;
+        const float mqn = group_sum<S::LPG>(o.s2) * inv;
+        if (on && r0 + g < p.rows) {
+            const size_t at = (size_t)(r0 + g) * p.d;
+            store_row<S>(p.dx + at, l, p.d, back_dx<S>(o, rstd, mq, mqn));
+            if (gate) store_row<S>(p.dz + at, l, p.d, o.dz);
         }
-        s1 = p.center ? group_sum<S::LPG>(s1) * inv : 0.f;
-        s2 = group_sum<S::LPG>(s2) * inv;
-        if (!in) continue;
-#pragma unroll
-        for (int k = 0; k < S::NV; ++k) {
-#pragma unroll
-            for (int j = 0; j < S::VEC; ++j)
-                dy[k][j] = rstd * (dy[k][j] - s1 - x[k][j] * s2);
-        }
-        store_row<S>(p.dx + at, l, p.d, dy);
-        if (gate) store_row<S>(p.dz + at, l, p.d, z);
     }
     if (!p.part) return;
 
@@ -181,16 +148,20 @@ norm_token_bwd(const NormParams<typename S::IO> p, int used, long long slots) {
 #pragma unroll
                 for (int j = 0; j < S::VEC; ++j) {
                     const int c = (k * S::LPG + l) * S::VEC + j;
+                    const F2 v = which ? db.f[k][j / 2] : dw.f[k][j / 2];
                     if (c < p.d)
                         p.part[(((size_t)(slot / p.H) * 2 + which) * p.H + head) * p.d + c] =
-                            which ? db[k][j] : dw[k][j];
+                            j & 1 ? v.hi() : v.lo();
                 }
                 continue;
             }
             __syncthreads();
 #pragma unroll
-            for (int j = 0; j < S::VEC; ++j)
-                sh[g * kCh + l * S::VEC + j] = on ? (which ? db[k][j] : dw[k][j]) : 0.f;
+            for (int j = 0; j < S::VEC / 2; ++j) {
+                const F2 v = which ? db.f[k][j] : dw.f[k][j];
+                sh[g * kCh + l * S::VEC + 2 * j] = on ? v.lo() : 0.f;
+                sh[g * kCh + l * S::VEC + 2 * j + 1] = on ? v.hi() : 0.f;
+            }
             __syncthreads();
             for (int i = threadIdx.x; i < heads * kCh; i += kNormThreads) {
                 const int h = i / kCh, c = k * kCh + i % kCh;

@@ -1,9 +1,10 @@
 // norm_impl.cuh -- what the kernels of the group norm share: how a group's channels lie in a
 // warp, sums over them, and the formulas of one element.
 //
-// The d channels of one token's head are spread over LPG lanes, NV vectors of VEC channels
-// each (16 bytes where d allows, else one element), so a warp holds 32 / LPG heads and a row of
-// a tensor is read in whole lines.
+// The d channels of one token's head are spread over LPG lanes, NV vectors of VEC channels each:
+// 16 bytes where rows are whole such words, else two elements, read one by one.  A warp so holds
+// 32 / LPG heads and reads whole lines of a tensor.  Channels go in pairs through packed fp32
+// arithmetic; lanes behind the last channel hold zeros.
 #pragma once
 
 #include "layer.cuh"
@@ -13,10 +14,11 @@ namespace gdr {
 constexpr int kNormThreads = 256;
 constexpr int kNormWarps = kNormThreads / 32;
 
-template <typename IO_, int VEC_, int LPG_, int NV_>
+template <typename IO_, bool kWhole_, int LPG_, int NV_>
 struct Shape {
     using IO = IO_;
-    static constexpr int VEC = VEC_, LPG = LPG_, NV = NV_;
+    static constexpr bool kWhole = kWhole_;
+    static constexpr int VEC = kWhole ? 16 / (int)sizeof(IO) : 2, LPG = LPG_, NV = NV_;
     static constexpr int kGroups = kNormThreads / LPG;  // heads a block holds at once
 };
 
@@ -41,60 +43,200 @@ __device__ __forceinline__ float group_sum(float x) {
     return x;
 }
 
-// One lane's channels of a row; zero where there are none.
+// One lane's channels of a row, as they lie in memory.
 template <typename S>
-__device__ __forceinline__ void load_row(const typename S::IO* p, int l, int d, bool on,
-                                         float (&f)[S::NV][S::VEC]) {
+struct Raw {
+    Vec<typename S::IO, S::VEC> v[S::NV];
+};
+// The same in fp32.
+template <typename S>
+struct Pairs {
+    F2 f[S::NV][S::VEC / 2];
+};
+
+template <typename S>
+__device__ __forceinline__ Raw<S> load_row(const typename S::IO* p, int l, int d, bool on) {
+    using IO = typename S::IO;
+    Raw<S> r;
 #pragma unroll
     for (int k = 0; k < S::NV; ++k) {
         const int c = (k * S::LPG + l) * S::VEC;
-        if (on && c < d) load_f<typename S::IO, S::VEC>(p + c, f[k]);
-        else {
+        if (S::kWhole && on && c < d) {
+            r.v[k] = load_vec<IO, S::VEC>(p + c);
+        } else {
 #pragma unroll
-            for (int j = 0; j < S::VEC; ++j) f[k][j] = 0.f;
+            for (int j = 0; j < S::VEC; ++j)
+                r.v[k].x[j] = !S::kWhole && on && c + j < d ? p[c + j] : from_f<IO>(0.f);
+        }
+    }
+    return r;
+}
+
+template <typename S>
+__device__ __forceinline__ Pairs<S> widen(const Raw<S>& r) {
+    Pairs<S> f;
+#pragma unroll
+    for (int k = 0; k < S::NV; ++k) {
+#pragma unroll
+        for (int j = 0; j < S::VEC / 2; ++j) f.f[k][j] = pair_of(r.v[k], j);
+    }
+    return f;
+}
+
+template <typename S>
+__device__ __forceinline__ void store_row(typename S::IO* p, int l, int d, const Pairs<S>& f) {
+#pragma unroll
+    for (int k = 0; k < S::NV; ++k) {
+        const int c = (k * S::LPG + l) * S::VEC;
+        Vec<typename S::IO, S::VEC> v;
+#pragma unroll
+        for (int j = 0; j < S::VEC / 2; ++j) set_pair(v, j, f.f[k][j]);
+        if constexpr (S::kWhole) {
+            if (c < d) store_raw(p + c, v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < S::VEC; ++j)
+                if (c + j < d) p[c + j] = v.x[j];
         }
     }
 }
 
 template <typename S>
-__device__ __forceinline__ void store_row(typename S::IO* p, int l, int d,
-                                          const float (&f)[S::NV][S::VEC]) {
+__device__ __forceinline__ Pairs<S> fill(float x) {
+    Pairs<S> f;
 #pragma unroll
     for (int k = 0; k < S::NV; ++k) {
-        const int c = (k * S::LPG + l) * S::VEC;
-        if (c < d) store_vec<typename S::IO, S::VEC>(p + c, f[k]);
+#pragma unroll
+        for (int j = 0; j < S::VEC / 2; ++j) f.f[k][j] = f2(x);
     }
+    return f;
 }
 
 // The lane's weights (or biases): ones (zeros) where there are none.
 template <typename S>
-__device__ __forceinline__ void load_affine(const float* w, float none, int head, int l,
-                                            const int d, int shared, float (&f)[S::NV][S::VEC]) {
+__device__ __forceinline__ Pairs<S> load_affine(const float* w, float none, int head, int l, int d,
+                                                int shared) {
+    Pairs<S> f;
+    const size_t row = shared ? 0 : (size_t)head * d;
+    auto at = [&](int c) { return w && c < d ? __ldg(w + row + c) : none; };
 #pragma unroll
     for (int k = 0; k < S::NV; ++k) {
 #pragma unroll
-        for (int j = 0; j < S::VEC; ++j) {
-            const int c = (k * S::LPG + l) * S::VEC + j;
-            f[k][j] = w && c < d ? __ldg(w + (shared ? 0 : (size_t)head * d) + c) : none;
+        for (int j = 0; j < S::VEC / 2; ++j) {
+            const int c = (k * S::LPG + l) * S::VEC + 2 * j;
+            f.f[k][j] = f2(at(c), at(c + 1));
         }
     }
+    return f;
 }
 
-// y from the normalised value n (and the gate z)
-__device__ __forceinline__ float norm_out(float n, float w, float b, bool gate, float z, int act) {
-    const float u = fmaf(n, w, b);
-    return gate ? u * act_f(z, act) : act_f(u, act);
+// One where the lane has a channel, else zero.
+template <typename S>
+__device__ __forceinline__ F2 mask_of(int k, int j, int l, int d) {
+    const int c = (k * S::LPG + l) * S::VEC + 2 * j;
+    return f2(c < d ? 1.f : 0.f, c + 1 < d ? 1.f : 0.f);
 }
 
-// du (the gradient of u = n w + b) and dz
-__device__ __forceinline__ float norm_du(float n, float w, float b, bool gate, float z, float dy,
-                                         int act, float& dz) {
-    const float u = fmaf(n, w, b);
-    float a, g;
-    act_both(gate ? z : u, act, a, g);
-    if (!gate) return dy * g;
-    dz = dy * u * g;
-    return dy * a;
+template <typename S>
+__device__ __forceinline__ float lane_sum(const Pairs<S>& x) {
+    F2 s = x.f[0][0];
+#pragma unroll
+    for (int k = 0; k < S::NV; ++k) {
+#pragma unroll
+        for (int j = 0; j < S::VEC / 2; ++j)
+            if (k + j) s = add2(s, x.f[k][j]);
+    }
+    return s.lo() + s.hi();
+}
+
+// The lane's sum of squares about the mean.
+template <typename S>
+__device__ __forceinline__ float lane_squares(const Pairs<S>& x, float mean, int l, int d) {
+    F2 s = f2(0.f);
+#pragma unroll
+    for (int k = 0; k < S::NV; ++k) {
+#pragma unroll
+        for (int j = 0; j < S::VEC / 2; ++j) {
+            const F2 t = mul2(add2(x.f[k][j], f2(-mean)), mask_of<S>(k, j, l, d));
+            s = fma2(t, t, s);
+        }
+    }
+    return s.lo() + s.hi();
+}
+
+// y from x: n = (x - mean) rstd, u = n w + b, y = u act(z) or act(u)
+template <typename S>
+__device__ __forceinline__ Pairs<S> norm_rows(const Pairs<S>& x, const Pairs<S>& w, const Pairs<S>& b,
+                                              bool gate, const Raw<S>& z, float mean, float rstd,
+                                              int act) {
+    Pairs<S> y;
+    const F2 m = f2(-mean), r = f2(rstd);
+#pragma unroll
+    for (int k = 0; k < S::NV; ++k) {
+#pragma unroll
+        for (int j = 0; j < S::VEC / 2; ++j) {
+            const F2 n = mul2(add2(x.f[k][j], m), r), u = fma2(n, w.f[k][j], b.f[k][j]);
+            y.f[k][j] = gate ? mul2(u, act2(pair_of(z.v[k], j), act)) : act2(u, act);
+        }
+    }
+    return y;
+}
+
+// What the backward has of a row: n, q = du w, dz; du joins the sums for dw and db if kSums.
+template <typename S>
+struct Back {
+    Pairs<S> n, q, dz;
+    float s1, s2;   // the lane's sums of q and q n
+};
+template <typename S, bool kSums>
+__device__ __forceinline__ Back<S> back_rows(const Raw<S>& x, const Raw<S>& dy, const Raw<S>& z,
+                                             bool gate, const Pairs<S>& w, const Pairs<S>& b, float mean,
+                                             float rstd, int act, Pairs<S>& dw, Pairs<S>& db) {
+    Back<S> o;
+    const F2 m = f2(-mean), r = f2(rstd);
+    F2 s1 = f2(0.f), s2 = f2(0.f);
+#pragma unroll
+    for (int k = 0; k < S::NV; ++k) {
+#pragma unroll
+        for (int j = 0; j < S::VEC / 2; ++j) {
+            const F2 n = mul2(add2(pair_of(x.v[k], j), m), r), g = pair_of(dy.v[k], j);
+            const F2 u = fma2(n, w.f[k][j], b.f[k][j]);
+            F2 a, da, du;
+            act2_both(gate ? pair_of(z.v[k], j) : u, act, a, da);
+            if (gate) {
+                o.dz.f[k][j] = mul2(mul2(g, u), da);
+                du = mul2(g, a);
+            } else {
+                du = mul2(g, da);
+            }
+            if (kSums) {
+                dw.f[k][j] = fma2(du, n, dw.f[k][j]);
+                db.f[k][j] = add2(db.f[k][j], du);
+            }
+            const F2 q = mul2(du, w.f[k][j]);
+            s1 = add2(s1, q);
+            s2 = fma2(q, n, s2);
+            o.n.f[k][j] = n;
+            o.q.f[k][j] = q;
+        }
+    }
+    o.s1 = s1.lo() + s1.hi();
+    o.s2 = s2.lo() + s2.hi();
+    return o;
+}
+
+// dx = rstd (q - mean(q) - n mean(q n))
+template <typename S>
+__device__ __forceinline__ Pairs<S> back_dx(const Back<S>& o, float rstd, float mq, float mqn) {
+    Pairs<S> dx;
+    const F2 r = f2(rstd), m1 = f2(-mq), m2 = f2(-mqn);
+#pragma unroll
+    for (int k = 0; k < S::NV; ++k) {
+#pragma unroll
+        for (int j = 0; j < S::VEC / 2; ++j)
+            dx.f[k][j] = mul2(fma2(o.n.f[k][j], m2, add2(o.q.f[k][j], m1)), r);
+    }
+    return dx;
 }
 
 // Calls Op::go<Shape>(a, x, st) for the shape that holds d channels; see norm_supported.
@@ -103,17 +245,16 @@ void norm_dispatch_io(const gdr_norm_args& a, const NormPtrs& x, cudaStream_t st
     constexpr int V = 16 / sizeof(IO);
     if (a.d % V == 0) {
         const int n = a.d / V;
-        if (n <= 4) Op::template go<Shape<IO, V, 4, 1>>(a, x, st);
-        else if (n <= 8) Op::template go<Shape<IO, V, 8, 1>>(a, x, st);
-        else if (n <= 16) Op::template go<Shape<IO, V, 16, 1>>(a, x, st);
-        else if (n <= 32) Op::template go<Shape<IO, V, 32, 1>>(a, x, st);
-        else if (n <= 64) Op::template go<Shape<IO, V, 32, 2>>(a, x, st);
-        else if (V == 8 || n <= 128) Op::template go<Shape<IO, V, 32, 4>>(a, x, st);
-        else if constexpr (V == 4) Op::template go<Shape<IO, V, 32, 8>>(a, x, st);
-    } else if (a.d <= 32) Op::template go<Shape<IO, 1, 32, 1>>(a, x, st);
-    else if (a.d <= 64) Op::template go<Shape<IO, 1, 32, 2>>(a, x, st);
-    else if (a.d <= 128) Op::template go<Shape<IO, 1, 32, 4>>(a, x, st);
-    else Op::template go<Shape<IO, 1, 32, 8>>(a, x, st);
+        if (n <= 4) Op::template go<Shape<IO, true, 4, 1>>(a, x, st);
+        else if (n <= 8) Op::template go<Shape<IO, true, 8, 1>>(a, x, st);
+        else if (n <= 16) Op::template go<Shape<IO, true, 16, 1>>(a, x, st);
+        else if (n <= 32) Op::template go<Shape<IO, true, 32, 1>>(a, x, st);
+        else if (n <= 64) Op::template go<Shape<IO, true, 32, 2>>(a, x, st);
+        else if (V == 8 || n <= 128) Op::template go<Shape<IO, true, 32, 4>>(a, x, st);
+        else if constexpr (V == 4) Op::template go<Shape<IO, true, 32, 8>>(a, x, st);
+    } else if (a.d <= 64) Op::template go<Shape<IO, false, 32, 1>>(a, x, st);
+    else if (a.d <= 128) Op::template go<Shape<IO, false, 32, 2>>(a, x, st);
+    else Op::template go<Shape<IO, false, 32, 4>>(a, x, st);
 }
 
 // Lane groups of a block (Shape::kGroups of the shape the dispatch below takes).

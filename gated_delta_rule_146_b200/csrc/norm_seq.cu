@@ -38,7 +38,6 @@ constexpr int kHold = S::NV >= 8 ? 1 : 8 / S::NV;
 template <typename S>
 __global__ void __launch_bounds__(kNormThreads)
 norm_seq_stats(const NormParams<typename S::IO> p) {
-    using IO = typename S::IO;
     constexpr int kTokens = S::kGroups * kHold<S>;
     __shared__ float sh[kNormWarps];
     const int g = threadIdx.x / S::LPG, l = threadIdx.x % S::LPG;
@@ -46,16 +45,11 @@ norm_seq_stats(const NormParams<typename S::IO> p) {
     if (blockIdx.x == 0) check_cu(p.q, p.status, threadIdx.x, kNormThreads);
     const int t0 = (int)min((long long)p.q.total, (long long)tile * kTokens);
     const int t1 = (int)min((long long)p.q.total, (long long)t0 + kTokens);
-    Vec<IO, S::VEC> x[kHold<S>][S::NV];
+    Raw<S> x[kHold<S>];
 #pragma unroll
     for (int i = 0; i < kHold<S>; ++i) {
         const int t = t0 + g + i * S::kGroups;
-#pragma unroll
-        for (int k = 0; k < S::NV; ++k) {
-            const int c = (k * S::LPG + l) * S::VEC;
-            if (t < t1 && c < p.d)
-                x[i][k] = load_vec<IO, S::VEC>(p.x + ((size_t)t * p.H + h) * p.d + c);
-        }
+        x[i] = load_row<S>(p.x + ((size_t)(t < t1 ? t : t0) * p.H + h) * p.d, l, p.d, t < t1);
     }
     for (int s = p.q.of(t0); s < p.q.n; ++s) {
         const int b = p.q.begin(s), e = p.q.end(s);
@@ -68,12 +62,7 @@ norm_seq_stats(const NormParams<typename S::IO> p) {
 #pragma unroll
             for (int i = 0; i < kHold<S>; ++i) {
                 const int t = t0 + g + i * S::kGroups;
-#pragma unroll
-                for (int k = 0; k < S::NV; ++k) {
-                    if (t < lo || t >= hi || (k * S::LPG + l) * S::VEC >= p.d) continue;
-#pragma unroll
-                    for (int j = 0; j < S::VEC; ++j) v += to_f(x[i][k].x[j]);
-                }
+                if (t >= lo && t < hi) v += lane_sum<S>(widen<S>(x[i]));
             }
             mean = block_sum(v, sh) / ((float)(hi - lo) * p.d);
         }
@@ -81,15 +70,7 @@ norm_seq_stats(const NormParams<typename S::IO> p) {
 #pragma unroll
         for (int i = 0; i < kHold<S>; ++i) {
             const int t = t0 + g + i * S::kGroups;
-#pragma unroll
-            for (int k = 0; k < S::NV; ++k) {
-                if (t < lo || t >= hi || (k * S::LPG + l) * S::VEC >= p.d) continue;
-#pragma unroll
-                for (int j = 0; j < S::VEC; ++j) {
-                    const float u = to_f(x[i][k].x[j]) - mean;
-                    v = fmaf(u, u, v);
-                }
-            }
+            if (t >= lo && t < hi) v += lane_squares<S>(widen<S>(x[i]), mean, l, p.d);
         }
         v = block_sum(v, sh);
         if (threadIdx.x == 0)
@@ -139,33 +120,40 @@ __device__ __forceinline__ int seq_from(const Seqs& q, int s, int t) {
     return s;
 }
 
+// Rows a lane group loads before it uses them.
+template <typename S>
+constexpr int kBatch = S::NV == 1 ? 4 : S::NV == 2 ? 2 : 1;
+
+// The second pass visits the tiles backwards: the first one's last tiles are still in L2.
 template <typename S>
 __global__ void __launch_bounds__(kNormThreads)
 norm_seq_apply(const NormParams<typename S::IO> p, int tokens) {
     const int g = threadIdx.x / S::LPG, l = threadIdx.x % S::LPG;
-    const int tile = blockIdx.x / p.H, h = blockIdx.x % p.H;
+    const int block = gridDim.x - 1 - blockIdx.x, tile = block / p.H, h = block % p.H;
     const int t0 = (int)min((long long)p.q.total, (long long)tile * tokens);
     const int t1 = (int)min((long long)p.q.total, (long long)t0 + tokens);
-    float w[S::NV][S::VEC], b[S::NV][S::VEC];
-    load_affine<S>(p.w, 1.f, h, l, p.d, p.shared, w);
-    load_affine<S>(p.b, 0.f, h, l, p.d, p.shared, b);
+    const Pairs<S> w = load_affine<S>(p.w, 1.f, h, l, p.d, p.shared);
+    const Pairs<S> b = load_affine<S>(p.b, 0.f, h, l, p.d, p.shared);
     const bool gate = p.z != nullptr;
     int s = t0 + g < t1 ? p.q.of(t0 + g) : 0;
-    for (int t = t0 + g; t < t1; t += S::kGroups) {
-        s = seq_from(p.q, s, t);
-        const float2 st = __ldg(reinterpret_cast<const float2*>(p.stats) + (size_t)s * p.H + h);
-        const size_t at = ((size_t)t * p.H + h) * p.d;
-        float x[S::NV][S::VEC], z[S::NV][S::VEC], y[S::NV][S::VEC];
-        load_row<S>(p.x + at, l, p.d, true, x);
-        if (gate) load_row<S>(p.z + at, l, p.d, true, z);
+    for (int t = t0 + g; t < t1; t += kBatch<S> * S::kGroups) {
+        Raw<S> x[kBatch<S>], z[kBatch<S>];
 #pragma unroll
-        for (int k = 0; k < S::NV; ++k) {
-#pragma unroll
-            for (int j = 0; j < S::VEC; ++j)
-                y[k][j] = norm_out((x[k][j] - st.x) * st.y, w[k][j], b[k][j], gate,
-                                   gate ? z[k][j] : 0.f, p.act);
+        for (int i = 0; i < kBatch<S>; ++i) {
+            const int ti = t + i * S::kGroups;
+            const size_t at = ((size_t)(ti < t1 ? ti : t) * p.H + h) * p.d;
+            x[i] = load_row<S>(p.x + at, l, p.d, true);
+            if (gate) z[i] = load_row<S>(p.z + at, l, p.d, true);
         }
-        store_row<S>(p.y + at, l, p.d, y);
+#pragma unroll
+        for (int i = 0; i < kBatch<S>; ++i) {
+            const int ti = t + i * S::kGroups;
+            if (ti >= t1) break;
+            s = seq_from(p.q, s, ti);
+            const float2 st = __ldg(reinterpret_cast<const float2*>(p.stats) + (size_t)s * p.H + h);
+            store_row<S>(p.y + ((size_t)ti * p.H + h) * p.d, l, p.d,
+                         norm_rows<S>(widen<S>(x[i]), w, b, gate, z[i], st.x, st.y, p.act));
+        }
     }
 }
 
@@ -181,10 +169,9 @@ norm_seq_bwd_sums(const NormParams<typename S::IO> p, int tokens, float2* __rest
     if (blockIdx.x == 0) check_cu(p.q, p.status, threadIdx.x, kNormThreads);
     const int t0 = (int)min((long long)p.q.total, (long long)tile * tokens);
     const int t1 = (int)min((long long)p.q.total, (long long)t0 + tokens);
-    float w[S::NV][S::VEC], b[S::NV][S::VEC];
-    float dw[S::NV][S::VEC] = {}, db[S::NV][S::VEC] = {};
-    load_affine<S>(p.w, 1.f, h, l, p.d, p.shared, w);
-    load_affine<S>(p.b, 0.f, h, l, p.d, p.shared, b);
+    const Pairs<S> w = load_affine<S>(p.w, 1.f, h, l, p.d, p.shared);
+    const Pairs<S> b = load_affine<S>(p.b, 0.f, h, l, p.d, p.shared);
+    Pairs<S> dw = fill<S>(0.f), db = fill<S>(0.f);
     const bool gate = p.z != nullptr;
     for (int s = t0 < t1 ? p.q.of(t0) : p.q.n; s < p.q.n; ++s) {
         const int sb = p.q.begin(s), se = p.q.end(s);
@@ -193,31 +180,26 @@ norm_seq_bwd_sums(const NormParams<typename S::IO> p, int tokens, float2* __rest
         if (lo >= hi) continue;
         const float2 st = __ldg(reinterpret_cast<const float2*>(p.stats) + (size_t)s * p.H + h);
         float s1 = 0.f, s2 = 0.f;
-        for (int t = lo + g; t < hi; t += S::kGroups) {
-            const size_t at = ((size_t)t * p.H + h) * p.d;
-            float x[S::NV][S::VEC], z[S::NV][S::VEC], dy[S::NV][S::VEC];
-            load_row<S>(p.x + at, l, p.d, true, x);
-            load_row<S>(p.dy + at, l, p.d, true, dy);
-            if (gate) load_row<S>(p.z + at, l, p.d, true, z);
+        for (int t = lo + g; t < hi; t += kBatch<S> * S::kGroups) {
+            Raw<S> x[kBatch<S>], dy[kBatch<S>], z[kBatch<S>];
 #pragma unroll
-            for (int k = 0; k < S::NV; ++k) {
-                const bool in = (k * S::LPG + l) * S::VEC < p.d;
-#pragma unroll
-                for (int j = 0; j < S::VEC; ++j) {
-                    const float n = (x[k][j] - st.x) * st.y;
-                    float dz = 0.f;
-                    const float du = norm_du(n, w[k][j], b[k][j], gate, gate ? z[k][j] : 0.f,
-                                             dy[k][j], p.act, dz);
-                    z[k][j] = dz;
-                    if (!in) continue;
-                    dw[k][j] = fmaf(du, n, dw[k][j]);
-                    db[k][j] += du;
-                    const float q = du * w[k][j];
-                    s1 += q;
-                    s2 = fmaf(q, n, s2);
-                }
+            for (int i = 0; i < kBatch<S>; ++i) {
+                const int ti = t + i * S::kGroups;
+                const size_t at = ((size_t)(ti < hi ? ti : t) * p.H + h) * p.d;
+                x[i] = load_row<S>(p.x + at, l, p.d, true);
+                dy[i] = load_row<S>(p.dy + at, l, p.d, true);
+                if (gate) z[i] = load_row<S>(p.z + at, l, p.d, true);
             }
-            if (gate) store_row<S>(p.dz + at, l, p.d, z);
+#pragma unroll
+            for (int i = 0; i < kBatch<S>; ++i) {
+                const int ti = t + i * S::kGroups;
+                if (ti >= hi) break;
+                const Back<S> o = back_rows<S, true>(x[i], dy[i], z[i], gate, w, b, st.x, st.y, p.act,
+                                                     dw, db);
+                s1 += o.s1;
+                s2 += o.s2;
+                if (gate) store_row<S>(p.dz + ((size_t)ti * p.H + h) * p.d, l, p.d, o.dz);
+            }
         }
         s1 = block_sum(s1, sh);
         s2 = block_sum(s2, sh);
@@ -229,8 +211,11 @@ norm_seq_bwd_sums(const NormParams<typename S::IO> p, int tokens, float2* __rest
         for (int k = 0; k < S::NV; ++k) {
             __syncthreads();
 #pragma unroll
-            for (int j = 0; j < S::VEC; ++j)
-                shw[g * kCh + l * S::VEC + j] = which ? db[k][j] : dw[k][j];
+            for (int j = 0; j < S::VEC / 2; ++j) {
+                const F2 v = which ? db.f[k][j] : dw.f[k][j];
+                shw[g * kCh + l * S::VEC + 2 * j] = v.lo();
+                shw[g * kCh + l * S::VEC + 2 * j + 1] = v.hi();
+            }
             __syncthreads();
             for (int i = threadIdx.x; i < kCh; i += kNormThreads) {
                 const int c = k * kCh + i;
@@ -272,35 +257,35 @@ __global__ void __launch_bounds__(kNormThreads)
 norm_seq_bwd_apply(const NormParams<typename S::IO> p, int tokens,
                    const float2* __restrict__ means) {
     const int g = threadIdx.x / S::LPG, l = threadIdx.x % S::LPG;
-    const int tile = blockIdx.x / p.H, h = blockIdx.x % p.H;
+    const int block = gridDim.x - 1 - blockIdx.x, tile = block / p.H, h = block % p.H;
     const int t0 = (int)min((long long)p.q.total, (long long)tile * tokens);
     const int t1 = (int)min((long long)p.q.total, (long long)t0 + tokens);
-    float w[S::NV][S::VEC], b[S::NV][S::VEC];
-    load_affine<S>(p.w, 1.f, h, l, p.d, p.shared, w);
-    load_affine<S>(p.b, 0.f, h, l, p.d, p.shared, b);
+    const Pairs<S> w = load_affine<S>(p.w, 1.f, h, l, p.d, p.shared);
+    const Pairs<S> b = load_affine<S>(p.b, 0.f, h, l, p.d, p.shared);
+    Pairs<S> none;
     const bool gate = p.z != nullptr;
     int s = t0 + g < t1 ? p.q.of(t0 + g) : 0;
-    for (int t = t0 + g; t < t1; t += S::kGroups) {
-        s = seq_from(p.q, s, t);
-        const float2 st = __ldg(reinterpret_cast<const float2*>(p.stats) + (size_t)s * p.H + h);
-        const float2 m = __ldg(means + (size_t)s * p.H + h);
-        const size_t at = ((size_t)t * p.H + h) * p.d;
-        float x[S::NV][S::VEC], z[S::NV][S::VEC], dy[S::NV][S::VEC];
-        load_row<S>(p.x + at, l, p.d, true, x);
-        load_row<S>(p.dy + at, l, p.d, true, dy);
-        if (gate) load_row<S>(p.z + at, l, p.d, true, z);
+    for (int t = t0 + g; t < t1; t += kBatch<S> * S::kGroups) {
+        Raw<S> x[kBatch<S>], dy[kBatch<S>], z[kBatch<S>];
 #pragma unroll
-        for (int k = 0; k < S::NV; ++k) {
-#pragma unroll
-            for (int j = 0; j < S::VEC; ++j) {
-                const float n = (x[k][j] - st.x) * st.y;
-                float dz;
-                const float du = norm_du(n, w[k][j], b[k][j], gate, gate ? z[k][j] : 0.f,
-                                         dy[k][j], p.act, dz);
-                x[k][j] = st.y * (du * w[k][j] - m.x - n * m.y);
-            }
+        for (int i = 0; i < kBatch<S>; ++i) {
+            const int ti = t + i * S::kGroups;
+            const size_t at = ((size_t)(ti < t1 ? ti : t) * p.H + h) * p.d;
+            x[i] = load_row<S>(p.x + at, l, p.d, true);
+            dy[i] = load_row<S>(p.dy + at, l, p.d, true);
+            if (gate) z[i] = load_row<S>(p.z + at, l, p.d, true);
         }
-        store_row<S>(p.dx + at, l, p.d, x);
+#pragma unroll
+        for (int i = 0; i < kBatch<S>; ++i) {
+            const int ti = t + i * S::kGroups;
+            if (ti >= t1) break;
+            s = seq_from(p.q, s, ti);
+            const float2 st = __ldg(reinterpret_cast<const float2*>(p.stats) + (size_t)s * p.H + h);
+            const float2 m = __ldg(means + (size_t)s * p.H + h);
+            const Back<S> o = back_rows<S, false>(x[i], dy[i], z[i], gate, w, b, st.x, st.y, p.act,
+                                                  none, none);
+            store_row<S>(p.dx + ((size_t)ti * p.H + h) * p.d, l, p.d, back_dx<S>(o, st.y, m.x, m.y));
+        }
     }
 }
 
@@ -309,7 +294,7 @@ norm_seq_bwd_apply(const NormParams<typename S::IO> p, int tokens,
 // Tokens of a tile in the statistics pass: what a block holds in registers.
 int stats_tile(const gdr_norm_args& a) {
     const int v = a.io_dtype == GDR_BF16 ? 8 : 4;
-    const int n = a.d % v ? a.d : a.d / v;             // vectors of a row
+    const int n = a.d % v ? (a.d + 1) / 2 : a.d / v;   // vectors of a row
     const int nv = n <= 32 ? 1 : n <= 64 ? 2 : n <= 128 ? 4 : 8;
     return norm_groups(a) * (8 / nv);
 }

@@ -10,6 +10,8 @@ namespace gdr {
 
 namespace {
 
+// Two tiles ahead.  More bytes in flight cost: with three tiles ahead the training shape takes 97
+// instead of 86 us (beta given), with one 95.
 constexpr int kStages = 3;
 
 // Tokens of a warp's run: eight in bf16, four where fp32 doubles the bytes of a tile.

@@ -12,8 +12,17 @@ namespace gdr {
 
 namespace {
 
-constexpr int kSeg = 4;      // tokens of a warp's run
-constexpr int kStages = 3;
+// Stages of the two rings.  The second is a step ahead; how far the first may be was measured on
+// 8 x 4096 x 2048 in bf16: plain 120 us one tile ahead, 136 two; with beta, whose second ring is
+// larger, 211 and 186.  More bytes in flight than the memory system takes in order cost time.
+template <int kWrite>
+constexpr int early_stages = kWrite == GDR_WRITE_GATE ? 3 : 2;
+constexpr int kLateStages = 2;
+
+// Tokens of a warp's run: eight where two blocks' rings of 8 warps fit an SM's shared memory,
+// bf16 in single blocks, else four.
+template <typename IO, typename GT>
+constexpr int seg_of(bool cluster) { return !cluster && sizeof(IO) + sizeof(GT) == 4 ? 8 : 4; }
 
 template <typename IO, typename GT>
 struct BwdParams {
@@ -28,17 +37,18 @@ struct BwdParams {
 
 // A warp's tokens in shared memory, in two rings: g and dO of a tile are read when its run is
 // formed, o of the token before, v and beta a step later, when it is finished.
-template <typename IO, typename GT, int kWrite>
+template <typename IO, typename GT, int kWrite, int kSeg>
 struct Ring {
     static constexpr int kG = Rows<GT, kSeg>::kBytes, kI = Rows<IO, kSeg>::kBytes;
     static constexpr int kEarly = kG + kI;
     static constexpr int v = kI, beta = v + kI;  // behind o
-    static constexpr int kLate = kI + (kWrite == GDR_WRITE_PLAIN ? 0 : kI) +
-                                 (kWrite == GDR_WRITE_GATE ? kG : 0);
-    static constexpr int kBytes = kStages * (kEarly + kLate);
+    static constexpr int kLate = kWrite == GDR_WRITE_GATE ? beta + kG
+                               : kWrite == GDR_WRITE_TIED ? beta : v;
+    static constexpr int kEarlyStages = early_stages<kWrite>;
+    static constexpr int kBytes = kEarlyStages * kEarly + kLateStages * kLate;
 };
 
-template <int kWrite>
+template <int kWrite, int kSeg>
 struct Elements {
     F2 a[kSeg], d[kSeg];           // alpha; dO, with dh_final at a sequence's last token
     F2 w[kWrite == GDR_WRITE_TIED ? kSeg : 1];
@@ -53,8 +63,10 @@ scan_bwd_kernel(const BwdParams<IO, GT> p, const int cluster) {
     using Shared = ScanShared<kWarps, kCluster>;
     Shared& sh = *reinterpret_cast<Shared*>(smem);
     char* const stages = smem + sizeof(sh) + (kSeqs ? kCuBytes : 0);
-    using R = Ring<IO, GT, kWrite>;
-    constexpr int kTile = kWarps * kSeg;
+    constexpr int kSeg = seg_of<IO, GT>(kCluster), kTile = kWarps * kSeg;
+    using R = Ring<IO, GT, kWrite, kSeg>;
+    constexpr int kEarlyStages = R::kEarlyStages;
+    using Els = Elements<kWrite, kSeg>;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int rank = blockIdx.x % cluster;
     const int unit = blockIdx.x / cluster;
@@ -86,7 +98,7 @@ scan_bwd_kernel(const BwdParams<IO, GT> p, const int cluster) {
     const int steps = (int)(((long long)L + stride - 1) / stride);
     const long long hop = (long long)dir * stride * D;
     char* const early = stages + wid * R::kBytes;
-    char* const late = early + kStages * R::kEarly;
+    char* const late = early + kEarlyStages * R::kEarly;
     Feed<GT, kCopy, kSeg> fg, fb;
     Feed<IO, kCopy, kSeg> fd, fo, fv;
     fg.open(p.g + base, origin, dir, first0, D, left, lane);
@@ -116,26 +128,25 @@ scan_bwd_kernel(const BwdParams<IO, GT> p, const int cluster) {
         scan_close<kCluster>();
         return;
     }
-    // copy group k: the first ring's tile k and the second's tile k - 1
-    feed_early(0, 0);
-    copy_commit();
-    feed_early(1, 1);
-    feed_late(0, 0);
-    copy_commit();
+    // copy group k: the first ring's tile k, with the second's kEarlyStages - 1 tiles behind it
+#pragma unroll
+    for (int k = 0; k < kEarlyStages - 1; ++k) {
+        feed_early(k, k);
+        copy_commit();
+    }
 
     if (!kSeqs && p.h0) h0_row = load_state<kCopy>(p.h0 + (size_t)row * D + c, mine);
     Here here{0, 0};
-    int stage = 0, last = 0;  // of the next tile to be formed, and to be finished
-    auto form = [&](int k, Elements<kWrite>& e) -> Run {
-        copy_wait<1>();
+    int stage = 0;  // of the next tile to be formed
+    auto form = [&](int k, Els& e) -> Run {
+        copy_wait<kEarlyStages - 2>();
         __syncwarp();
         // into the stages of tiles k - 1 and k - 2, which every lane has read
-        const int second = stage == kStages - 1 ? 0 : stage + 1;
-        feed_early(k + 2, stage == 0 ? kStages - 1 : stage - 1);
-        feed_late(k + 1, second);
+        feed_early(k + kEarlyStages - 1, stage == 0 ? kEarlyStages - 1 : stage - 1);
+        feed_late(k, k & 1);
         copy_commit();
         const char* s = early + stage * R::kEarly;
-        stage = second;
+        stage = stage == kEarlyStages - 1 ? 0 : stage + 1;
         if constexpr (kSeqs) {
             const int first = first0 + k * stride;
             e.m = find_marks(seqs, here, origin, dir, first, min(kSeg, L - first), lane);
@@ -169,13 +180,12 @@ scan_bwd_kernel(const BwdParams<IO, GT> p, const int cluster) {
 
     const long long next = (long long)dir * D;
     long long out = (long long)base + (origin + (long long)dir * first0) * D + 2 * lane;
-    auto finish = [&](int k, const Elements<kWrite>& e, F2 mu) {
-        if (k + 1 == steps) {  // no tile was formed behind this one: its second ring may be on the way
-            copy_wait<0>();
-            __syncwarp();
-        }
-        const char* s = late + last * R::kLate;
-        last = last == kStages - 1 ? 0 : last + 1;
+    auto finish = [&](int k, const Els& e, F2 mu) {
+        // the second ring's tile k came in the group before the last; behind the last tile nothing
+        // was formed
+        if (k + 1 == steps) copy_wait<0>(); else copy_wait<1>();
+        __syncwarp();
+        const char* s = late + (k & 1) * R::kLate;
         const int first = first0 + k * stride, n = L - first;
         long long at = out;
         out += hop;
@@ -223,9 +233,9 @@ scan_bwd_kernel(const BwdParams<IO, GT> p, const int cluster) {
         }
     };
     if constexpr (kCluster) {
-        scan_work<Elements<kWrite>>(sh, steps, wid, lane, form, finish);
+        scan_work<Els>(sh, steps, wid, lane, form, finish);
     } else {
-        scan_walk<kSeqs, Elements<kWrite>>(sh, steps, wid, lane, carry, form, finish);
+        scan_walk<kSeqs, Els>(sh, steps, wid, lane, carry, form, finish);
     }
     copy_wait<0>();
     scan_close<kCluster>();
@@ -256,8 +266,8 @@ gdr_status bwd_launch(const gdr_scan_args& a, const ScanPtrs& x, cudaStream_t st
     const int cluster = kCopy == kCopyOne ? 0 : scan_cluster(units);
     // 16 warps' rings fit an SM's shared memory in bf16 only
     constexpr int kWide = sizeof(IO) + sizeof(GT) == 4 ? 16 : 8;
-    auto launch = [&](auto kernel, int warps, int threads, size_t shared) {
-        const size_t smem = (size_t)warps * Ring<IO, GT, kWrite>::kBytes + shared +
+    auto launch = [&](auto kernel, int warps, int threads, size_t ring, size_t shared) {
+        const size_t smem = warps * ring + shared +
                             (seqs ? kCuBytes : 0);
         return scan_launch(kernel, p, units, cluster ? cluster : 1, threads, smem, st);
     };
@@ -265,12 +275,14 @@ gdr_status bwd_launch(const gdr_scan_args& a, const ScanPtrs& x, cudaStream_t st
         if (cluster) {
             constexpr int kThreads = 32 * (kWide + 2);
             constexpr size_t kShared = sizeof(ScanShared<kWide, true>);
-            return seqs ? launch(scan_bwd_kernel<IO, GT, kWrite, kCopy, true, true, kWide>, kWide, kThreads, kShared)
-                        : launch(scan_bwd_kernel<IO, GT, kWrite, kCopy, false, true, kWide>, kWide, kThreads, kShared);
+            constexpr size_t kRing = Ring<IO, GT, kWrite, seg_of<IO, GT>(true)>::kBytes;
+            return seqs ? launch(scan_bwd_kernel<IO, GT, kWrite, kCopy, true, true, kWide>, kWide, kThreads, kRing, kShared)
+                        : launch(scan_bwd_kernel<IO, GT, kWrite, kCopy, false, true, kWide>, kWide, kThreads, kRing, kShared);
         }
     }
-    return seqs ? launch(scan_bwd_kernel<IO, GT, kWrite, kCopy, true, false, 8>, 8, 256, sizeof(ScanShared<8, false>))
-                : launch(scan_bwd_kernel<IO, GT, kWrite, kCopy, false, false, 8>, 8, 256, sizeof(ScanShared<8, false>));
+    constexpr size_t kRing = Ring<IO, GT, kWrite, seg_of<IO, GT>(false)>::kBytes;
+    return seqs ? launch(scan_bwd_kernel<IO, GT, kWrite, kCopy, true, false, 8>, 8, 256, kRing, sizeof(ScanShared<8, false>))
+                : launch(scan_bwd_kernel<IO, GT, kWrite, kCopy, false, false, 8>, 8, 256, kRing, sizeof(ScanShared<8, false>));
 }
 
 struct Bwd {

@@ -35,54 +35,6 @@ constexpr int kSlab = 64;                      // channels of a block
 constexpr float kReset = -1.f;
 constexpr uint64_t kScanWaitNs = 2000000000ull;
 
-// ---- a lane's two channels, in one 64-bit register pair -------------------------------------------
-struct F2 {
-    uint64_t v;
-    __device__ __forceinline__ float lo() const { return __uint_as_float((uint32_t)v); }
-    __device__ __forceinline__ float hi() const { return __uint_as_float((uint32_t)(v >> 32)); }
-};
-__device__ __forceinline__ F2 f2(float lo, float hi) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ F2 f2(float x) { return f2(x, x); }
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 pick2(bool c, F2 a, F2 b) { return F2{c ? a.v : b.v}; }
-
-// max that lets NaN through
-__device__ __forceinline__ float max_nan(float x, float y) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
-    return r;
-}
-
-// e^g = 2^(g log2 e).  The product is rounded; what the rounding left out, e, and the low part of
-// log2 e multiply the result by 2^e = 1 + e ln 2 to first order (e is below 2^-16 in the range).
-// Below e^-150 the result is zero in either case, and the clamp keeps -inf out of the products.
-__device__ __forceinline__ F2 exp2ch(F2 g) {
-    const F2 x = f2(max_nan(g.lo(), -150.f), max_nan(g.hi(), -150.f));
-    const F2 t = mul2(x, f2(1.44269504f));
-    F2 e = fma2(x, f2(-1.44269504f), t);  // -e
-    e = fma2(x, f2(-1.92596303e-8f), e);
-    const F2 m = f2(ex2(t.lo()), ex2(t.hi()));
-    return fma2(mul2(m, e), f2(-0.693147181f), m);
-}
-
 // 1 - e^g given a = e^g: the series of e^g - 1 near zero (|g| < 1/2; the term left out is below
 // 2^-26 of the sum), the difference elsewhere.
 __device__ __forceinline__ F2 one_minus(F2 g, F2 a) {
@@ -120,13 +72,14 @@ __device__ __forceinline__ Run run_join(const Run& f, const Run& r) {
     return o;
 }
 
-// Runs go by tile parity: a warp forms tile k + 2 behind a barrier that all readers of tile k's
-// runs have passed (in a cluster: once it has the state of tile k, and the folder has read them by
-// then).  Blocks' runs go by tile modulo four: a block sends tile j when its workers have the
+// In a single block runs go by tile modulo four: between the readings of tile k, behind the
+// barrier of its step, and the writing of tile k + 4 lies another step's barrier.  In a cluster
+// they go by tile parity: a worker forms tile k + 2 once it has the state of tile k, and the folder
+// has read that tile's runs by then.  Blocks' runs go by tile modulo four: a block sends tile j when its workers have the
 // states of tile j - 2, for which every block has sent tile j - 2, and so has folded tile j - 4.
 template <int kWarps, bool kCluster>
 struct alignas(128) ScanShared {
-    Run run[2][kWarps][32];
+    Run run[kCluster ? 2 : 4][kWarps][32];
     F2 before[kCluster ? 2 : 1][kCluster ? kWarps : 1][32];
     Run block[kCluster ? 4 : 1][kScanMaxCluster][32];
     alignas(128) uint64_t full[4];   // bytes of block[] that have come
@@ -139,15 +92,15 @@ template <bool kSeqs, typename E, int kWarps, typename Form, typename Finish>
 __device__ __forceinline__ void scan_walk(ScanShared<kWarps, false>& sh, int steps, int wid, int lane,
                                           F2& carry, Form form, Finish finish) {
     auto turn = [&](int k, E& now, E& next) {
-        if (k + 1 < steps) sh.run[(k + 1) & 1][wid][lane] = form(k + 1, next);
+        if (k + 1 < steps) sh.run[(k + 1) & 3][wid][lane] = form(k + 1, next);
+        __syncthreads();
         F2 x = carry;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             if (w == wid) x = carry;
-            carry = run_apply<kSeqs>(sh.run[k & 1][w][lane], carry);
+            carry = run_apply<kSeqs>(sh.run[k & 3][w][lane], carry);
         }
         finish(k, now, x);
-        __syncthreads();
     };
     E even, odd;
     sh.run[0][wid][lane] = form(0, even);
