@@ -4,8 +4,8 @@
 //
 // A thread owns N neighbouring channels (8 bytes of a row) and walks a run of tokens with the last
 // W inputs in registers, so that every input is read once (and W - 1 more at the start of each
-// run, which the cache serves).  Tokens are loaded in batches, the next batch before one is used.
-// Channels go in pairs through packed fp32 arithmetic, and the activation costs one exponential
+// run, which the cache serves).  Tokens arrive by asynchronous copies, two batches of four ahead,
+// in shared memory of the thread's own, which takes no registers and no barrier.  Channels go in pairs through packed fp32 arithmetic, and the activation costs one exponential
 // and one reciprocal: with an IEEE division the forward took 2.5 times as long as its bytes.  HBM
 // bounds all three kernels: 4 bytes per token and channel forward and 6 backward, in bf16.
 //
@@ -52,11 +52,14 @@ __device__ __forceinline__ void run_places(const Span& sp, int t0, int t1, int& 
 // `left` channels from the thread's first one on.
 template <typename IO, int N, bool kWhole>
 __device__ __forceinline__ Vec<IO, N> fetch(const IO* p, int left) {
-    if constexpr (kWhole) return load_vec<IO, N>(p);
-    Vec<IO, N> v;
+    if constexpr (kWhole) {
+        return load_vec<IO, N>(p);
+    } else {
+        Vec<IO, N> v;
 #pragma unroll
-    for (int j = 0; j < N; ++j) v.x[j] = j < left ? p[j] : from_f<IO>(0.f);
-    return v;
+        for (int j = 0; j < N; ++j) v.x[j] = j < left ? p[j] : from_f<IO>(0.f);
+        return v;
+    }
 }
 template <typename IO, int N, bool kWhole>
 __device__ __forceinline__ void put(IO* p, const F2 (&f)[N / 2], int left) {
@@ -102,6 +105,57 @@ __device__ __forceinline__ void load_weights(const float* w, const float* bias, 
     }
 }
 
+// A thread's next tokens of kT tensors: batches of kBatch tokens in a ring of kStages.
+constexpr int kBatch = 4, kStages = 3;
+template <typename IO, int N, bool kWhole, int kT>
+struct Ring {
+    using V = Vec<IO, N>;
+    static constexpr int kBytes = kStages * kT * kBatch * kConvThreads * (int)sizeof(V);
+    V* slot;              // the thread's first
+    const IO* at[kT];     // the next token to be fetched
+    int ask, have, n;     // batches asked for, used, in all
+
+    __device__ __forceinline__ V* place(int stage, int t, int u) {
+        return slot + ((stage * kT + t) * kBatch + u) * kConvThreads;
+    }
+    __device__ __forceinline__ void next(long long hop, int left) {
+        if (ask < n) {
+#pragma unroll
+            for (int t = 0; t < kT; ++t) {
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    V* to = place(ask % kStages, t, u);
+                    if constexpr (kWhole) copy_async<(int)sizeof(V)>(smem_u32(to), at[t], true);
+                    else *to = fetch<IO, N, false>(at[t], left);
+                    at[t] += hop;
+                }
+            }
+        }
+        ++ask;
+        copy_commit();
+    }
+    // n batches from the given tokens on
+    __device__ __forceinline__ void open(char* smem, int thread, int batches, long long hop, int left) {
+        slot = reinterpret_cast<V*>(smem) + thread;
+        ask = have = 0;
+        n = batches;
+        copy_wait<0>();
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) next(hop, left);
+    }
+    // the next batch; the one behind the last asked for is asked for
+    __device__ __forceinline__ void take(V (&v)[kT][kBatch], long long hop, int left) {
+        copy_wait<kStages - 2>();
+#pragma unroll
+        for (int t = 0; t < kT; ++t) {
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) v[t][u] = *place(have % kStages, t, u);
+        }
+        ++have;
+        next(hop, left);
+    }
+};
+
 // The block's warp and slab: slabs vary fastest, so that blocks that run together read whole rows.
 struct Where {
     long long warp, warps, tokens_block;
@@ -117,7 +171,8 @@ struct Where {
 template <typename IO, int W, int N, bool kWhole>
 __global__ void __launch_bounds__(kConvThreads)
 conv_fwd_kernel(const ConvParams<IO> p) {
-    constexpr int P = N / 2, kBatch = 8;
+    constexpr int P = N / 2;
+    __shared__ __align__(16) char smem[Ring<IO, N, kWhole, 1>::kBytes];
     const int lane = threadIdx.x, wid = threadIdx.y;
     const Where me(p.slabs, wid);
     const int c = (me.slab * 32 + lane) * N, left = p.D - c;
@@ -163,7 +218,7 @@ conv_fwd_kernel(const ConvParams<IO> p) {
                 F2 a = fma2(w[W - 1][j], now[j], bias[j]);
 #pragma unroll
                 for (int k = 0; k < W - 1; ++k) a = fma2(w[k][j], x[k][j], a);
-                y[j] = act2(a, p.act);
+                y[j] = act2<false>(a, p.act);
 #pragma unroll
                 for (int k = 0; k < W - 2; ++k) x[k][j] = x[k + 1][j];
                 x[W - 2][j] = now[j];
@@ -172,23 +227,16 @@ conv_fwd_kernel(const ConvParams<IO> p) {
             out += hop;
         };
         int i = i0;
-        if (i + kBatch <= i1) {
-            Vec<IO, N> next[kBatch];
+        Ring<IO, N, kWhole, 1> ring;
+        ring.at[0] = in;
+        ring.open(smem, wid * 32 + lane, (i1 - i0) / kBatch, hop, left);
+        for (; i + kBatch <= i1; i += kBatch) {
+            Vec<IO, N> v[1][kBatch];
+            ring.take(v, hop, left);
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) next[u] = fetch<IO, N, kWhole>(in + u * hop, left);
-            for (; i + kBatch <= i1; i += kBatch) {
-                Vec<IO, N> now[kBatch];
-#pragma unroll
-                for (int u = 0; u < kBatch; ++u) now[u] = next[u];
-                in += kBatch * hop;
-                if (i + 2 * kBatch <= i1) {
-#pragma unroll
-                    for (int u = 0; u < kBatch; ++u) next[u] = fetch<IO, N, kWhole>(in + u * hop, left);
-                }
-#pragma unroll
-                for (int u = 0; u < kBatch; ++u) step(now[u]);
-            }
+            for (int u = 0; u < kBatch; ++u) step(v[0][u]);
         }
+        in += (long long)(i - i0) * hop;
         for (; i < i1; ++i, in += hop) step(fetch<IO, N, kWhole>(in, left));
     }
 }
@@ -196,8 +244,13 @@ conv_fwd_kernel(const ConvParams<IO> p) {
 template <typename IO, int W, int N, bool kWhole>
 __global__ void __launch_bounds__(kConvThreads)
 conv_bwd_kernel(const ConvParams<IO> p) {
-    constexpr int P = N / 2, kBatch = 4;
-    __shared__ float sh[kConvWarps][32 * N];
+    constexpr int P = N / 2;
+    union Shared {
+        char ring[Ring<IO, N, kWhole, 2>::kBytes];
+        float sums[kConvWarps][32 * N];
+    };
+    __shared__ __align__(16) Shared smem;
+    auto& sh = smem.sums;
     const int lane = threadIdx.x, wid = threadIdx.y;
     const Where me(p.slabs, wid);
     const int c = (me.slab * 32 + lane) * N, left = p.D - c;
@@ -254,7 +307,7 @@ conv_bwd_kernel(const ConvParams<IO> p) {
                     F2 a = fma2(w[W - 1][j], xi[j], bias[j]), v, g;
 #pragma unroll
                     for (int k = 0; k < W - 1; ++k) a = fma2(w[k][j], x[k][j], a);
-                    act2_both(a, p.act, v, g);
+                    act2_both<false>(a, p.act, v, g);
                     d[j] = past ? f2(0.f) : mul2(d[j], g);
                     if (own) {
                         db[j] = add2(db[j], d[j]);
@@ -293,30 +346,17 @@ conv_bwd_kernel(const ConvParams<IO> p) {
             for (; i < min(i0 + W - 1, i1); ++i) any(i);
             if (i + kBatch <= i1) {  // the run's own tokens, dx of its own tokens
                 const size_t at = (size_t)sp.token(i) * p.D + c;
-                const IO *ix = p.x + at, *idy = p.dy + at;
                 IO* out = p.dx + (size_t)sp.token(i - (W - 1)) * p.D + c;
-                Vec<IO, N> nx[kBatch], ny[kBatch];
-#pragma unroll
-                for (int u = 0; u < kBatch; ++u) {
-                    nx[u] = fetch<IO, N, kWhole>(ix + u * hop, left);
-                    ny[u] = fetch<IO, N, kWhole>(idy + u * hop, left);
-                }
+                Ring<IO, N, kWhole, 2> ring;
+                ring.at[0] = p.x + at;
+                ring.at[1] = p.dy + at;
+                ring.open(smem.ring, wid * 32 + lane, (i1 - i) / kBatch, hop, left);
                 for (; i + kBatch <= i1; i += kBatch) {
-                    Vec<IO, N> cx[kBatch], cy[kBatch];
-#pragma unroll
-                    for (int u = 0; u < kBatch; ++u) { cx[u] = nx[u]; cy[u] = ny[u]; }
-                    ix += kBatch * hop;
-                    idy += kBatch * hop;
-                    if (i + 2 * kBatch <= i1) {
-#pragma unroll
-                        for (int u = 0; u < kBatch; ++u) {
-                            nx[u] = fetch<IO, N, kWhole>(ix + u * hop, left);
-                            ny[u] = fetch<IO, N, kWhole>(idy + u * hop, left);
-                        }
-                    }
+                    Vec<IO, N> v[2][kBatch];
+                    ring.take(v, hop, left);
 #pragma unroll
                     for (int u = 0; u < kBatch; ++u) {
-                        step(cx[u], cy[u], true, false);
+                        step(v[0][u], v[1][u], true, false);
                         put<IO, N, kWhole>(out, dx, left);
                         out += hop;
                     }
@@ -325,7 +365,8 @@ conv_bwd_kernel(const ConvParams<IO> p) {
             for (; i < i1 + W - 1; ++i) any(i);
         }
     }
-    // the block's runs, then one row of partial sums a block
+    // the block's runs, then one row of partial sums a block, in the rings' place
+    copy_wait<0>();
 #pragma unroll
     for (int k = 0; k <= W; ++k) {
         __syncthreads();
@@ -401,7 +442,7 @@ conv_step_kernel(const IO* __restrict__ x, const float* __restrict__ w,
         F2 a = fma2(wr[W - 1][j], win[W - 1][j], b[j]);
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) a = fma2(wr[k][j], win[k][j], a);
-        out[j] = act2(a, act);
+        out[j] = act2<false>(a, act);
     }
     put<IO, N, kWhole>(y + n * D + c, out, left);
     IO* so = state_out + n * (W - 1) * D + c;

@@ -8,6 +8,7 @@
 namespace gdr {
 
 using tc::ex2;
+using tc::smem_u32;
 
 // ---- sequences ------------------------------------------------------------------------------
 // The tokens of a call lie on one axis of `total` rows: B rows of T tokens one after the other,
@@ -96,6 +97,23 @@ __device__ __forceinline__ void load_f(const E* p, float (&f)[N]) {
     for (int i = 0; i < N; ++i) f[i] = to_f(v.x[i]);
 }
 
+// ---- asynchronous copies into shared memory ----------------------------------------------------
+template <int kBytes>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool in) {
+    const int n = in ? kBytes : 0;  // the rest of the word is zero
+    if constexpr (kBytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes), "r"(n) : "memory");
+}
+
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
 // ---- two channels in one 64-bit register pair ---------------------------------------------------
 struct F2 {
     uint64_t v;
@@ -161,25 +179,37 @@ __device__ __forceinline__ F2 exp2ch(F2 g) {
 }
 
 // ---- activations -------------------------------------------------------------------------------
-// sigmoid(x) = 1 / (1 + e^-x).  At the lower clamp e^-x is above 2^126, whose reciprocal the
-// hardware flushes to zero: so it is for all x below, and x sigmoid(x) is -0 (NaN for -inf, as
-// -inf times 0 is).  Exponential and reciprocal are off by one step of fp32 each.
+// sigmoid(x) = 1 / (1 + e^-x).
+// kFine: exponential and reciprocal are off by one step of fp32 each.  At the lower clamp e^-x is
+// above 2^126, whose reciprocal the hardware flushes to zero: so it is for all x below, and
+// x sigmoid(x) is -0 (NaN for -inf, as -inf times 0 is).
+// Else e^-x is off by another |x| half steps, from the rounded product with log2 e: no more than a
+// last-place error of x itself would do, for an x that is a rounded sum or a result that is rounded
+// to bf16.  It needs no clamps (infinities go the right way) and half the instructions.
+template <bool kFine>
 __device__ __forceinline__ F2 sigmoid2(F2 x) {
+    if constexpr (!kFine) {
+        const F2 t = mul2(x, f2(-1.44269504f));
+        const F2 s = add2(f2(ex2(t.lo()), ex2(t.hi())), f2(1.f));
+        return f2(rcp_ftz(s.lo()), rcp_ftz(s.hi()));
+    }
     const F2 c = f2(min_nan(max_nan(-x.lo(), -88.f), 87.7f), min_nan(max_nan(-x.hi(), -88.f), 87.7f));
     const F2 s = add2(exp_in_range(c), f2(1.f));
     return f2(rcp_ftz(s.lo()), rcp_ftz(s.hi()));
 }
 
+template <bool kFine>
 __device__ __forceinline__ F2 act2(F2 x, int act) {
     if (act == GDR_ACT_NONE) return x;
-    const F2 s = sigmoid2(x);
+    const F2 s = sigmoid2<kFine>(x);
     return act == GDR_ACT_SILU ? mul2(x, s) : s;
 }
 
 // act(x) and act'(x)
+template <bool kFine>
 __device__ __forceinline__ void act2_both(F2 x, int act, F2& a, F2& d) {
     if (act == GDR_ACT_NONE) { a = x; d = f2(1.f); return; }
-    const F2 s = sigmoid2(x), rest = fma2(s, f2(-1.f), f2(1.f));
+    const F2 s = sigmoid2<kFine>(x), rest = fma2(s, f2(-1.f), f2(1.f));
     if (act == GDR_ACT_SILU) {
         a = mul2(x, s);
         d = mul2(s, fma2(x, rest, f2(1.f)));

@@ -26,22 +26,21 @@ struct Deal {
     int part_rows;     // rows of partial sums
 };
 
-Deal deal(const gdr_norm_args& a, int groups, int per_slot) {
-    const long long rows = (long long)a.B * a.T * a.H;
+Deal deal(const gdr_norm_args& a, int groups, int resident, int per_slot) {
+    const long long rows = (long long)a.B * a.T * a.H, most_blocks = 148LL * resident;
     Deal d;
-    // 148 * 4 blocks fill the GPU at the kernels' register use; a slot takes at least
-    // `per_slot` rows where there are so many, so that partial sums stay a small share of the
-    // traffic
+    // the blocks fill the GPU once; a slot takes at least `per_slot` rows where there are so many,
+    // so that partial sums stay a small share of the traffic
     if (a.H <= groups) {
         d.used = groups / a.H * a.H;
-        long long b = (rows + (long long)d.used * per_slot - 1) / ((long long)d.used * per_slot);
-        d.blocks = (int)(b < 1 ? 1 : b > 148 * 4 ? 148 * 4 : b);
+        const long long per = (long long)d.used * per_slot, b = (rows + per - 1) / per;
+        d.blocks = (int)(b < 1 ? 1 : b > most_blocks ? most_blocks : b);
         d.slots = (long long)d.blocks * d.used;
         d.part_rows = d.blocks;
     } else {
         d.used = groups;
         long long per_head = rows / a.H / per_slot;
-        const long long most = 148LL * 4 * groups / a.H;
+        const long long most = most_blocks * groups / a.H;
         if (per_head > most) per_head = most;
         if (per_head < 1) per_head = 1;
         d.slots = per_head * a.H;
@@ -51,18 +50,18 @@ Deal deal(const gdr_norm_args& a, int groups, int per_slot) {
     return d;
 }
 
+// The row's centred values and 1 / deviation.
 template <typename S>
-__device__ __forceinline__ void token_stats(const Pairs<S>& x, int l, int d, int center, float eps,
-                                            float& mean, float& rstd) {
+__device__ __forceinline__ float token_stats(Pairs<S>& x, int l, int d, int center, float eps) {
     const float inv = 1.f / d;
-    mean = center ? group_sum<S::LPG>(lane_sum<S>(x)) * inv : 0.f;
-    rstd = 1.f / sqrtf(group_sum<S::LPG>(lane_squares<S>(x, mean, l, d)) * inv + eps);
+    if (center) centre<S>(x, group_sum<S::LPG>(lane_sum<S>(x)) * inv, l, d);
+    return rsqrtf(group_sum<S::LPG>(lane_squares<S>(x)) * inv + eps);
 }
 
 template <typename S>
-__global__ void __launch_bounds__(kNormThreads)
+__global__ void __launch_bounds__(kNormThreads, S::kResident)
 norm_token_fwd(const NormParams<typename S::IO> p, int used, long long slots) {
-    constexpr int kAhead = S::NV == 1 ? 2 : 1;   // rows loaded ahead of the one in work
+    extern __shared__ __align__(16) char smem[];
     const int g = threadIdx.x / S::LPG, l = threadIdx.x % S::LPG;
     const long long slot = (long long)blockIdx.x * used + g;
     const bool on = g < used && slot < slots;
@@ -70,36 +69,35 @@ norm_token_fwd(const NormParams<typename S::IO> p, int used, long long slots) {
     const Pairs<S> w = load_affine<S>(p.w, 1.f, head, l, p.d, p.shared);
     const Pairs<S> b = load_affine<S>(p.b, 0.f, head, l, p.d, p.shared);
     const bool gate = p.z != nullptr;
-    Raw<S> x[kAhead], z[kAhead];
-    auto fetch = [&](long long r0, int i) {
-        const bool in = on && r0 + g < p.rows;
-        const size_t at = (size_t)(in ? r0 + g : 0) * p.d;
-        x[i] = load_row<S>(p.x + at, l, p.d, in);
-        if (gate) z[i] = load_row<S>(p.z + at, l, p.d, in);
+    const typename S::IO* const src[2] = {p.x, p.z};
+    Ring<S, 2> ring(smem, l, p.d, gate ? 2 : 1);
+    const size_t hop = (size_t)slots * p.d;
+    long long ask_row = slot;
+    size_t ask_at = (size_t)slot * p.d, at = ask_at;
+    auto ask = [&] {
+        ring.ask(src, ask_at, on && ask_row < p.rows);
+        ask_row += slots;
+        ask_at += hop;
     };
+#pragma unroll
+    for (int i = 0; i < S::kStages - 1; ++i) ask();
     // every lane takes part in the group sums until the block's last row
-    const long long first = (long long)blockIdx.x * used;
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) fetch(first + i * slots, i);
-    for (long long r0 = first; r0 < p.rows; r0 += kAhead * slots) {
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const long long r = r0 + i * slots;
-            const Pairs<S> f = widen<S>(x[i]);
-            const Raw<S> zz = z[i];
-            fetch(r + kAhead * slots, i);
-            float mean, rstd;
-            token_stats<S>(f, l, p.d, p.center, p.eps, mean, rstd);
-            if (on && r + g < p.rows)
-                store_row<S>(p.y + (size_t)(r + g) * p.d, l, p.d,
-                             norm_rows<S>(f, w, b, gate, zz, mean, rstd, p.act));
-        }
+    for (long long r0 = (long long)blockIdx.x * used; r0 < p.rows; r0 += slots, at += hop) {
+        Raw<S> raw[2];
+        ring.take(raw);
+        ask();
+        Pairs<S> x = widen<S>(raw[0]);
+        const float rstd = token_stats<S>(x, l, p.d, p.center, p.eps);
+        if (on && r0 + g < p.rows)
+            store_row<S>(p.y + at, l, p.d, norm_rows<S>(x, w, b, gate, raw[1], rstd, p.act));
     }
+    copy_wait<0>();
 }
 
 template <typename S>
-__global__ void __launch_bounds__(kNormThreads)
+__global__ void __launch_bounds__(kNormThreads, S::kResident)
 norm_token_bwd(const NormParams<typename S::IO> p, int used, long long slots) {
+    extern __shared__ __align__(16) char smem[];
     const int g = threadIdx.x / S::LPG, l = threadIdx.x % S::LPG;
     const long long slot = (long long)blockIdx.x * used + g;
     const bool on = g < used && slot < slots;
@@ -109,36 +107,41 @@ norm_token_bwd(const NormParams<typename S::IO> p, int used, long long slots) {
     Pairs<S> dw = fill<S>(0.f), db = fill<S>(0.f);
     const bool gate = p.z != nullptr;
     const float inv = 1.f / p.d;
-    Raw<S> x, dy, z;
-    auto fetch = [&](long long r0) {
-        const bool in = on && r0 + g < p.rows;
-        const size_t at = (size_t)(in ? r0 + g : 0) * p.d;
-        x = load_row<S>(p.x + at, l, p.d, in);
-        dy = load_row<S>(p.dy + at, l, p.d, in);
-        if (gate) z = load_row<S>(p.z + at, l, p.d, in);
+    const typename S::IO* const src[3] = {p.x, p.dy, p.z};
+    Ring<S, 3> ring(smem, l, p.d, gate ? 3 : 2);
+    const size_t hop = (size_t)slots * p.d;
+    long long ask_row = slot;
+    size_t ask_at = (size_t)slot * p.d, at = ask_at;
+    auto ask = [&] {
+        ring.ask(src, ask_at, on && ask_row < p.rows);
+        ask_row += slots;
+        ask_at += hop;
     };
-    const long long first = (long long)blockIdx.x * used;
-    fetch(first);
-    for (long long r0 = first; r0 < p.rows; r0 += slots) {
-        const Raw<S> cx = x, cdy = dy, cz = z;
-        fetch(r0 + slots);
-        float mean, rstd;
-        token_stats<S>(widen<S>(cx), l, p.d, p.center, p.eps, mean, rstd);
-        if (!on || r0 + g >= p.rows) rstd = 0.f;  // zeros throughout: nothing for the sums
-        const Back<S> o = back_rows<S, true>(cx, cdy, cz, gate, w, b, mean, rstd, p.act, dw, db);
+#pragma unroll
+    for (int i = 0; i < S::kStages - 1; ++i) ask();
+    for (long long r0 = (long long)blockIdx.x * used; r0 < p.rows; r0 += slots, at += hop) {
+        Raw<S> raw[3];
+        ring.take(raw);
+        ask();
+        const bool in = on && r0 + g < p.rows;
+        Pairs<S> x = widen<S>(raw[0]);
+        float rstd = token_stats<S>(x, l, p.d, p.center, p.eps);
+        if (!in) rstd = 0.f;  // zeros throughout: nothing for the sums
+        const Back<S> o = back_rows<S, true>(x, raw[1], raw[2], gate, w, b, rstd, p.act, dw, db);
         const float mq = p.center ? group_sum<S::LPG>(o.s1) * inv : 0.f;
         const float mqn = group_sum<S::LPG>(o.s2) * inv;
-        if (on && r0 + g < p.rows) {
-            const size_t at = (size_t)(r0 + g) * p.d;
+        if (in) {
             store_row<S>(p.dx + at, l, p.d, back_dx<S>(o, rstd, mq, mqn));
             if (gate) store_row<S>(p.dz + at, l, p.d, o.dz);
         }
     }
+    copy_wait<0>();
     if (!p.part) return;
 
     // sums over the block's lane groups of one head (of all, for a shared weight)
     constexpr int kCh = S::LPG * S::VEC;
-    __shared__ float sh[S::kGroups * kCh];
+    float* const sh = reinterpret_cast<float*>(smem);  // in the rings' place
+    static_assert(sizeof(float) * S::kGroups * kCh <= Ring<S, 3>::kBytes, "the rings are larger");
     const int heads = p.shared ? 1 : p.H <= S::kGroups ? p.H : 0;
     for (int which = 0; which < 2; ++which) {
 #pragma unroll
@@ -201,30 +204,36 @@ constexpr int kPerSlot = 8;
 struct TokenFwd {
     template <typename S>
     static void go(const gdr_norm_args& a, const NormPtrs& x, cudaStream_t st) {
-        const Deal d = deal(a, S::kGroups, 1);
-        norm_token_fwd<S><<<d.blocks, kNormThreads, 0, st>>>(norm_params<typename S::IO>(a, x),
-                                                             d.used, d.slots);
+        const Deal d = deal(a, S::kGroups, S::kResident, 1);
+        norm_launch<Ring<S, 2>::kBytes>(norm_token_fwd<S>, d.blocks, st,
+                                        norm_params<typename S::IO>(a, x), d.used, d.slots);
     }
 };
 
 struct TokenBwd {
     template <typename S>
     static void go(const gdr_norm_args& a, const NormPtrs& x, cudaStream_t st) {
-        const Deal d = deal(a, S::kGroups, kPerSlot);
+        const Deal d = deal(a, S::kGroups, S::kResident, kPerSlot);
         auto p = norm_params<typename S::IO>(a, x);
         if (!x.dw && !x.db) p.part = nullptr;
-        norm_token_bwd<S><<<d.blocks, kNormThreads, 0, st>>>(p, d.used, d.slots);
+        norm_launch<Ring<S, 3>::kBytes>(norm_token_bwd<S>, d.blocks, st, p, d.used, d.slots);
         if (p.part) launch_norm_reduce(a, x.ws, d.part_rows, x.dw, x.db, st);
+    }
+};
+
+struct TokenBwdSize {
+    template <typename S>
+    static void go(const gdr_norm_args& a, const NormPtrs& x, cudaStream_t) {
+        *reinterpret_cast<int*>(x.ws) = deal(a, S::kGroups, S::kResident, kPerSlot).part_rows;
     }
 };
 
 }  // namespace
 
-gdr_status launch_norm_reduce(const gdr_norm_args& a, const float* part, int rows, float* dw,
+void launch_norm_reduce(const gdr_norm_args& a, const float* part, int rows, float* dw,
                               float* db, cudaStream_t st) {
     const int H = a.shared_weight ? 1 : a.H;
     norm_reduce_kernel<<<dim3((a.d + 31) / 32, H, 2), 1024, 0, st>>>(part, rows, H, a.d, dw, db);
-    return cudaGetLastError() == cudaSuccess ? GDR_OK : GDR_ERR_CUDA;
 }
 
 bool norm_supported(const gdr_norm_args& a) {
@@ -238,8 +247,11 @@ size_t norm_fwd_workspace(const gdr_norm_args& a) {
 
 size_t norm_bwd_workspace(const gdr_norm_args& a) {
     if (a.per_sequence) return norm_seq_bwd_workspace(a);
-    const Deal d = deal(a, norm_groups(a), kPerSlot);
-    return align_up(sizeof(float) * 2 * (size_t)d.part_rows * (a.shared_weight ? 1 : a.H) * a.d, 256);
+    int part_rows = 0;
+    NormPtrs x{};
+    x.ws = reinterpret_cast<float*>(&part_rows);
+    norm_shape<TokenBwdSize>(a, x, nullptr);
+    return align_up(sizeof(float) * 2 * (size_t)part_rows * (a.shared_weight ? 1 : a.H) * a.d, 256);
 }
 
 gdr_status launch_norm_fwd(const gdr_norm_args& a, const NormPtrs& x, cudaStream_t st) {

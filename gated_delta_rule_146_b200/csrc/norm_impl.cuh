@@ -20,6 +20,11 @@ struct Shape {
     static constexpr bool kWhole = kWhole_;
     static constexpr int VEC = kWhole ? 16 / (int)sizeof(IO) : 2, LPG = LPG_, NV = NV_;
     static constexpr int kGroups = kNormThreads / LPG;  // heads a block holds at once
+    // results in bf16, or of rounded sums, do not show the coarser sigmoid's error (layer.cuh)
+    static constexpr bool kFine = sizeof(IO) == 4;
+    // rows of a lane group on their way at once, and blocks on an SM that the registers allow
+    static constexpr int kStages = NV == 1 ? 3 : 2;
+    static constexpr int kResident = NV == 1 ? 3 : NV == 2 ? 2 : 1;
 };
 
 template <typename IO>
@@ -71,6 +76,54 @@ __device__ __forceinline__ Raw<S> load_row(const typename S::IO* p, int l, int d
     }
     return r;
 }
+
+// A lane's next rows of kT tensors, on their way into shared memory of its own: no registers, no
+// barrier.  Tensors behind the first `used` are left out.
+template <typename S, int kT>
+struct Ring {
+    using V = Vec<typename S::IO, S::VEC>;
+    static constexpr int kBytes = S::kStages * kT * S::NV * kNormThreads * (int)sizeof(V);
+    V* slot;
+    int l, d, used, put, got;
+
+    __device__ __forceinline__ Ring(char* smem, int l_, int d_, int used_)
+        : slot(reinterpret_cast<V*>(smem) + threadIdx.x), l(l_), d(d_), used(used_), put(0), got(0) {}
+    __device__ __forceinline__ V* place(int stage, int t, int k) {
+        return slot + ((stage * kT + t) * S::NV + k) * kNormThreads;
+    }
+    // asks for the row at element `at` of every tensor (zeros if not `on`)
+    __device__ __forceinline__ void ask(const typename S::IO* const (&base)[kT], size_t at, bool on) {
+#pragma unroll
+        for (int t = 0; t < kT; ++t) {
+            if (t >= used) break;
+            if constexpr (S::kWhole) {
+#pragma unroll
+                for (int k = 0; k < S::NV; ++k) {
+                    const int c = (k * S::LPG + l) * S::VEC;
+                    const bool in = on && c < d;
+                    copy_async<16>(smem_u32(place(put, t, k)), base[t] + (in ? at + c : 0), in);
+                }
+            } else {
+                const Raw<S> r = load_row<S>(base[t] + at, l, d, on);
+#pragma unroll
+                for (int k = 0; k < S::NV; ++k) *place(put, t, k) = r.v[k];
+            }
+        }
+        copy_commit();
+        put = put == S::kStages - 1 ? 0 : put + 1;
+    }
+    // the row asked for longest ago
+    __device__ __forceinline__ void take(Raw<S> (&r)[kT]) {
+        copy_wait<S::kStages - 2>();
+#pragma unroll
+        for (int t = 0; t < kT; ++t) {
+            if (t >= used) break;
+#pragma unroll
+            for (int k = 0; k < S::NV; ++k) r[t].v[k] = *place(got, t, k);
+        }
+        got = got == S::kStages - 1 ? 0 : got + 1;
+    }
+};
 
 template <typename S>
 __device__ __forceinline__ Pairs<S> widen(const Raw<S>& r) {
@@ -130,13 +183,6 @@ __device__ __forceinline__ Pairs<S> load_affine(const float* w, float none, int 
     return f;
 }
 
-// One where the lane has a channel, else zero.
-template <typename S>
-__device__ __forceinline__ F2 mask_of(int k, int j, int l, int d) {
-    const int c = (k * S::LPG + l) * S::VEC + 2 * j;
-    return f2(c < d ? 1.f : 0.f, c + 1 < d ? 1.f : 0.f);
-}
-
 template <typename S>
 __device__ __forceinline__ float lane_sum(const Pairs<S>& x) {
     F2 s = x.f[0][0];
@@ -149,60 +195,70 @@ __device__ __forceinline__ float lane_sum(const Pairs<S>& x) {
     return s.lo() + s.hi();
 }
 
-// The lane's sum of squares about the mean.
+// x - mean; zeros stay where there are no channels
 template <typename S>
-__device__ __forceinline__ float lane_squares(const Pairs<S>& x, float mean, int l, int d) {
+__device__ __forceinline__ void centre(Pairs<S>& x, float mean, int l, int d) {
+#pragma unroll
+    for (int k = 0; k < S::NV; ++k) {
+        const int c = (k * S::LPG + l) * S::VEC;
+#pragma unroll
+        for (int j = 0; j < S::VEC / 2; ++j) {
+            const F2 m = S::kWhole ? f2(c < d ? -mean : 0.f)
+                                   : f2(c < d ? -mean : 0.f, c + 1 < d ? -mean : 0.f);
+            x.f[k][j] = add2(x.f[k][j], m);
+        }
+    }
+}
+
+template <typename S>
+__device__ __forceinline__ float lane_squares(const Pairs<S>& x) {
     F2 s = f2(0.f);
 #pragma unroll
     for (int k = 0; k < S::NV; ++k) {
 #pragma unroll
-        for (int j = 0; j < S::VEC / 2; ++j) {
-            const F2 t = mul2(add2(x.f[k][j], f2(-mean)), mask_of<S>(k, j, l, d));
-            s = fma2(t, t, s);
-        }
+        for (int j = 0; j < S::VEC / 2; ++j) s = fma2(x.f[k][j], x.f[k][j], s);
     }
     return s.lo() + s.hi();
 }
 
-// y from x: n = (x - mean) rstd, u = n w + b, y = u act(z) or act(u)
+// y from the centred x: n = x rstd, u = n w + b, y = u act(z) or act(u)
 template <typename S>
 __device__ __forceinline__ Pairs<S> norm_rows(const Pairs<S>& x, const Pairs<S>& w, const Pairs<S>& b,
-                                              bool gate, const Raw<S>& z, float mean, float rstd,
-                                              int act) {
+                                              bool gate, const Raw<S>& z, float rstd, int act) {
     Pairs<S> y;
-    const F2 m = f2(-mean), r = f2(rstd);
+    const F2 r = f2(rstd);
 #pragma unroll
     for (int k = 0; k < S::NV; ++k) {
 #pragma unroll
         for (int j = 0; j < S::VEC / 2; ++j) {
-            const F2 n = mul2(add2(x.f[k][j], m), r), u = fma2(n, w.f[k][j], b.f[k][j]);
-            y.f[k][j] = gate ? mul2(u, act2(pair_of(z.v[k], j), act)) : act2(u, act);
+            const F2 u = fma2(mul2(x.f[k][j], r), w.f[k][j], b.f[k][j]);
+            y.f[k][j] = gate ? mul2(u, act2<S::kFine>(pair_of(z.v[k], j), act)) : act2<S::kFine>(u, act);
         }
     }
     return y;
 }
 
-// What the backward has of a row: n, q = du w, dz; du joins the sums for dw and db if kSums.
+// What the backward has of a row (x centred): n, q = du w, dz; du joins the sums for dw and db if kSums.
 template <typename S>
 struct Back {
     Pairs<S> n, q, dz;
     float s1, s2;   // the lane's sums of q and q n
 };
 template <typename S, bool kSums>
-__device__ __forceinline__ Back<S> back_rows(const Raw<S>& x, const Raw<S>& dy, const Raw<S>& z,
-                                             bool gate, const Pairs<S>& w, const Pairs<S>& b, float mean,
-                                             float rstd, int act, Pairs<S>& dw, Pairs<S>& db) {
+__device__ __forceinline__ Back<S> back_rows(const Pairs<S>& x, const Raw<S>& dy, const Raw<S>& z,
+                                             bool gate, const Pairs<S>& w, const Pairs<S>& b, float rstd,
+                                             int act, Pairs<S>& dw, Pairs<S>& db) {
     Back<S> o;
-    const F2 m = f2(-mean), r = f2(rstd);
+    const F2 r = f2(rstd);
     F2 s1 = f2(0.f), s2 = f2(0.f);
 #pragma unroll
     for (int k = 0; k < S::NV; ++k) {
 #pragma unroll
         for (int j = 0; j < S::VEC / 2; ++j) {
-            const F2 n = mul2(add2(pair_of(x.v[k], j), m), r), g = pair_of(dy.v[k], j);
+            const F2 n = mul2(x.f[k][j], r), g = pair_of(dy.v[k], j);
             const F2 u = fma2(n, w.f[k][j], b.f[k][j]);
             F2 a, da, du;
-            act2_both(gate ? pair_of(z.v[k], j) : u, act, a, da);
+            act2_both<S::kFine>(gate ? pair_of(z.v[k], j) : u, act, a, da);
             if (gate) {
                 o.dz.f[k][j] = mul2(mul2(g, u), da);
                 du = mul2(g, a);
@@ -265,9 +321,22 @@ inline int norm_groups(const gdr_norm_args& a) {
 }
 
 template <typename Op>
-gdr_status norm_dispatch(const gdr_norm_args& a, const NormPtrs& x, cudaStream_t st) {
+void norm_shape(const gdr_norm_args& a, const NormPtrs& x, cudaStream_t st) {
     if (a.io_dtype == GDR_BF16) norm_dispatch_io<Op, __nv_bfloat16>(a, x, st);
     else norm_dispatch_io<Op, float>(a, x, st);
+}
+
+// Launches with the shared memory of a ring.
+template <int kBytes, typename... P, typename... A>
+void norm_launch(void (*kernel)(P...), long long blocks, cudaStream_t st, A... args) {
+    if (kBytes > 40 << 10)  // (with the kernels' own arrays, above what needs no asking for)
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    kernel<<<(unsigned)blocks, kNormThreads, kBytes, st>>>(args...);
+}
+
+template <typename Op>
+gdr_status norm_dispatch(const gdr_norm_args& a, const NormPtrs& x, cudaStream_t st) {
+    norm_shape<Op>(a, x, st);
     return cudaGetLastError() == cudaSuccess ? GDR_OK : GDR_ERR_CUDA;
 }
 
@@ -297,7 +366,7 @@ NormParams<IO> norm_params(const gdr_norm_args& a, const NormPtrs& x) {
 }
 
 // Sums part[0 .. rows)[2][H][d] over the rows (and the heads of a shared weight) into dw, db.
-gdr_status launch_norm_reduce(const gdr_norm_args& a, const float* part, int rows, float* dw,
+void launch_norm_reduce(const gdr_norm_args& a, const float* part, int rows, float* dw,
                               float* db, cudaStream_t st);
 
 gdr_status launch_norm_seq_fwd(const gdr_norm_args& a, const NormPtrs& p, cudaStream_t st);

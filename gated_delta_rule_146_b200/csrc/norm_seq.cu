@@ -70,7 +70,10 @@ norm_seq_stats(const NormParams<typename S::IO> p) {
 #pragma unroll
         for (int i = 0; i < kHold<S>; ++i) {
             const int t = t0 + g + i * S::kGroups;
-            if (t >= lo && t < hi) v += lane_squares<S>(widen<S>(x[i]), mean, l, p.d);
+            if (t < lo || t >= hi) continue;
+            Pairs<S> f = widen<S>(x[i]);
+            centre<S>(f, mean, l, p.d);
+            v += lane_squares<S>(f);
         }
         v = block_sum(v, sh);
         if (threadIdx.x == 0)
@@ -111,7 +114,7 @@ norm_seq_join_stats(Seqs q, int H, int d, int tokens, float eps, const float2* _
         if (lane + o < 32) join(nb, mb, sb);
     }
     if (lane == 0)
-        stats[unit] = make_float2(mean, 1.f / sqrtf((n > 0.f ? m2 / n : 0.f) + eps));
+        stats[unit] = make_float2(mean, rsqrtf((n > 0.f ? m2 / n : 0.f) + eps));
 }
 
 // The sequence of token t, not before s.
@@ -120,14 +123,11 @@ __device__ __forceinline__ int seq_from(const Seqs& q, int s, int t) {
     return s;
 }
 
-// Rows a lane group loads before it uses them.
-template <typename S>
-constexpr int kBatch = S::NV == 1 ? 4 : S::NV == 2 ? 2 : 1;
-
 // The second pass visits the tiles backwards: the first one's last tiles are still in L2.
 template <typename S>
-__global__ void __launch_bounds__(kNormThreads)
+__global__ void __launch_bounds__(kNormThreads, S::kResident)
 norm_seq_apply(const NormParams<typename S::IO> p, int tokens) {
+    extern __shared__ __align__(16) char smem[];
     const int g = threadIdx.x / S::LPG, l = threadIdx.x % S::LPG;
     const int block = gridDim.x - 1 - blockIdx.x, tile = block / p.H, h = block % p.H;
     const int t0 = (int)min((long long)p.q.total, (long long)tile * tokens);
@@ -135,35 +135,40 @@ norm_seq_apply(const NormParams<typename S::IO> p, int tokens) {
     const Pairs<S> w = load_affine<S>(p.w, 1.f, h, l, p.d, p.shared);
     const Pairs<S> b = load_affine<S>(p.b, 0.f, h, l, p.d, p.shared);
     const bool gate = p.z != nullptr;
+    const typename S::IO* const src[2] = {p.x, p.z};
+    Ring<S, 2> ring(smem, l, p.d, gate ? 2 : 1);
+    const size_t hop = (size_t)S::kGroups * p.H * p.d;
+    int ask_t = t0 + g;
+    size_t ask_at = ((size_t)ask_t * p.H + h) * p.d, at = ask_at;
+    auto ask = [&] {
+        ring.ask(src, ask_at, ask_t < t1);
+        ask_t += S::kGroups;
+        ask_at += hop;
+    };
+#pragma unroll
+    for (int i = 0; i < S::kStages - 1; ++i) ask();
     int s = t0 + g < t1 ? p.q.of(t0 + g) : 0;
-    for (int t = t0 + g; t < t1; t += kBatch<S> * S::kGroups) {
-        Raw<S> x[kBatch<S>], z[kBatch<S>];
-#pragma unroll
-        for (int i = 0; i < kBatch<S>; ++i) {
-            const int ti = t + i * S::kGroups;
-            const size_t at = ((size_t)(ti < t1 ? ti : t) * p.H + h) * p.d;
-            x[i] = load_row<S>(p.x + at, l, p.d, true);
-            if (gate) z[i] = load_row<S>(p.z + at, l, p.d, true);
-        }
-#pragma unroll
-        for (int i = 0; i < kBatch<S>; ++i) {
-            const int ti = t + i * S::kGroups;
-            if (ti >= t1) break;
-            s = seq_from(p.q, s, ti);
-            const float2 st = __ldg(reinterpret_cast<const float2*>(p.stats) + (size_t)s * p.H + h);
-            store_row<S>(p.y + ((size_t)ti * p.H + h) * p.d, l, p.d,
-                         norm_rows<S>(widen<S>(x[i]), w, b, gate, z[i], st.x, st.y, p.act));
-        }
+    for (int t = t0 + g; t < t1; t += S::kGroups, at += hop) {
+        Raw<S> raw[2];
+        ring.take(raw);
+        ask();
+        s = seq_from(p.q, s, t);
+        const float2 st = __ldg(reinterpret_cast<const float2*>(p.stats) + (size_t)s * p.H + h);
+        Pairs<S> x = widen<S>(raw[0]);
+        centre<S>(x, st.x, l, p.d);
+        store_row<S>(p.y + at, l, p.d, norm_rows<S>(x, w, b, gate, raw[1], st.y, p.act));
     }
+    copy_wait<0>();
 }
 
 // First pass of the backward: dz, the tile's sums for dw and db, and per piece the sums of q
 // and q n.
 template <typename S>
-__global__ void __launch_bounds__(kNormThreads)
+__global__ void __launch_bounds__(kNormThreads, S::kResident)
 norm_seq_bwd_sums(const NormParams<typename S::IO> p, int tokens, float2* __restrict__ pieces) {
+    extern __shared__ __align__(16) char smem[];
     constexpr int kCh = S::LPG * S::VEC;
-    __shared__ float sh[kNormWarps], shw[S::kGroups * kCh];
+    __shared__ float sh[kNormWarps];
     const int g = threadIdx.x / S::LPG, l = threadIdx.x % S::LPG;
     const int tile = blockIdx.x / p.H, h = blockIdx.x % p.H;
     if (blockIdx.x == 0) check_cu(p.q, p.status, threadIdx.x, kNormThreads);
@@ -173,6 +178,9 @@ norm_seq_bwd_sums(const NormParams<typename S::IO> p, int tokens, float2* __rest
     const Pairs<S> b = load_affine<S>(p.b, 0.f, h, l, p.d, p.shared);
     Pairs<S> dw = fill<S>(0.f), db = fill<S>(0.f);
     const bool gate = p.z != nullptr;
+    const typename S::IO* const src[3] = {p.x, p.dy, p.z};
+    Ring<S, 3> ring(smem, l, p.d, gate ? 3 : 2);
+    const size_t hop = (size_t)S::kGroups * p.H * p.d;
     for (int s = t0 < t1 ? p.q.of(t0) : p.q.n; s < p.q.n; ++s) {
         const int sb = p.q.begin(s), se = p.q.end(s);
         if (sb >= t1) break;
@@ -180,31 +188,35 @@ norm_seq_bwd_sums(const NormParams<typename S::IO> p, int tokens, float2* __rest
         if (lo >= hi) continue;
         const float2 st = __ldg(reinterpret_cast<const float2*>(p.stats) + (size_t)s * p.H + h);
         float s1 = 0.f, s2 = 0.f;
-        for (int t = lo + g; t < hi; t += kBatch<S> * S::kGroups) {
-            Raw<S> x[kBatch<S>], dy[kBatch<S>], z[kBatch<S>];
+        int ask_t = lo + g;
+        size_t ask_at = ((size_t)ask_t * p.H + h) * p.d, at = ask_at;
+        auto ask = [&] {
+            ring.ask(src, ask_at, ask_t < hi);
+            ask_t += S::kGroups;
+            ask_at += hop;
+        };
+        copy_wait<0>();
+        ring.put = ring.got = 0;
 #pragma unroll
-            for (int i = 0; i < kBatch<S>; ++i) {
-                const int ti = t + i * S::kGroups;
-                const size_t at = ((size_t)(ti < hi ? ti : t) * p.H + h) * p.d;
-                x[i] = load_row<S>(p.x + at, l, p.d, true);
-                dy[i] = load_row<S>(p.dy + at, l, p.d, true);
-                if (gate) z[i] = load_row<S>(p.z + at, l, p.d, true);
-            }
-#pragma unroll
-            for (int i = 0; i < kBatch<S>; ++i) {
-                const int ti = t + i * S::kGroups;
-                if (ti >= hi) break;
-                const Back<S> o = back_rows<S, true>(x[i], dy[i], z[i], gate, w, b, st.x, st.y, p.act,
-                                                     dw, db);
-                s1 += o.s1;
-                s2 += o.s2;
-                if (gate) store_row<S>(p.dz + ((size_t)ti * p.H + h) * p.d, l, p.d, o.dz);
-            }
+        for (int i = 0; i < S::kStages - 1; ++i) ask();
+        for (int t = lo + g; t < hi; t += S::kGroups, at += hop) {
+            Raw<S> raw[3];
+            ring.take(raw);
+            ask();
+            Pairs<S> x = widen<S>(raw[0]);
+            centre<S>(x, st.x, l, p.d);
+            const Back<S> o = back_rows<S, true>(x, raw[1], raw[2], gate, w, b, st.y, p.act, dw, db);
+            s1 += o.s1;
+            s2 += o.s2;
+            if (gate) store_row<S>(p.dz + at, l, p.d, o.dz);
         }
         s1 = block_sum(s1, sh);
         s2 = block_sum(s2, sh);
         if (threadIdx.x == 0) pieces[((size_t)tile + s) * p.H + h] = make_float2(s1, s2);
     }
+    copy_wait<0>();
+    float* const shw = reinterpret_cast<float*>(smem);  // in the rings' place
+    static_assert(sizeof(float) * S::kGroups * kCh <= Ring<S, 3>::kBytes, "the rings are larger");
     if (!p.part) return;
     for (int which = 0; which < 2; ++which) {
 #pragma unroll
@@ -253,9 +265,10 @@ norm_seq_join_sums(Seqs q, int H, int d, int tokens, int center, const float2* _
 }
 
 template <typename S>
-__global__ void __launch_bounds__(kNormThreads)
+__global__ void __launch_bounds__(kNormThreads, S::kResident)
 norm_seq_bwd_apply(const NormParams<typename S::IO> p, int tokens,
                    const float2* __restrict__ means) {
+    extern __shared__ __align__(16) char smem[];
     const int g = threadIdx.x / S::LPG, l = threadIdx.x % S::LPG;
     const int block = gridDim.x - 1 - blockIdx.x, tile = block / p.H, h = block % p.H;
     const int t0 = (int)min((long long)p.q.total, (long long)tile * tokens);
@@ -264,29 +277,32 @@ norm_seq_bwd_apply(const NormParams<typename S::IO> p, int tokens,
     const Pairs<S> b = load_affine<S>(p.b, 0.f, h, l, p.d, p.shared);
     Pairs<S> none;
     const bool gate = p.z != nullptr;
+    const typename S::IO* const src[3] = {p.x, p.dy, p.z};
+    Ring<S, 3> ring(smem, l, p.d, gate ? 3 : 2);
+    const size_t hop = (size_t)S::kGroups * p.H * p.d;
+    int ask_t = t0 + g;
+    size_t ask_at = ((size_t)ask_t * p.H + h) * p.d, at = ask_at;
+    auto ask = [&] {
+        ring.ask(src, ask_at, ask_t < t1);
+        ask_t += S::kGroups;
+        ask_at += hop;
+    };
+#pragma unroll
+    for (int i = 0; i < S::kStages - 1; ++i) ask();
     int s = t0 + g < t1 ? p.q.of(t0 + g) : 0;
-    for (int t = t0 + g; t < t1; t += kBatch<S> * S::kGroups) {
-        Raw<S> x[kBatch<S>], dy[kBatch<S>], z[kBatch<S>];
-#pragma unroll
-        for (int i = 0; i < kBatch<S>; ++i) {
-            const int ti = t + i * S::kGroups;
-            const size_t at = ((size_t)(ti < t1 ? ti : t) * p.H + h) * p.d;
-            x[i] = load_row<S>(p.x + at, l, p.d, true);
-            dy[i] = load_row<S>(p.dy + at, l, p.d, true);
-            if (gate) z[i] = load_row<S>(p.z + at, l, p.d, true);
-        }
-#pragma unroll
-        for (int i = 0; i < kBatch<S>; ++i) {
-            const int ti = t + i * S::kGroups;
-            if (ti >= t1) break;
-            s = seq_from(p.q, s, ti);
-            const float2 st = __ldg(reinterpret_cast<const float2*>(p.stats) + (size_t)s * p.H + h);
-            const float2 m = __ldg(means + (size_t)s * p.H + h);
-            const Back<S> o = back_rows<S, false>(x[i], dy[i], z[i], gate, w, b, st.x, st.y, p.act,
-                                                  none, none);
-            store_row<S>(p.dx + ((size_t)ti * p.H + h) * p.d, l, p.d, back_dx<S>(o, st.y, m.x, m.y));
-        }
+    for (int t = t0 + g; t < t1; t += S::kGroups, at += hop) {
+        Raw<S> raw[3];
+        ring.take(raw);
+        ask();
+        s = seq_from(p.q, s, t);
+        const float2 st = __ldg(reinterpret_cast<const float2*>(p.stats) + (size_t)s * p.H + h);
+        const float2 m = __ldg(means + (size_t)s * p.H + h);
+        Pairs<S> x = widen<S>(raw[0]);
+        centre<S>(x, st.x, l, p.d);
+        const Back<S> o = back_rows<S, false>(x, raw[1], raw[2], gate, w, b, st.y, p.act, none, none);
+        store_row<S>(p.dx + at, l, p.d, back_dx<S>(o, st.y, m.x, m.y));
     }
+    copy_wait<0>();
 }
 
 // ---- launching ---------------------------------------------------------------------------------
@@ -328,8 +344,8 @@ struct SeqApply {
     template <typename S>
     static void go(const gdr_norm_args& a, const NormPtrs& x, cudaStream_t st) {
         const int tile = apply_tile(a);
-        norm_seq_apply<S><<<(unsigned)(tiles_of(a, tile) * a.H), kNormThreads, 0, st>>>(
-            norm_params<typename S::IO>(a, x), tile);
+        norm_launch<Ring<S, 2>::kBytes>(norm_seq_apply<S>, tiles_of(a, tile) * a.H, st,
+                                        norm_params<typename S::IO>(a, x), tile);
     }
 };
 
@@ -342,7 +358,7 @@ struct SeqBwd {
     static void go(const gdr_norm_args& a, const NormPtrs& x, cudaStream_t st) {
         const int tile = apply_tile(a);
         const long long tiles = tiles_of(a, tile);
-        const unsigned blocks = (unsigned)(tiles * a.H);
+        const long long blocks = tiles * a.H;
         auto p = norm_params<typename S::IO>(a, x);
         char* ws = reinterpret_cast<char*>(x.ws);
         float2* pieces = reinterpret_cast<float2*>(ws);
@@ -351,10 +367,11 @@ struct SeqBwd {
                                           pair_bytes(a.n_seqs, a.H));
         if (!x.dw && !x.db) p.part = nullptr;
         if (tiles) {
-            norm_seq_bwd_sums<S><<<blocks, kNormThreads, 0, st>>>(p, tile, pieces);
+            norm_launch<Ring<S, 3>::kBytes>(norm_seq_bwd_sums<S>, blocks, st, p, tile, pieces);
             norm_seq_join_sums<<<unit_blocks(a), 128, 0, st>>>(p.q, a.H, a.d, tile, a.center,
                                                                pieces, means);
-            norm_seq_bwd_apply<S><<<blocks, kNormThreads, 0, st>>>(p, tile, means);
+            norm_launch<Ring<S, 3>::kBytes>(norm_seq_bwd_apply<S>, blocks, st, p, tile,
+                                            (const float2*)means);
         }
         if (p.part)
             launch_norm_reduce(a, p.part, (int)(a.shared_weight ? tiles * a.H : tiles), x.dw, x.db,

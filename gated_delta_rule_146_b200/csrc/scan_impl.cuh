@@ -242,22 +242,6 @@ __device__ __forceinline__ void scan_close() {
 // channels (4 or 8 bytes) where D is even; else through registers, one element at a time.
 enum Copy { kCopy16, kCopyPair, kCopyOne };
 
-template <int kBytes>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool in) {
-    const int n = in ? kBytes : 0;  // the rest of the word is zero
-    if constexpr (kBytes == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes), "r"(n) : "memory");
-}
-
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-
-template <int kLeft>
-__device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
-}
-
 // A warp's kSeg rows of 64 channels of one tensor in shared memory.
 template <typename E, int kSeg>
 struct Rows {
