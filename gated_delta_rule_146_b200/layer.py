@@ -27,20 +27,22 @@ def _code(t):
         raise TypeError(f"unsupported dtype {t.dtype}; use bfloat16 or float32") from None
 
 
-def _check(*tensors):
-    """Every given tensor is a contiguous CUDA tensor, all on one device; returns the device."""
-    dev = None
-    for t in tensors:
+def _check(first, *others):
+    """Every given tensor is a contiguous CUDA tensor, all on one device; returns its index."""
+    dev = first.get_device()
+    if dev < 0:
+        raise ValueError("gdr kernels take CUDA tensors only (there is no CPU path)")
+    if not first.is_contiguous():
+        raise ValueError("gdr kernels take contiguous tensors")
+    for t in others:
         if t is None:
             continue
-        if not t.is_cuda:
-            raise ValueError("gdr kernels take CUDA tensors only (there is no CPU path)")
+        if t.get_device() != dev:
+            if t.get_device() < 0:
+                raise ValueError("gdr kernels take CUDA tensors only (there is no CPU path)")
+            raise ValueError(f"tensors on devices {dev} and {t.get_device()}: one call uses one")
         if not t.is_contiguous():
             raise ValueError("gdr kernels take contiguous tensors")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}: one call uses one device")
     return dev
 
 
@@ -49,7 +51,7 @@ def _expect(name, t, shape, dtype):
         return
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:  # (torch.Size is a tuple)
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
 
 
@@ -62,20 +64,26 @@ def _expect_channels(name, t, count, dtype=torch.float32):
         raise ValueError(f"{name} must hold {count} values, not {t.numel()}")
 
 
-class _On:
-    """The call's device and stream: makes the device current if it is not, and allocations
-    belong to the stream."""
+_HERE = nullcontext()
 
-    def __init__(self, dev, stream):
-        s = torch.cuda.current_stream(dev)
-        same = stream is None or stream.cuda_stream == s.cuda_stream
-        if not same and stream.device != dev:
-            raise ValueError(f"a stream of {stream.device} for tensors on {dev}")
-        self.raw = s.cuda_stream if same else stream.cuda_stream
-        if dev.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(dev) if same else torch.cuda.stream(stream)
-        else:
-            self.ctx = nullcontext() if same else torch.cuda.stream(stream)
+
+def _on(dev, stream):
+    """(context, raw stream) of a call on device ``dev``: the context makes the device current if
+    it is not, and what is allocated in it belongs to the stream."""
+    here = dev == torch.cuda.current_device()
+    if stream is None:
+        return (_HERE if here else torch.cuda.device(dev)), _raw_stream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"a stream of device {stream.device_index} for tensors on {dev}")
+    return torch.cuda.stream(stream), stream.cuda_stream
+
+
+def _raw_stream(dev):
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+# the same without the Stream object: a third of a short call's time otherwise
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
 
 
 def _status(status, dev):
@@ -83,7 +91,7 @@ def _status(status, dev):
         return None
     if status.dtype != torch.int32 or not status.is_cuda or status.numel() < 1:
         raise TypeError("status must be an int32 CUDA tensor")
-    if status.device != dev:
+    if status.get_device() != dev:
         raise ValueError("status is on another device")
     return status.data_ptr()
 
@@ -113,10 +121,7 @@ def _workspace(size, given, dev):
 
 
 def _count(shape):
-    n = 1
-    for x in shape:
-        n *= x
-    return n
+    return shape[0] if len(shape) == 1 else shape.numel()
 
 
 # ---- gated linear recurrence ---------------------------------------------------------------------
@@ -151,15 +156,15 @@ def linear_scan_fwd(v, g, beta=None, h0=None, cu_seqlens=None, *, tied=False, re
     _expect("h0", h0, (n, *chan), torch.float32)
     _expect("o", o, v.shape, v.dtype)
     _expect("h_final", h_final, (n, *chan), torch.float32)
-    on = _On(dev, stream)
-    with on.ctx:
+    ctx, raw = _on(dev, stream)
+    with ctx:
         if o is None:
             o = torch.empty_like(v)
         if h_final is None and output_final_state:
             h_final = torch.empty((n, *chan), dtype=torch.float32, device=dev)
         _abi.check(_abi.lib().gdr_scan_fwd(
             ctypes.byref(a), v.data_ptr(), g.data_ptr(), _ptr(beta), _ptr(h0), _ptr(cu_seqlens),
-            o.data_ptr(), _ptr(h_final), on.raw))
+            o.data_ptr(), _ptr(h_final), raw))
     return o, h_final
 
 
@@ -178,15 +183,15 @@ def linear_scan_bwd(v, g, beta, o, dO, h0=None, cu_seqlens=None, dh_final=None, 
     _expect("dO", dO, v.shape, v.dtype)
     _expect("h0", h0, (n, *chan), torch.float32)
     _expect("dh_final", dh_final, (n, *chan), torch.float32)
-    on = _On(dev, stream)
-    with on.ctx:
+    ctx, raw = _on(dev, stream)
+    with ctx:
         dv, dg = torch.empty_like(v), torch.empty_like(g)
         dbeta = None if beta is None else torch.empty_like(beta)
         dh = torch.empty((n, *chan), dtype=torch.float32, device=dev) if dh0 else None
         _abi.check(_abi.lib().gdr_scan_bwd(
             ctypes.byref(a), v.data_ptr(), g.data_ptr(), _ptr(beta), o.data_ptr(), dO.data_ptr(),
             _ptr(h0), _ptr(cu_seqlens), _ptr(dh_final), dv.data_ptr(), dg.data_ptr(), _ptr(dbeta),
-            _ptr(dh), on.raw))
+            _ptr(dh), raw))
     return dv, dg, dbeta, dh
 
 
@@ -201,14 +206,14 @@ def linear_scan_step(v, g, beta, h, *, tied=False, h_out=None, o=None, stream=No
     _expect("h", h, v.shape, torch.float32)
     _expect("h_out", h_out, v.shape, torch.float32)
     _expect("o", o, v.shape, v.dtype)
-    on = _On(dev, stream)
-    with on.ctx:
+    ctx, raw = _on(dev, stream)
+    with ctx:
         if o is None:
             o = torch.empty_like(v)
         if N:
             _abi.check(_abi.lib().gdr_scan_step(
                 ctypes.byref(a), v.data_ptr(), g.data_ptr(), _ptr(beta), h.data_ptr(),
-                (h if h_out is None else h_out).data_ptr(), o.data_ptr(), on.raw))
+                (h if h_out is None else h_out).data_ptr(), o.data_ptr(), raw))
     return o
 
 
@@ -249,15 +254,15 @@ def short_conv_fwd(x, weight, bias=None, state=None, cu_seqlens=None, *, activat
     _expect("state", state, (n, W - 1, *chan), x.dtype)
     _expect("state_out", state_out, (n, W - 1, *chan), x.dtype)
     _expect("y", y, x.shape, x.dtype)
-    on = _On(dev, stream)
-    with on.ctx:
+    ctx, raw = _on(dev, stream)
+    with ctx:
         if y is None:
             y = torch.empty_like(x)
         if state_out is None and output_final_state:
             state_out = torch.empty((n, W - 1, *chan), dtype=x.dtype, device=dev)
         _abi.check(_abi.lib().gdr_conv_fwd(
             ctypes.byref(a), x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(state),
-            _ptr(cu_seqlens), y.data_ptr(), _ptr(state_out), on.raw))
+            _ptr(cu_seqlens), y.data_ptr(), _ptr(state_out), raw))
     return y, state_out
 
 
@@ -275,9 +280,9 @@ def short_conv_bwd(x, weight, bias, dy, state=None, cu_seqlens=None, *, activati
                  _status(status, dev))
     _expect("dy", dy, x.shape, x.dtype)
     _expect("state", state, (n, W - 1, *chan), x.dtype)
-    on = _On(dev, stream)
+    ctx, raw = _on(dev, stream)
     lib = _abi.lib()
-    with on.ctx:
+    with ctx:
         ws, size = _workspace(lib.gdr_conv_bwd_workspace_size(ctypes.byref(a)), workspace, dev)
         dx, dw = torch.empty_like(x), torch.empty_like(weight)
         db = None if bias is None else torch.empty_like(bias)
@@ -285,7 +290,7 @@ def short_conv_bwd(x, weight, bias, dy, state=None, cu_seqlens=None, *, activati
         _abi.check(lib.gdr_conv_bwd(
             ctypes.byref(a), x.data_ptr(), weight.data_ptr(), _ptr(bias), dy.data_ptr(),
             _ptr(state), _ptr(cu_seqlens), dx.data_ptr(), dw.data_ptr(), _ptr(db), _ptr(ds),
-            _ptr(ws), size, on.raw))
+            _ptr(ws), size, raw))
     return dx, dw, db, ds
 
 
@@ -303,14 +308,14 @@ def short_conv_step(x, weight, bias, state, *, activation="silu", state_out=None
     _expect("state", state, (N, W - 1, *chan), x.dtype)
     _expect("state_out", state_out, (N, W - 1, *chan), x.dtype)
     _expect("y", y, x.shape, x.dtype)
-    on = _On(dev, stream)
-    with on.ctx:
+    ctx, raw = _on(dev, stream)
+    with ctx:
         if y is None:
             y = torch.empty_like(x)
         if N:
             _abi.check(_abi.lib().gdr_conv_step(
                 ctypes.byref(a), x.data_ptr(), weight.data_ptr(), _ptr(bias), state.data_ptr(),
-                (state if state_out is None else state_out).data_ptr(), y.data_ptr(), on.raw))
+                (state if state_out is None else state_out).data_ptr(), y.data_ptr(), raw))
     return y
 
 
@@ -353,9 +358,9 @@ def group_norm_fwd(x, weight=None, bias=None, z=None, cu_seqlens=None, *, per="t
     if output_stats and per != "sequence":
         raise ValueError('stats go with per="sequence"')
     _expect("y", y, x.shape, x.dtype)
-    on = _On(dev, stream)
+    ctx, raw = _on(dev, stream)
     lib = _abi.lib()
-    with on.ctx:
+    with ctx:
         if y is None:
             y = torch.empty_like(x)
         stats = torch.empty(stats_shape, dtype=torch.float32, device=dev) if output_stats else None
@@ -364,7 +369,7 @@ def group_norm_fwd(x, weight=None, bias=None, z=None, cu_seqlens=None, *, per="t
             ws, size = _workspace(lib.gdr_norm_fwd_workspace_size(ctypes.byref(a)), workspace, dev)
         _abi.check(lib.gdr_norm_fwd(
             ctypes.byref(a), x.data_ptr(), _ptr(weight), _ptr(bias), _ptr(z), _ptr(cu),
-            y.data_ptr(), _ptr(stats), _ptr(ws), size, on.raw))
+            y.data_ptr(), _ptr(stats), _ptr(ws), size, raw))
     return (y, stats) if output_stats else y
 
 
@@ -381,9 +386,9 @@ def group_norm_bwd(x, weight, bias, z, dy, cu_seqlens=None, *, per="token", cent
     if per == "sequence" and stats is None:
         raise ValueError('per="sequence" takes the forward\'s stats')
     _expect("stats", stats, stats_shape, torch.float32)
-    on = _On(dev, stream)
+    ctx, raw = _on(dev, stream)
     lib = _abi.lib()
-    with on.ctx:
+    with ctx:
         ws, size = _workspace(lib.gdr_norm_bwd_workspace_size(ctypes.byref(a)), workspace, dev)
         dx = torch.empty_like(x)
         dw = None if weight is None else torch.empty_like(weight)
@@ -392,5 +397,5 @@ def group_norm_bwd(x, weight, bias, z, dy, cu_seqlens=None, *, per="token", cent
         _abi.check(lib.gdr_norm_bwd(
             ctypes.byref(a), x.data_ptr(), _ptr(weight), _ptr(bias), _ptr(z), dy.data_ptr(),
             _ptr(cu), _ptr(stats), dx.data_ptr(), _ptr(dw), _ptr(db), _ptr(dz), _ptr(ws), size,
-            on.raw))
+            raw))
     return dx, dw, db, dz

@@ -174,6 +174,9 @@ class Fake:
     def is_contiguous(self):
         return self._c
 
+    def get_device(self):
+        return self.device.index
+
 
 def test_the_binding_checks_shapes_types_and_devices():
     F = lambda *s, dtype=torch.float32, **k: Fake(torch.zeros(*s, dtype=dtype), **k)  # noqa: E731
