@@ -30,7 +30,7 @@ struct ConvParams {
     float* part;              // [blocks over tokens][W + 1][D]
     int* status;
     Seqs q;
-    int D, act, reverse;
+    int D, reverse;
     int run, slabs;           // tokens of a warp's run, slabs of channels
 };
 
@@ -168,7 +168,7 @@ struct Where {
     }
 };
 
-template <typename IO, int W, int N, bool kWhole>
+template <typename IO, int W, int N, bool kWhole, int kAct>
 __global__ void __launch_bounds__(kConvThreads)
 conv_fwd_kernel(const ConvParams<IO> p) {
     constexpr int P = N / 2;
@@ -218,7 +218,7 @@ conv_fwd_kernel(const ConvParams<IO> p) {
                 F2 a = fma2(w[W - 1][j], now[j], bias[j]);
 #pragma unroll
                 for (int k = 0; k < W - 1; ++k) a = fma2(w[k][j], x[k][j], a);
-                y[j] = act2<false>(a, p.act);
+                y[j] = act2<kAct, false>(a);
 #pragma unroll
                 for (int k = 0; k < W - 2; ++k) x[k][j] = x[k + 1][j];
                 x[W - 2][j] = now[j];
@@ -241,7 +241,7 @@ conv_fwd_kernel(const ConvParams<IO> p) {
     }
 }
 
-template <typename IO, int W, int N, bool kWhole>
+template <typename IO, int W, int N, bool kWhole, int kAct>
 __global__ void __launch_bounds__(kConvThreads)
 conv_bwd_kernel(const ConvParams<IO> p) {
     constexpr int P = N / 2;
@@ -307,7 +307,7 @@ conv_bwd_kernel(const ConvParams<IO> p) {
                     F2 a = fma2(w[W - 1][j], xi[j], bias[j]), v, g;
 #pragma unroll
                     for (int k = 0; k < W - 1; ++k) a = fma2(w[k][j], x[k][j], a);
-                    act2_both<false>(a, p.act, v, g);
+                    act2_both<kAct, false>(a, v, g);
                     d[j] = past ? f2(0.f) : mul2(d[j], g);
                     if (own) {
                         db[j] = add2(db[j], d[j]);
@@ -408,11 +408,11 @@ conv_reduce_kernel(const float* __restrict__ part, int rows, int D, float* __res
     else if (dbias) dbias[c] = v;
 }
 
-template <typename IO, int W, int N, bool kWhole>
+template <typename IO, int W, int N, bool kWhole, int kAct>
 __global__ void __launch_bounds__(128)
 conv_step_kernel(const IO* __restrict__ x, const float* __restrict__ w,
                  const float* __restrict__ bias, const IO* state, IO* state_out,
-                 IO* __restrict__ y, int D, int act) {
+                 IO* __restrict__ y, int D) {
     constexpr int P = N / 2;
     const int c = (blockIdx.x * 128 + threadIdx.x) * N, left = D - c;
     if (left <= 0) return;
@@ -442,7 +442,7 @@ conv_step_kernel(const IO* __restrict__ x, const float* __restrict__ w,
         F2 a = fma2(wr[W - 1][j], win[W - 1][j], b[j]);
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) a = fma2(wr[k][j], win[k][j], a);
-        out[j] = act2<false>(a, act);
+        out[j] = act2<kAct, false>(a);
     }
     put<IO, N, kWhole>(y + n * D + c, out, left);
     IO* so = state_out + n * (W - 1) * D + c;
@@ -493,7 +493,6 @@ ConvParams<IO> conv_params(const gdr_conv_args& a, const ConvPtrs& x, const Conv
     p.status = a.status;
     p.q = Seqs{x.cu, a.n_seqs, a.T, a.B * a.T};
     p.D = a.D;
-    p.act = a.activation;
     p.reverse = a.reverse;
     p.run = g.run;
     p.slabs = (int)g.slabs;
@@ -501,19 +500,19 @@ ConvParams<IO> conv_params(const gdr_conv_args& a, const ConvPtrs& x, const Conv
 }
 
 struct ConvFwd {
-    template <typename IO, int W, int N, bool kWhole>
+    template <typename IO, int W, int N, bool kWhole, int kAct>
     static void go(const gdr_conv_args& a, const ConvPtrs& x, cudaStream_t st) {
         const ConvGrid g = fwd_grid(a);
-        conv_fwd_kernel<IO, W, N, kWhole><<<g.blocks * g.slabs, dim3(32, kConvWarps), 0, st>>>(
+        conv_fwd_kernel<IO, W, N, kWhole, kAct><<<g.blocks * g.slabs, dim3(32, kConvWarps), 0, st>>>(
             conv_params<IO>(a, x, g));
     }
 };
 
 struct ConvBwd {
-    template <typename IO, int W, int N, bool kWhole>
+    template <typename IO, int W, int N, bool kWhole, int kAct>
     static void go(const gdr_conv_args& a, const ConvPtrs& x, cudaStream_t st) {
         const ConvGrid g = bwd_grid(a);
-        conv_bwd_kernel<IO, W, N, kWhole><<<g.blocks * g.slabs, dim3(32, kConvWarps), 0, st>>>(
+        conv_bwd_kernel<IO, W, N, kWhole, kAct><<<g.blocks * g.slabs, dim3(32, kConvWarps), 0, st>>>(
             conv_params<IO>(a, x, g));
         conv_reduce_kernel<W><<<dim3((a.D + 31) / 32, W + 1), 256, 0, st>>>(
             x.ws, (int)g.blocks, a.D, x.dw, x.dbias);
@@ -521,33 +520,39 @@ struct ConvBwd {
 };
 
 struct ConvStep {
-    template <typename IO, int W, int N, bool kWhole>
+    template <typename IO, int W, int N, bool kWhole, int kAct>
     static void go(const gdr_conv_args& a, const ConvPtrs& x, cudaStream_t st) {
         const unsigned bx = (unsigned)((a.D + 128 * N - 1) / (128 * N));
         for (int n0 = 0; n0 < a.B; n0 += 65535) {  // a grid's second dimension ends at 65535
             const int n = a.B - n0 < 65535 ? a.B - n0 : 65535;
             const size_t row = (size_t)n0 * a.D, srow = row * (W - 1);
-            conv_step_kernel<IO, W, N, kWhole><<<dim3(bx, n), 128, 0, st>>>(
+            conv_step_kernel<IO, W, N, kWhole, kAct><<<dim3(bx, n), 128, 0, st>>>(
                 static_cast<const IO*>(x.x) + row, x.w, x.bias,
                 static_cast<const IO*>(x.state) + srow, static_cast<IO*>(x.state_out) + srow,
-                static_cast<IO*>(x.y) + row, a.D, a.activation);
+                static_cast<IO*>(x.y) + row, a.D);
         }
     }
 };
 
-template <typename Op, typename IO, int W>
+template <typename Op, typename IO, int W, int kAct>
 void conv_vectors(const gdr_conv_args& a, const ConvPtrs& x, cudaStream_t st) {
-    if (a.D % 4 == 0) Op::template go<IO, W, 4, true>(a, x, st);
-    else if (a.D % 2 == 0) Op::template go<IO, W, 2, true>(a, x, st);
-    else Op::template go<IO, W, 2, false>(a, x, st);
+    if (a.D % 4 == 0) Op::template go<IO, W, 4, true, kAct>(a, x, st);
+    else if (a.D % 2 == 0) Op::template go<IO, W, 2, true, kAct>(a, x, st);
+    else Op::template go<IO, W, 2, false, kAct>(a, x, st);
+}
+
+template <typename Op, typename IO, int W>
+void conv_act(const gdr_conv_args& a, const ConvPtrs& x, cudaStream_t st) {
+    if (a.activation == GDR_ACT_SILU) conv_vectors<Op, IO, W, GDR_ACT_SILU>(a, x, st);
+    else conv_vectors<Op, IO, W, GDR_ACT_NONE>(a, x, st);
 }
 
 template <typename Op, typename IO>
 void conv_width(const gdr_conv_args& a, const ConvPtrs& x, cudaStream_t st) {
     switch (a.width) {
-        case 2: conv_vectors<Op, IO, 2>(a, x, st); break;
-        case 3: conv_vectors<Op, IO, 3>(a, x, st); break;
-        default: conv_vectors<Op, IO, 4>(a, x, st);
+        case 2: conv_act<Op, IO, 2>(a, x, st); break;
+        case 3: conv_act<Op, IO, 3>(a, x, st); break;
+        default: conv_act<Op, IO, 4>(a, x, st);
     }
 }
 

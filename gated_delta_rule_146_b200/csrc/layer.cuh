@@ -70,6 +70,13 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float
     return __float2bfloat16_rn(x);
 }
 
+// Two values rounded to bf16 in one word, by one instruction.
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    uint32_t w;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+    return w;
+}
+
 template <typename E, int N>
 __device__ __forceinline__ Vec<E, N> load_vec(const E* p) {
     using R = typename RawOf<sizeof(E) * N>::T;
@@ -83,8 +90,16 @@ template <typename E, int N>
 __device__ __forceinline__ void store_vec(E* p, const float (&f)[N]) {
     using R = typename RawOf<sizeof(E) * N>::T;
     Vec<E, N> v;
+    if constexpr (sizeof(E) == 2 && N % 2 == 0) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v.x[i] = from_f<E>(f[i]);
+        for (int i = 0; i < N; i += 2) {
+            const uint32_t w = bf16x2(f[i], f[i + 1]);
+            memcpy(&v.x[i], &w, 4);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v.x[i] = from_f<E>(f[i]);
+    }
     R r;
     memcpy(&r, &v, sizeof(R));
     *reinterpret_cast<R*>(p) = r;
@@ -198,24 +213,28 @@ __device__ __forceinline__ F2 sigmoid2(F2 x) {
     return f2(rcp_ftz(s.lo()), rcp_ftz(s.hi()));
 }
 
-template <bool kFine>
-__device__ __forceinline__ F2 act2(F2 x, int act) {
-    if (act == GDR_ACT_NONE) return x;
+template <int kAct, bool kFine>
+__device__ __forceinline__ F2 act2(F2 x) {
+    if constexpr (kAct == GDR_ACT_NONE) return x;
     const F2 s = sigmoid2<kFine>(x);
-    return act == GDR_ACT_SILU ? mul2(x, s) : s;
+    return kAct == GDR_ACT_SILU ? mul2(x, s) : s;
 }
 
 // act(x) and act'(x)
-template <bool kFine>
-__device__ __forceinline__ void act2_both(F2 x, int act, F2& a, F2& d) {
-    if (act == GDR_ACT_NONE) { a = x; d = f2(1.f); return; }
-    const F2 s = sigmoid2<kFine>(x), rest = fma2(s, f2(-1.f), f2(1.f));
-    if (act == GDR_ACT_SILU) {
-        a = mul2(x, s);
-        d = mul2(s, fma2(x, rest, f2(1.f)));
+template <int kAct, bool kFine>
+__device__ __forceinline__ void act2_both(F2 x, F2& a, F2& d) {
+    if constexpr (kAct == GDR_ACT_NONE) {
+        a = x;
+        d = f2(1.f);
     } else {
-        a = s;
-        d = mul2(s, rest);
+        const F2 s = sigmoid2<kFine>(x), rest = fma2(s, f2(-1.f), f2(1.f));
+        if constexpr (kAct == GDR_ACT_SILU) {
+            a = mul2(x, s);
+            d = mul2(s, fma2(x, rest, f2(1.f)));
+        } else {
+            a = s;
+            d = mul2(s, rest);
+        }
     }
 }
 
@@ -232,8 +251,13 @@ __device__ __forceinline__ F2 pair_of(const Vec<E, N>& v, int i) {
 }
 template <typename E, int N>
 __device__ __forceinline__ void set_pair(Vec<E, N>& v, int i, F2 f) {
-    v.x[2 * i] = from_f<E>(f.lo());
-    v.x[2 * i + 1] = from_f<E>(f.hi());
+    if constexpr (sizeof(E) == 2) {
+        const uint32_t w = bf16x2(f.lo(), f.hi());
+        memcpy(&v.x[2 * i], &w, 4);
+    } else {
+        v.x[2 * i] = f.lo();
+        v.x[2 * i + 1] = f.hi();
+    }
 }
 template <typename E, int N>
 __device__ __forceinline__ void store_raw(E* p, const Vec<E, N>& v) {

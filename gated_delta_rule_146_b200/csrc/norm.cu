@@ -89,7 +89,9 @@ norm_token_fwd(const NormParams<typename S::IO> p, int used, long long slots) {
         Pairs<S> x = widen<S>(raw[0]);
         const float rstd = token_stats<S>(x, l, p.d, p.center, p.eps);
         if (on && r0 + g < p.rows)
-            store_row<S>(p.y + at, l, p.d, norm_rows<S>(x, w, b, gate, raw[1], rstd, p.act));
+            with_form(p.act, gate, [&](auto form) {
+                store_row<S>(p.y + at, l, p.d, norm_rows<S>(form, x, w, b, raw[1], rstd));
+            });
     }
     copy_wait<0>();
 }
@@ -127,7 +129,10 @@ norm_token_bwd(const NormParams<typename S::IO> p, int used, long long slots) {
         Pairs<S> x = widen<S>(raw[0]);
         float rstd = token_stats<S>(x, l, p.d, p.center, p.eps);
         if (!in) rstd = 0.f;  // zeros throughout: nothing for the sums
-        const Back<S> o = back_rows<S, true>(x, raw[1], raw[2], gate, w, b, rstd, p.act, dw, db);
+        Back<S> o;
+        with_form(p.act, gate, [&](auto form) {
+            o = back_rows<S, true>(form, x, raw[1], raw[2], w, b, rstd, dw, db);
+        });
         const float mq = p.center ? group_sum<S::LPG>(o.s1) * inv : 0.f;
         const float mqn = group_sum<S::LPG>(o.s2) * inv;
         if (in) {
@@ -187,8 +192,10 @@ norm_reduce_kernel(const float* __restrict__ part, int rows, int H, int d, float
     float* out = which ? db : dw;
     if (!out) return;
     float v = 0.f;
-    if (c < d)
+    if (c < d) {
+#pragma unroll 8
         for (int r = wid; r < rows; r += 32) v += part[(((size_t)r * 2 + which) * H + h) * d + c];
+    }
     sh[wid][lane] = v;
     __syncthreads();
     if (wid == 0 && c < d) {

@@ -221,10 +221,27 @@ __device__ __forceinline__ float lane_squares(const Pairs<S>& x) {
     return s.lo() + s.hi();
 }
 
+// Calls f with the activation and the gate as compile-time constants: one branch for a row.
+template <int kAct_, bool kGate_>
+struct Form {
+    static constexpr int kAct = kAct_;
+    static constexpr bool kGate = kGate_;
+};
+template <typename F>
+__device__ __forceinline__ void with_form(int act, bool gate, F f) {
+    if (act == GDR_ACT_SILU) {
+        if (gate) f(Form<GDR_ACT_SILU, true>{}); else f(Form<GDR_ACT_SILU, false>{});
+    } else if (act == GDR_ACT_SIGMOID) {
+        if (gate) f(Form<GDR_ACT_SIGMOID, true>{}); else f(Form<GDR_ACT_SIGMOID, false>{});
+    } else {
+        if (gate) f(Form<GDR_ACT_NONE, true>{}); else f(Form<GDR_ACT_NONE, false>{});
+    }
+}
+
 // y from the centred x: n = x rstd, u = n w + b, y = u act(z) or act(u)
-template <typename S>
-__device__ __forceinline__ Pairs<S> norm_rows(const Pairs<S>& x, const Pairs<S>& w, const Pairs<S>& b,
-                                              bool gate, const Raw<S>& z, float rstd, int act) {
+template <typename S, typename Fm>
+__device__ __forceinline__ Pairs<S> norm_rows(Fm, const Pairs<S>& x, const Pairs<S>& w, const Pairs<S>& b,
+                                              const Raw<S>& z, float rstd) {
     Pairs<S> y;
     const F2 r = f2(rstd);
 #pragma unroll
@@ -232,7 +249,8 @@ __device__ __forceinline__ Pairs<S> norm_rows(const Pairs<S>& x, const Pairs<S>&
 #pragma unroll
         for (int j = 0; j < S::VEC / 2; ++j) {
             const F2 u = fma2(mul2(x.f[k][j], r), w.f[k][j], b.f[k][j]);
-            y.f[k][j] = gate ? mul2(u, act2<S::kFine>(pair_of(z.v[k], j), act)) : act2<S::kFine>(u, act);
+            if constexpr (Fm::kGate) y.f[k][j] = mul2(u, act2<Fm::kAct, S::kFine>(pair_of(z.v[k], j)));
+            else y.f[k][j] = act2<Fm::kAct, S::kFine>(u);
         }
     }
     return y;
@@ -244,10 +262,10 @@ struct Back {
     Pairs<S> n, q, dz;
     float s1, s2;   // the lane's sums of q and q n
 };
-template <typename S, bool kSums>
-__device__ __forceinline__ Back<S> back_rows(const Pairs<S>& x, const Raw<S>& dy, const Raw<S>& z,
-                                             bool gate, const Pairs<S>& w, const Pairs<S>& b, float rstd,
-                                             int act, Pairs<S>& dw, Pairs<S>& db) {
+template <typename S, bool kSums, typename Fm>
+__device__ __forceinline__ Back<S> back_rows(Fm, const Pairs<S>& x, const Raw<S>& dy, const Raw<S>& z,
+                                             const Pairs<S>& w, const Pairs<S>& b, float rstd,
+                                             Pairs<S>& dw, Pairs<S>& db) {
     Back<S> o;
     const F2 r = f2(rstd);
     F2 s1 = f2(0.f), s2 = f2(0.f);
@@ -258,8 +276,8 @@ __device__ __forceinline__ Back<S> back_rows(const Pairs<S>& x, const Raw<S>& dy
             const F2 n = mul2(x.f[k][j], r), g = pair_of(dy.v[k], j);
             const F2 u = fma2(n, w.f[k][j], b.f[k][j]);
             F2 a, da, du;
-            act2_both<S::kFine>(gate ? pair_of(z.v[k], j) : u, act, a, da);
-            if (gate) {
+            act2_both<Fm::kAct, S::kFine>(Fm::kGate ? pair_of(z.v[k], j) : u, a, da);
+            if constexpr (Fm::kGate) {
                 o.dz.f[k][j] = mul2(mul2(g, u), da);
                 du = mul2(g, a);
             } else {

@@ -156,7 +156,9 @@ norm_seq_apply(const NormParams<typename S::IO> p, int tokens) {
         const float2 st = __ldg(reinterpret_cast<const float2*>(p.stats) + (size_t)s * p.H + h);
         Pairs<S> x = widen<S>(raw[0]);
         centre<S>(x, st.x, l, p.d);
-        store_row<S>(p.y + at, l, p.d, norm_rows<S>(x, w, b, gate, raw[1], st.y, p.act));
+        with_form(p.act, gate, [&](auto form) {
+            store_row<S>(p.y + at, l, p.d, norm_rows<S>(form, x, w, b, raw[1], st.y));
+        });
     }
     copy_wait<0>();
 }
@@ -205,7 +207,10 @@ norm_seq_bwd_sums(const NormParams<typename S::IO> p, int tokens, float2* __rest
             ask();
             Pairs<S> x = widen<S>(raw[0]);
             centre<S>(x, st.x, l, p.d);
-            const Back<S> o = back_rows<S, true>(x, raw[1], raw[2], gate, w, b, st.y, p.act, dw, db);
+            Back<S> o;
+            with_form(p.act, gate, [&](auto form) {
+                o = back_rows<S, true>(form, x, raw[1], raw[2], w, b, st.y, dw, db);
+            });
             s1 += o.s1;
             s2 += o.s2;
             if (gate) store_row<S>(p.dz + at, l, p.d, o.dz);
@@ -299,8 +304,10 @@ norm_seq_bwd_apply(const NormParams<typename S::IO> p, int tokens,
         const float2 m = __ldg(means + (size_t)s * p.H + h);
         Pairs<S> x = widen<S>(raw[0]);
         centre<S>(x, st.x, l, p.d);
-        const Back<S> o = back_rows<S, false>(x, raw[1], raw[2], gate, w, b, st.y, p.act, none, none);
-        store_row<S>(p.dx + at, l, p.d, back_dx<S>(o, st.y, m.x, m.y));
+        with_form(p.act, gate, [&](auto form) {
+            const Back<S> o = back_rows<S, false>(form, x, raw[1], raw[2], w, b, st.y, none, none);
+            store_row<S>(p.dx + at, l, p.d, back_dx<S>(o, st.y, m.x, m.y));
+        });
     }
     copy_wait<0>();
 }
