@@ -31,7 +31,7 @@ struct ConvParams {
     int* status;
     Seqs q;
     int D, reverse;
-    int run, slabs;           // tokens of a warp's run, slabs of channels
+    int run, slabs, across;   // tokens of a warp's run, slabs of channels, slabs of a block
 };
 
 // The tokens of one sequence in scan order: place 0 is its first token there.
@@ -156,15 +156,20 @@ struct Ring {
     }
 };
 
-// The block's warp and slab: slabs vary fastest, so that blocks that run together read whole rows.
+// What a warp works on: a slab of channels and a run of tokens.  A block's warps take `across`
+// neighbouring slabs, of as many runs as that leaves, and blocks go over the slabs first, so that
+// what runs together reads long pieces of rows.
 struct Where {
     long long warp, warps, tokens_block;
-    int slab;
-    __device__ __forceinline__ Where(int slabs, int wid) {
-        tokens_block = blockIdx.x / slabs;
-        slab = blockIdx.x % slabs;
-        warp = tokens_block * kConvWarps + wid;
-        warps = (long long)(gridDim.x / slabs) * kConvWarps;
+    int slab, across, col, line;  // the warp's column and line in the block
+    __device__ __forceinline__ Where(int slabs, int across_, int wid) : across(across_) {
+        const int columns = (slabs + across - 1) / across, lines = kConvWarps / across;
+        col = wid % across;
+        line = wid / across;
+        tokens_block = blockIdx.x / columns;
+        slab = blockIdx.x % columns * across + col;
+        warp = tokens_block * lines + line;
+        warps = (long long)(gridDim.x / columns) * lines;
     }
 };
 
@@ -174,7 +179,7 @@ conv_fwd_kernel(const ConvParams<IO> p) {
     constexpr int P = N / 2;
     __shared__ __align__(16) char smem[Ring<IO, N, kWhole, 1>::kBytes];
     const int lane = threadIdx.x, wid = threadIdx.y;
-    const Where me(p.slabs, wid);
+    const Where me(p.slabs, p.across, wid);
     const int c = (me.slab * 32 + lane) * N, left = p.D - c;
     if (blockIdx.x == 0) check_cu(p.q, p.status, wid * 32 + lane, kConvThreads);
     if (left <= 0) return;
@@ -241,8 +246,11 @@ conv_fwd_kernel(const ConvParams<IO> p) {
     }
 }
 
+// Blocks on an SM: five spill (115 instead of 102 us).
+constexpr int kBwdResident = 4;
+
 template <typename IO, int W, int N, bool kWhole, int kAct>
-__global__ void __launch_bounds__(kConvThreads)
+__global__ void __launch_bounds__(kConvThreads, kBwdResident)
 conv_bwd_kernel(const ConvParams<IO> p) {
     constexpr int P = N / 2;
     union Shared {
@@ -252,7 +260,7 @@ conv_bwd_kernel(const ConvParams<IO> p) {
     __shared__ __align__(16) Shared smem;
     auto& sh = smem.sums;
     const int lane = threadIdx.x, wid = threadIdx.y;
-    const Where me(p.slabs, wid);
+    const Where me(p.slabs, p.across, wid);
     const int c = (me.slab * 32 + lane) * N, left = p.D - c;
     if (blockIdx.x == 0) check_cu(p.q, p.status, wid * 32 + lane, kConvThreads);
     if (p.dstate && left > 0) {  // nothing reads an empty sequence's state
@@ -365,6 +373,7 @@ conv_bwd_kernel(const ConvParams<IO> p) {
             for (; i < i1 + W - 1; ++i) any(i);
         }
     }
+    let_follow();
     // the block's runs, then one row of partial sums a block, in the rings' place
     copy_wait<0>();
 #pragma unroll
@@ -377,13 +386,14 @@ conv_bwd_kernel(const ConvParams<IO> p) {
             sh[wid][lane * N + 2 * j + 1] = v.hi();
         }
         __syncthreads();
-        for (int i = wid * 32 + lane; i < 32 * N; i += kConvThreads) {
-            const int ch = me.slab * 32 * N + i;
-            if (ch >= p.D) break;
-            float v = 0.f;
-#pragma unroll
-            for (int g = 0; g < kConvWarps; ++g) v += sh[g][i];
-            p.part[((size_t)me.tokens_block * (W + 1) + k) * p.D + ch] = v;
+        if (me.line == 0) {
+            for (int i = lane; i < 32 * N; i += 32) {
+                const int ch = me.slab * 32 * N + i;
+                if (ch >= p.D) break;
+                float v = 0.f;
+                for (int g = me.col; g < kConvWarps; g += me.across) v += sh[g][i];
+                p.part[((size_t)me.tokens_block * (W + 1) + k) * p.D + ch] = v;
+            }
         }
     }
 }
@@ -396,8 +406,10 @@ conv_reduce_kernel(const float* __restrict__ part, int rows, int D, float* __res
     __shared__ float sh[8][32];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane, k = blockIdx.y;
+    wait_before();
     float v = 0.f;
     if (c < D)
+#pragma unroll 4
         for (int r = wid; r < rows; r += 8) v += part[((size_t)r * (W + 1) + k) * D + c];
     sh[wid][lane] = v;
     __syncthreads();
@@ -456,26 +468,35 @@ conv_step_kernel(const IO* __restrict__ x, const float* __restrict__ w,
 int conv_channels(const gdr_conv_args& a) { return a.D % 4 ? 2 : 4; }
 
 struct ConvGrid {
-    int run;                 // tokens of a warp's run
-    unsigned slabs, blocks;  // blocks over the tokens
+    int run, slabs, across;  // as in ConvParams
+    unsigned rows, blocks;   // blocks over the tokens, blocks
 };
 
 // A run is long enough that the W - 1 extra tokens read at its ends cost little, and short enough
-// that `warps` of them fill the GPU.
-ConvGrid conv_grid(const gdr_conv_args& a, int warps, int most) {
+// that `resident` blocks on an SM are there where the tokens suffice.
+ConvGrid conv_grid(const gdr_conv_args& a, int across, int resident, int most) {
     ConvGrid g;
     const int per_slab = 32 * conv_channels(a);
     const long long tokens = (long long)a.B * a.T;
-    g.slabs = (unsigned)((a.D + per_slab - 1) / per_slab);
-    const long long run = (tokens * g.slabs + warps - 1) / warps;
+    g.slabs = (a.D + per_slab - 1) / per_slab;
+    while (across > g.slabs) across /= 2;
+    g.across = across;
+    const int columns = (g.slabs + across - 1) / across, lines = kConvWarps / across;
+    const long long rows = 148 * resident / columns > 0 ? 148 * resident / columns : 1;
+    const long long run = (tokens + rows * lines - 1) / (rows * lines);
     g.run = (int)(run < 8 ? 8 : run > most ? most : run);
-    const long long per = (long long)g.run * kConvWarps;
-    g.blocks = (unsigned)((tokens + per - 1) / per);
-    if (g.blocks == 0) g.blocks = 1;
+    const long long per = (long long)g.run * lines;
+    g.rows = (unsigned)((tokens + per - 1) / per);
+    if (g.rows == 0) g.rows = 1;
+    g.blocks = g.rows * (unsigned)columns;
     return g;
 }
-ConvGrid fwd_grid(const gdr_conv_args& a) { return conv_grid(a, 148 * 32, 64); }
-ConvGrid bwd_grid(const gdr_conv_args& a) { return conv_grid(a, 148 * 16, 256); }
+// Measured on 65537 x 4096 (forward) and 8 x 4096 x 2048 (backward) in bf16.  Forward: a block's
+// warps on four neighbouring slabs 186 us, on four runs of one slab 190; runs of up to 64, 128, 256
+// tokens 195, 186, 198.  Backward: one slab 98 us, four 104; runs of up to 32, 64, 128, 256 tokens
+// 131, 108, 100, 98.
+ConvGrid fwd_grid(const gdr_conv_args& a) { return conv_grid(a, 4, 8, 128); }
+ConvGrid bwd_grid(const gdr_conv_args& a) { return conv_grid(a, 1, kBwdResident, 256); }
 
 template <typename IO>
 ConvParams<IO> conv_params(const gdr_conv_args& a, const ConvPtrs& x, const ConvGrid& g) {
@@ -496,6 +517,7 @@ ConvParams<IO> conv_params(const gdr_conv_args& a, const ConvPtrs& x, const Conv
     p.reverse = a.reverse;
     p.run = g.run;
     p.slabs = (int)g.slabs;
+    p.across = g.across;
     return p;
 }
 
@@ -503,7 +525,7 @@ struct ConvFwd {
     template <typename IO, int W, int N, bool kWhole, int kAct>
     static void go(const gdr_conv_args& a, const ConvPtrs& x, cudaStream_t st) {
         const ConvGrid g = fwd_grid(a);
-        conv_fwd_kernel<IO, W, N, kWhole, kAct><<<g.blocks * g.slabs, dim3(32, kConvWarps), 0, st>>>(
+        conv_fwd_kernel<IO, W, N, kWhole, kAct><<<g.blocks, dim3(32, kConvWarps), 0, st>>>(
             conv_params<IO>(a, x, g));
     }
 };
@@ -512,10 +534,10 @@ struct ConvBwd {
     template <typename IO, int W, int N, bool kWhole, int kAct>
     static void go(const gdr_conv_args& a, const ConvPtrs& x, cudaStream_t st) {
         const ConvGrid g = bwd_grid(a);
-        conv_bwd_kernel<IO, W, N, kWhole, kAct><<<g.blocks * g.slabs, dim3(32, kConvWarps), 0, st>>>(
+        conv_bwd_kernel<IO, W, N, kWhole, kAct><<<g.blocks, dim3(32, kConvWarps), 0, st>>>(
             conv_params<IO>(a, x, g));
-        conv_reduce_kernel<W><<<dim3((a.D + 31) / 32, W + 1), 256, 0, st>>>(
-            x.ws, (int)g.blocks, a.D, x.dw, x.dbias);
+        launch_follower(conv_reduce_kernel<W>, dim3((a.D + 31) / 32, W + 1), dim3(256), 0, st, x.ws,
+                        (int)g.rows, a.D, x.dw, x.dbias);
     }
 };
 
@@ -567,7 +589,7 @@ gdr_status conv_dispatch(const gdr_conv_args& a, const ConvPtrs& x, cudaStream_t
 
 size_t conv_bwd_workspace(const gdr_conv_args& a) {
     const ConvGrid g = bwd_grid(a);
-    return align_up(sizeof(float) * (size_t)g.blocks * (a.width + 1) * a.D, 256);
+    return align_up(sizeof(float) * (size_t)g.rows * (a.width + 1) * a.D, 256);
 }
 
 gdr_status launch_conv_fwd(const gdr_conv_args& a, const ConvPtrs& x, cudaStream_t st) {

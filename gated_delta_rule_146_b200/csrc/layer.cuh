@@ -267,6 +267,30 @@ __device__ __forceinline__ void store_raw(E* p, const Vec<E, N>& v) {
     *reinterpret_cast<R*>(p) = r;
 }
 
+// ---- kernels that follow one another --------------------------------------------------------------
+// A follower is launched while its predecessor still runs, and waits for its results here, before
+// it reads or writes anything.  The predecessor lets it come when it calls let_follow, or ends.
+__device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_follow() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_follower(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                            A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // ---- launchers (host) ----------------------------------------------------------------------------
 struct ScanPtrs {
     const void *v, *g, *beta, *o_in, *dO;

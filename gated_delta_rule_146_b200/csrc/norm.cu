@@ -141,6 +141,7 @@ norm_token_bwd(const NormParams<typename S::IO> p, int used, long long slots) {
         }
     }
     copy_wait<0>();
+    let_follow();
     if (!p.part) return;
 
     // sums over the block's lane groups of one head (of all, for a shared weight)
@@ -190,6 +191,7 @@ norm_reduce_kernel(const float* __restrict__ part, int rows, int H, int d, float
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane, h = blockIdx.y, which = blockIdx.z;
     float* out = which ? db : dw;
+    wait_before();
     if (!out) return;
     float v = 0.f;
     if (c < d) {
@@ -240,7 +242,8 @@ struct TokenBwdSize {
 void launch_norm_reduce(const gdr_norm_args& a, const float* part, int rows, float* dw,
                               float* db, cudaStream_t st) {
     const int H = a.shared_weight ? 1 : a.H;
-    norm_reduce_kernel<<<dim3((a.d + 31) / 32, H, 2), 1024, 0, st>>>(part, rows, H, a.d, dw, db);
+    launch_follower(norm_reduce_kernel, dim3((a.d + 31) / 32, H, 2), dim3(1024), 0, st, part, rows, H,
+                    a.d, dw, db);
 }
 
 bool norm_supported(const gdr_norm_args& a) {

@@ -345,11 +345,14 @@ void norm_shape(const gdr_norm_args& a, const NormPtrs& x, cudaStream_t st) {
 }
 
 // Launches with the shared memory of a ring.
-template <int kBytes, typename... P, typename... A>
+template <int kBytes, bool kFollows = false, typename... P, typename... A>
 void norm_launch(void (*kernel)(P...), long long blocks, cudaStream_t st, A... args) {
     if (kBytes > 40 << 10)  // (with the kernels' own arrays, above what needs no asking for)
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
-    kernel<<<(unsigned)blocks, kNormThreads, kBytes, st>>>(args...);
+    if (kFollows)
+        launch_follower(kernel, dim3((unsigned)blocks), dim3(kNormThreads), kBytes, st, args...);
+    else
+        kernel<<<(unsigned)blocks, kNormThreads, kBytes, st>>>(args...);
 }
 
 template <typename Op>

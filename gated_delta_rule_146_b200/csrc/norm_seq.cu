@@ -51,6 +51,7 @@ norm_seq_stats(const NormParams<typename S::IO> p) {
         const int t = t0 + g + i * S::kGroups;
         x[i] = load_row<S>(p.x + ((size_t)(t < t1 ? t : t0) * p.H + h) * p.d, l, p.d, t < t1);
     }
+    let_follow();
     for (int s = p.q.of(t0); s < p.q.n; ++s) {
         const int b = p.q.begin(s), e = p.q.end(s);
         if (b >= t1) break;
@@ -87,6 +88,8 @@ norm_seq_join_stats(Seqs q, int H, int d, int tokens, float eps, const float2* _
                     float2* __restrict__ stats) {
     const long long unit = (long long)blockIdx.x * 4 + threadIdx.x / 32;
     const int lane = threadIdx.x & 31;
+    wait_before();
+    let_follow();
     if (unit >= (long long)q.n * H) return;
     const int s = (int)(unit / H), h = (int)(unit % H);
     const int b = q.begin(s), e = q.end(s);
@@ -148,12 +151,13 @@ norm_seq_apply(const NormParams<typename S::IO> p, int tokens) {
 #pragma unroll
     for (int i = 0; i < S::kStages - 1; ++i) ask();
     int s = t0 + g < t1 ? p.q.of(t0 + g) : 0;
+    wait_before();  // for the statistics; the tensors are the caller's
     for (int t = t0 + g; t < t1; t += S::kGroups, at += hop) {
         Raw<S> raw[2];
         ring.take(raw);
         ask();
         s = seq_from(p.q, s, t);
-        const float2 st = __ldg(reinterpret_cast<const float2*>(p.stats) + (size_t)s * p.H + h);
+        const float2 st = reinterpret_cast<const float2*>(p.stats)[(size_t)s * p.H + h];
         Pairs<S> x = widen<S>(raw[0]);
         centre<S>(x, st.x, l, p.d);
         with_form(p.act, gate, [&](auto form) {
@@ -220,6 +224,7 @@ norm_seq_bwd_sums(const NormParams<typename S::IO> p, int tokens, float2* __rest
         if (threadIdx.x == 0) pieces[((size_t)tile + s) * p.H + h] = make_float2(s1, s2);
     }
     copy_wait<0>();
+    let_follow();
     float* const shw = reinterpret_cast<float*>(smem);  // in the rings' place
     static_assert(sizeof(float) * S::kGroups * kCh <= Ring<S, 3>::kBytes, "the rings are larger");
     if (!p.part) return;
@@ -253,6 +258,8 @@ norm_seq_join_sums(Seqs q, int H, int d, int tokens, int center, const float2* _
                    float2* __restrict__ means) {
     const long long unit = (long long)blockIdx.x * 4 + threadIdx.x / 32;
     const int lane = threadIdx.x & 31;
+    wait_before();
+    let_follow();
     if (unit >= (long long)q.n * H) return;
     const int s = (int)(unit / H), h = (int)(unit % H);
     const int b = q.begin(s), e = q.end(s);
@@ -272,7 +279,7 @@ norm_seq_join_sums(Seqs q, int H, int d, int tokens, int center, const float2* _
 template <typename S>
 __global__ void __launch_bounds__(kNormThreads, S::kResident)
 norm_seq_bwd_apply(const NormParams<typename S::IO> p, int tokens,
-                   const float2* __restrict__ means) {
+                   const float2* means) {
     extern __shared__ __align__(16) char smem[];
     const int g = threadIdx.x / S::LPG, l = threadIdx.x % S::LPG;
     const int block = gridDim.x - 1 - blockIdx.x, tile = block / p.H, h = block % p.H;
@@ -295,13 +302,14 @@ norm_seq_bwd_apply(const NormParams<typename S::IO> p, int tokens,
 #pragma unroll
     for (int i = 0; i < S::kStages - 1; ++i) ask();
     int s = t0 + g < t1 ? p.q.of(t0 + g) : 0;
+    wait_before();  // for the statistics; the tensors are the caller's
     for (int t = t0 + g; t < t1; t += S::kGroups, at += hop) {
         Raw<S> raw[3];
         ring.take(raw);
         ask();
         s = seq_from(p.q, s, t);
         const float2 st = __ldg(reinterpret_cast<const float2*>(p.stats) + (size_t)s * p.H + h);
-        const float2 m = __ldg(means + (size_t)s * p.H + h);
+        const float2 m = means[(size_t)s * p.H + h];
         Pairs<S> x = widen<S>(raw[0]);
         centre<S>(x, st.x, l, p.d);
         with_form(p.act, gate, [&](auto form) {
@@ -322,13 +330,14 @@ int stats_tile(const gdr_norm_args& a) {
     return norm_groups(a) * (8 / nv);
 }
 
-// Tokens of a tile in the other passes: a multiple of the block's lane groups, so many that the
-// partial sums stay small, so few that the blocks fill the GPU.
+// Tokens of a tile in the other passes: as many as make the blocks (a tile and head each) one wave
+// of three on an SM, in whole passes of the block's lane groups.
 int apply_tile(const gdr_norm_args& a) {
     const int g = norm_groups(a);
     const long long tokens = (long long)a.B * a.T;
-    long long per = tokens * a.H / (148 * 8) / g;
-    return (int)(per < 1 ? 1 : per > 64 ? 64 : per) * g;
+    const long long tiles = 148 * 3 / a.H > 0 ? 148 * 3 / a.H : 1;
+    const long long per = (tokens + tiles * g - 1) / (tiles * g);
+    return (int)(per < 1 ? 1 : per > 256 ? 256 : per) * g;
 }
 
 long long tiles_of(const gdr_norm_args& a, int tile) {
@@ -351,7 +360,7 @@ struct SeqApply {
     template <typename S>
     static void go(const gdr_norm_args& a, const NormPtrs& x, cudaStream_t st) {
         const int tile = apply_tile(a);
-        norm_launch<Ring<S, 2>::kBytes>(norm_seq_apply<S>, tiles_of(a, tile) * a.H, st,
+        norm_launch<Ring<S, 2>::kBytes, true>(norm_seq_apply<S>, tiles_of(a, tile) * a.H, st,
                                         norm_params<typename S::IO>(a, x), tile);
     }
 };
@@ -375,9 +384,9 @@ struct SeqBwd {
         if (!x.dw && !x.db) p.part = nullptr;
         if (tiles) {
             norm_launch<Ring<S, 3>::kBytes>(norm_seq_bwd_sums<S>, blocks, st, p, tile, pieces);
-            norm_seq_join_sums<<<unit_blocks(a), 128, 0, st>>>(p.q, a.H, a.d, tile, a.center,
-                                                               pieces, means);
-            norm_launch<Ring<S, 3>::kBytes>(norm_seq_bwd_apply<S>, blocks, st, p, tile,
+            launch_follower(norm_seq_join_sums, dim3(unit_blocks(a)), dim3(128), 0, st, p.q, a.H, a.d,
+                            tile, a.center, pieces, means);
+            norm_launch<Ring<S, 3>::kBytes, true>(norm_seq_bwd_apply<S>, blocks, st, p, tile,
                                             (const float2*)means);
         }
         if (p.part)
@@ -408,10 +417,10 @@ gdr_status launch_norm_seq_fwd(const gdr_norm_args& a, const NormPtrs& x, cudaSt
                                            pair_bytes(tiles + a.n_seqs, a.H));
     y.stats_in = y.stats;
     if (tiles && norm_dispatch<SeqStats>(a, y, st) != GDR_OK) return GDR_ERR_CUDA;
-    norm_seq_join_stats<<<unit_blocks(a), 128, 0, st>>>(
-        Seqs{x.cu, a.n_seqs, a.T, a.B * a.T}, a.H, a.d, tile, a.eps, part,
-        reinterpret_cast<float2*>(y.stats));
-    if (cudaGetLastError() != cudaSuccess) return GDR_ERR_CUDA;
+    if (launch_follower(norm_seq_join_stats, dim3(unit_blocks(a)), dim3(128), 0, st,
+                        Seqs{x.cu, a.n_seqs, a.T, a.B * a.T}, a.H, a.d, tile, a.eps, part,
+                        reinterpret_cast<float2*>(y.stats)) != cudaSuccess)
+        return GDR_ERR_CUDA;
     return tiles ? norm_dispatch<SeqApply>(a, y, st) : GDR_OK;
 }
 
