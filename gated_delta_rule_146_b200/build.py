@@ -20,7 +20,8 @@ LIB = os.path.join(PKG, "libgdr.so")
 SOURCES = ["api.cu", "plan.cu", "chunk_simt.cu", "chunk_tc.cu", "chunk_g2_tc.cu", "chunk_bwd.cu",
            "chunk_bwd_tc.cu",
            "decode.cu", "noalloc.cu",
-           "layer_api.cu", "scan.cu", "scan_bwd.cu", "conv.cu", "norm.cu", "norm_seq.cu"]
+           "layer_api.cu", "scan.cu", "scan_f32.cu", "scan_bwd.cu", "scan_bwd_f32.cu",
+            "conv.cu", "norm.cu", "norm_seq.cu"]
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 OBJ_DIR = os.path.join(ROOT, "_build")

@@ -1,303 +1,10 @@
-// scan_bwd.cu -- gated linear recurrence: backward pass.
-//
-// With m_t = alpha_t lam_t the adjoint runs from the last token to the first,
-//     lam_t = dO_t + m_{t+1},   m_t = alpha_t lam_t,
-// again a recurrence of maps m -> A m + H with the same A, split and joined as in the forward
-// (scan_impl.cuh).  dg_t = m_t h_{t-1} reads h from the forward's output, so nothing is
-// recomputed and every element is read and written once: 10 (plain), 12 (tied) or 16 (gate)
-// bytes per token and channel in bf16.  HBM bounds it.
-#include "scan_impl.cuh"
+// scan_bwd.cu -- gated linear recurrence: the backward's dispatch, its kernels for bf16.
+#include "scan_bwd.cuh"
 
 namespace gdr {
 
-namespace {
-
-// Stages of the two rings.  The second is a step ahead; how far the first may be was measured on
-// 8 x 4096 x 2048 in bf16: plain 120 us one tile ahead, 136 two; with beta, whose second ring is
-// larger, 211 and 186.  More bytes in flight than the memory system takes in order cost time.
-template <int kWrite>
-constexpr int early_stages = kWrite == GDR_WRITE_GATE ? 3 : 2;
-constexpr int kLateStages = 2;
-
-// Tokens of a warp's run: eight where two blocks' rings of 8 warps fit an SM's shared memory,
-// bf16 in single blocks, else four.
-template <typename IO, typename GT>
-constexpr int seg_of(bool cluster) { return !cluster && sizeof(IO) + sizeof(GT) == 4 ? 8 : 4; }
-
-template <typename IO, typename GT>
-struct BwdParams {
-    const IO* v; const GT* g; const GT* beta; const IO* o; const IO* dO;
-    const float *h0, *dh_final;
-    IO* dv; GT* dg; GT* dbeta;
-    float* dh0;
-    int* status;
-    Seqs q;
-    int D, L, slabs, reverse;
-};
-
-// A warp's tokens in shared memory, in two rings: g and dO of a tile are read when its run is
-// formed, o of the token before, v and beta a step later, when it is finished.
-template <typename IO, typename GT, int kWrite, int kSeg>
-struct Ring {
-    static constexpr int kG = Rows<GT, kSeg>::kBytes, kI = Rows<IO, kSeg>::kBytes;
-    static constexpr int kEarly = kG + kI;
-    static constexpr int v = kI, beta = v + kI;  // behind o
-    static constexpr int kLate = kWrite == GDR_WRITE_GATE ? beta + kG
-                               : kWrite == GDR_WRITE_TIED ? beta : v;
-    static constexpr int kEarlyStages = early_stages<kWrite>;
-    static constexpr int kBytes = kEarlyStages * kEarly + kLateStages * kLate;
-};
-
-template <int kWrite, int kSeg>
-struct Elements {
-    F2 a[kSeg], d[kSeg];           // alpha; dO, with dh_final at a sequence's last token
-    F2 w[kWrite == GDR_WRITE_TIED ? kSeg : 1];
-    Marks m;                       // start: the last token of a sequence, end: its first
-};
-
-template <typename IO, typename GT, int kWrite, Copy kCopy, bool kSeqs, bool kCluster,
-          int kWarps>
-__global__ void __launch_bounds__(32 * (kWarps + 2 * kCluster), kCluster ? 1 : 2)
-scan_bwd_kernel(const BwdParams<IO, GT> p, const int cluster) {
-    extern __shared__ __align__(128) char smem[];
-    using Shared = ScanShared<kWarps, kCluster>;
-    Shared& sh = *reinterpret_cast<Shared*>(smem);
-    char* const stages = smem + sizeof(sh) + (kSeqs ? kCuBytes : 0);
-    constexpr int kSeg = seg_of<IO, GT>(kCluster), kTile = kWarps * kSeg;
-    using R = Ring<IO, GT, kWrite, kSeg>;
-    constexpr int kEarlyStages = R::kEarlyStages;
-    using Els = Elements<kWrite, kSeg>;
-    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-    const int rank = blockIdx.x % cluster;
-    const int unit = blockIdx.x / cluster;
-    const int slab = unit % p.slabs, row = unit / p.slabs;
-    const int left = p.D - slab * kSlab;
-    const int c = slab * kSlab + 2 * lane, mine = left - 2 * lane;
-    const int L = p.L, D = p.D;
-    // the adjoint's order: the forward's, backwards
-    const int origin = p.reverse ? 0 : L - 1, dir = p.reverse ? 1 : -1;
-
-    F2 carry = f2(0.f), h0_row = f2(0.f);  // the folder's, the workers'
-    if (!kSeqs && (!kCluster || wid == kWarps) && p.dh_final)
-        carry = load_state<kCopy>(p.dh_final + (size_t)row * D + c, mine);
-    Seqs seqs = p.q;
-    if constexpr (kSeqs) seqs = share_cu(p.q, reinterpret_cast<int32_t*>(smem + sizeof(sh)));
-    scan_open<kCluster>(sh.full);
-    if (kSeqs && blockIdx.x == 0) check_cu(p.q, p.status, tid, 32 * (kWarps + 2 * kCluster));
-    if (kSeqs && rank == 0 && p.dh0) {  // the state's gradient passes an empty sequence unchanged
-        for (int s = wid; s < seqs.n; s += kWarps + 2 * kCluster) {
-            if (seqs.begin(s) != seqs.end(s)) continue;
-            F2 x = f2(0.f);
-            if (p.dh_final) x = load_state<kCopy>(p.dh_final + (size_t)s * D + c, mine);
-            store_pair<float, kCopy>(p.dh0 + (size_t)s * D + c, x, mine);
-        }
-    }
-
-    const size_t base = (size_t)row * L * D + slab * kSlab;
-    const int stride = cluster * kTile, first0 = rank * kTile + wid * kSeg;
-    const int steps = (int)(((long long)L + stride - 1) / stride);
-    const long long hop = (long long)dir * stride * D;
-    char* const early = stages + wid * R::kBytes;
-    char* const late = early + kEarlyStages * R::kEarly;
-    Feed<GT, kCopy, kSeg> fg, fb;
-    Feed<IO, kCopy, kSeg> fd, fo, fv;
-    fg.open(p.g + base, origin, dir, first0, D, left, lane);
-    fd.open(p.dO + base, origin, dir, first0, D, left, lane);
-    fo.open(p.o + base, origin, dir, first0 + 1, D, left, lane);
-    if constexpr (kWrite != GDR_WRITE_PLAIN) fv.open(p.v + base, origin, dir, first0, D, left, lane);
-    if constexpr (kWrite == GDR_WRITE_GATE) fb.open(p.beta + base, origin, dir, first0, D, left, lane);
-    auto place_of = [&](int k) { return k < steps ? first0 + k * stride : L; };
-    auto feed_early = [&](int k, int stage) {
-        char* s = early + stage * R::kEarly;
-        fg.tile(s, place_of(k), L, hop);
-        fd.tile(s + R::kG, place_of(k), L, hop);
-    };
-    auto feed_late = [&](int k, int stage) {
-        char* s = late + stage * R::kLate;
-        fo.tile(s, place_of(k) + 1, L, hop);
-        if constexpr (kWrite != GDR_WRITE_PLAIN) fv.tile(s + R::v, place_of(k), L, hop);
-        if constexpr (kWrite == GDR_WRITE_GATE) fb.tile(s + R::beta, place_of(k), L, hop);
-    };
-    if constexpr (kCluster) if (wid >= kWarps) {
-        if (wid > kWarps) {
-            scan_publish<kSeqs>(sh, steps, cluster, rank, lane);
-        } else {
-            const bool ok = scan_fold<kSeqs>(sh, steps, cluster, rank, lane, carry);
-            if (!ok && p.status && lane == 0) atomicCAS(p.status, (int)GDR_OK, (int)GDR_ERR_TIMEOUT);
-        }
-        scan_close<kCluster>();
-        return;
-    }
-    // copy group k: the first ring's tile k, with the second's kEarlyStages - 1 tiles behind it
-#pragma unroll
-    for (int k = 0; k < kEarlyStages - 1; ++k) {
-        feed_early(k, k);
-        copy_commit();
-    }
-
-    if (!kSeqs && p.h0) h0_row = load_state<kCopy>(p.h0 + (size_t)row * D + c, mine);
-    Here here{0, 0};
-    int stage = 0;  // of the next tile to be formed
-    auto form = [&](int k, Els& e) -> Run {
-        copy_wait<kEarlyStages - 2>();
-        __syncwarp();
-        // into the stages of tiles k - 1 and k - 2, which every lane has read
-        feed_early(k + kEarlyStages - 1, stage == 0 ? kEarlyStages - 1 : stage - 1);
-        feed_late(k, k & 1);
-        copy_commit();
-        const char* s = early + stage * R::kEarly;
-        stage = stage == kEarlyStages - 1 ? 0 : stage + 1;
-        if constexpr (kSeqs) {
-            const int first = first0 + k * stride;
-            e.m = find_marks(seqs, here, origin, dir, first, min(kSeg, L - first), lane);
-        }
-#pragma unroll
-        for (int i = 0; i < kSeg; ++i) {
-            const F2 g = Rows<GT, kSeg>::read(s, i, lane);
-            e.a[i] = exp2ch(g);
-            if constexpr (kWrite == GDR_WRITE_TIED) e.w[i] = one_minus(g, e.a[i]);
-            e.d[i] = Rows<IO, kSeg>::read(s + R::kG, i, lane);
-            if (kSeqs && (e.m.start >> i & 1u) && p.dh_final) {
-                const int q = __shfl_sync(0xffffffffu, e.m.seq, i);
-                e.d[i] = add2(e.d[i], load_state<kCopy>(p.dh_final + (size_t)q * D + c, mine));
-            }
-        }
-        Run run{e.a[0], mul2(e.a[0], e.d[0])};
-        if (!kSeqs || !e.m.start) {
-#pragma unroll
-            for (int i = 1; i < kSeg; ++i) {
-                run.H = mul2(e.a[i], add2(e.d[i], run.H));
-                run.A = mul2(run.A, e.a[i]);
-            }
-        } else {
-#pragma unroll
-            for (int i = 1; i < kSeg; ++i)
-                run.H = mul2(e.a[i], pick2(e.m.start >> i & 1u, e.d[i], add2(e.d[i], run.H)));
-            run.A = f2(kReset);
-        }
-        return run;
-    };
-
-    const long long next = (long long)dir * D;
-    long long out = (long long)base + (origin + (long long)dir * first0) * D + 2 * lane;
-    auto finish = [&](int k, const Els& e, F2 mu) {
-        // the second ring's tile k came in the group before the last; behind the last tile nothing
-        // was formed
-        if (k + 1 == steps) copy_wait<0>(); else copy_wait<1>();
-        __syncwarp();
-        const char* s = late + (k & 1) * R::kLate;
-        const int first = first0 + k * stride, n = L - first;
-        long long at = out;
-        out += hop;
-        // the gradients of token i of the run, at element `at`, h of the token before being hp
-        auto element = [&](int i, F2 lam, F2 hp) {
-            if constexpr (kWrite == GDR_WRITE_PLAIN) {
-                store_pair<IO, kCopy>(p.dv + at, lam, mine);
-            } else {
-                const F2 v = Rows<IO, kSeg>::read(s + R::v, i, lane);
-                if constexpr (kWrite == GDR_WRITE_GATE) {
-                    store_pair<GT, kCopy>(p.dbeta + at, mul2(lam, v), mine);
-                    store_pair<IO, kCopy>(
-                        p.dv + at, mul2(lam, Rows<GT, kSeg>::read(s + R::beta, i, lane)), mine);
-                } else {
-                    hp = add2(hp, f2(-v.lo(), -v.hi()));
-                    store_pair<IO, kCopy>(p.dv + at, mul2(e.w[i], lam), mine);
-                }
-            }
-            store_pair<GT, kCopy>(p.dg + at, mul2(mu, hp), mine);
-        };
-        if (kSeqs ? n >= kSeg && !e.m.any() : n > kSeg) {  // no sequence ends here
-#pragma unroll
-            for (int i = 0; i < kSeg; ++i, at += next) {
-                const F2 lam = add2(e.d[i], mu);
-                mu = mul2(e.a[i], lam);
-                element(i, lam, Rows<IO, kSeg>::read(s, i, lane));
-            }
-            return;
-        }
-#pragma unroll
-        for (int i = 0; i < kSeg; ++i, at += next) {
-            const bool ends = kSeqs ? (e.m.end >> i & 1u) : first + i == L - 1;
-            const int q = !kSeqs ? row : ends ? __shfl_sync(0xffffffffu, e.m.seq, i) : 0;
-            const F2 sum = add2(e.d[i], mu);
-            const F2 lam = kSeqs ? pick2(e.m.start >> i & 1u, e.d[i], sum) : sum;
-            mu = mul2(e.a[i], lam);
-            if (i >= n) continue;
-            F2 hp = Rows<IO, kSeg>::read(s, i, lane);
-            if (ends) {
-                hp = h0_row;
-                if (kSeqs && p.h0) hp = load_state<kCopy>(p.h0 + (size_t)q * D + c, mine);
-                if (p.dh0) store_pair<float, kCopy>(p.dh0 + (size_t)q * D + c, mu, mine);
-            }
-            element(i, lam, hp);
-        }
-    };
-    if constexpr (kCluster) {
-        scan_work<Els>(sh, steps, wid, lane, form, finish);
-    } else {
-        scan_walk<kSeqs, Els>(sh, steps, wid, lane, carry, form, finish);
-    }
-    copy_wait<0>();
-    scan_close<kCluster>();
-}
-
-template <typename IO, typename GT, int kWrite, Copy kCopy>
-gdr_status bwd_launch(const gdr_scan_args& a, const ScanPtrs& x, cudaStream_t st) {
-    const bool seqs = scan_one_row(a, x.cu);
-    BwdParams<IO, GT> p;
-    p.v = static_cast<const IO*>(x.v);
-    p.g = static_cast<const GT*>(x.g);
-    p.beta = static_cast<const GT*>(x.beta);
-    p.o = static_cast<const IO*>(x.o_in);
-    p.dO = static_cast<const IO*>(x.dO);
-    p.h0 = x.h0;
-    p.dh_final = x.dh_final;
-    p.dv = static_cast<IO*>(x.dv);
-    p.dg = static_cast<GT*>(x.dg);
-    p.dbeta = static_cast<GT*>(x.dbeta);
-    p.dh0 = x.dh0;
-    p.status = a.status;
-    p.q = Seqs{x.cu, a.n_seqs, a.T, a.B * a.T};
-    p.D = a.D;
-    p.L = seqs ? a.B * a.T : a.T;
-    p.slabs = (a.D + kSlab - 1) / kSlab;
-    p.reverse = a.reverse;
-    const long long units = (long long)p.slabs * (seqs ? 1 : a.B);
-    const int cluster = kCopy == kCopyOne ? 0 : scan_cluster(units);
-    // 16 warps' rings fit an SM's shared memory in bf16 only
-    constexpr int kWide = sizeof(IO) + sizeof(GT) == 4 ? 16 : 8;
-    auto launch = [&](auto kernel, int warps, int threads, size_t ring, size_t shared) {
-        const size_t smem = warps * ring + shared +
-                            (seqs ? kCuBytes : 0);
-        return scan_launch(kernel, p, units, cluster ? cluster : 1, threads, smem, st);
-    };
-    if constexpr (kCopy != kCopyOne) {
-        if (cluster) {
-            constexpr int kThreads = 32 * (kWide + 2);
-            constexpr size_t kShared = sizeof(ScanShared<kWide, true>);
-            constexpr size_t kRing = Ring<IO, GT, kWrite, seg_of<IO, GT>(true)>::kBytes;
-            return seqs ? launch(scan_bwd_kernel<IO, GT, kWrite, kCopy, true, true, kWide>, kWide, kThreads, kRing, kShared)
-                        : launch(scan_bwd_kernel<IO, GT, kWrite, kCopy, false, true, kWide>, kWide, kThreads, kRing, kShared);
-        }
-    }
-    constexpr size_t kRing = Ring<IO, GT, kWrite, seg_of<IO, GT>(false)>::kBytes;
-    return seqs ? launch(scan_bwd_kernel<IO, GT, kWrite, kCopy, true, false, 8>, 8, 256, kRing, sizeof(ScanShared<8, false>))
-                : launch(scan_bwd_kernel<IO, GT, kWrite, kCopy, false, false, 8>, 8, 256, kRing, sizeof(ScanShared<8, false>));
-}
-
-struct Bwd {
-    template <typename IO, typename GT, int kWrite>
-    static gdr_status go(const gdr_scan_args& a, const ScanPtrs& x, cudaStream_t st) {
-        const Copy copy = scan_copy(a);
-        if (copy == kCopy16) return bwd_launch<IO, GT, kWrite, kCopy16>(a, x, st);
-        if constexpr (sizeof(IO) == sizeof(GT)) {
-            if (copy == kCopyPair) return bwd_launch<IO, GT, kWrite, kCopyPair>(a, x, st);
-        }
-        return bwd_launch<IO, GT, kWrite, kCopyOne>(a, x, st);
-    }
-};
-
-}  // namespace
+extern template gdr_status scan_bwd_io<float>(const gdr_scan_args&, const ScanPtrs&, cudaStream_t);
+template gdr_status scan_bwd_io<__nv_bfloat16>(const gdr_scan_args&, const ScanPtrs&, cudaStream_t);
 
 gdr_status launch_scan_bwd(const gdr_scan_args& a, const ScanPtrs& x, cudaStream_t st) {
     if (a.B * (long long)a.T == 0) {
@@ -308,7 +15,7 @@ gdr_status launch_scan_bwd(const gdr_scan_args& a, const ScanPtrs& x, cudaStream
                                          : cudaMemsetAsync(x.dh0, 0, bytes, st);
         return e == cudaSuccess ? GDR_OK : GDR_ERR_CUDA;
     }
-    return scan_dispatch<Bwd>(a, x, st);
+    return a.io_dtype == GDR_BF16 ? scan_bwd_io<__nv_bfloat16>(a, x, st) : scan_bwd_io<float>(a, x, st);
 }
 
 }  // namespace gdr

@@ -3,12 +3,14 @@
 // joining of its pieces.
 //
 // A recurrence x <- a x + b over a run of tokens is the map x -> A x + H (A the product of the
-// decays, H the run's result from zero), and maps compose.  A block owns a slab of 64 channels
-// of one row, two per lane, and walks it in tiles of kWarps * kSeg tokens: a warp takes kSeg
-// tokens and forms its run's (A, H); the block's warps join theirs through shared memory,
-// in order.  Where rows and channels give too few blocks, the blocks of a cluster take
-// neighbouring tiles at once and join through distributed shared memory.  There is no other wait
-// between blocks, no workspace, and every join has a fixed order.
+// decays, H the run's result from zero), and maps compose.  A block owns a slab of 64 / kGroups
+// channels of one row, two per lane, and walks it in tiles.  A lane takes kSeg tokens of a tile;
+// the kGroups groups of lanes of a warp take runs that follow one another, and so do the warps.
+// Runs are formed, (A, H), and joined in order: a warp's by shuffles, a block's through shared
+// memory.  Where rows and channels give too few blocks, the blocks of a cluster take neighbouring
+// tiles at once and join through distributed shared memory; and with groups, slabs are narrower and
+// tiles longer, for more blocks and fewer steps.  There is no other wait between blocks, no
+// workspace, and every join has a fixed order.
 //
 // The walk is a pipeline.  A warp's tokens arrive by asynchronous copies, two tiles ahead, into
 // shared memory of its own, and it forms the run of tile k + 1 before it finishes tile k.  In a
@@ -31,7 +33,7 @@ namespace gdr {
 using namespace tc;
 
 constexpr int kScanMaxCluster = 8;             // a warp hands the block's run to one block
-constexpr int kSlab = 64;                      // channels of a block
+constexpr int kSlab = 64;                      // channels of a block without groups
 constexpr float kReset = -1.f;
 constexpr uint64_t kScanWaitNs = 2000000000ull;
 
@@ -72,11 +74,28 @@ __device__ __forceinline__ Run run_join(const Run& f, const Run& r) {
     return o;
 }
 
+// A warp's joined runs, behind the groups' own: what came before a group in its warp.
+template <int kGroups, bool kSeqs>
+__device__ __forceinline__ Run join_groups(Run& run, int lane) {
+    constexpr int n = 32 / kGroups;
+    auto up = [&](const Run& r, int by) {
+        return Run{F2{__shfl_up_sync(0xffffffffu, r.A.v, by)}, F2{__shfl_up_sync(0xffffffffu, r.H.v, by)}};
+    };
+#pragma unroll
+    for (int by = n; by < 32; by *= 2) {
+        const Run f = up(run, by);
+        if (lane >= by) run = run_join<kSeqs>(f, run);
+    }
+    const Run before = up(run, n);
+    return lane >= n ? before : Run{f2(1.f), f2(0.f)};
+}
+
 // In a single block runs go by tile modulo four: between the readings of tile k, behind the
 // barrier of its step, and the writing of tile k + 4 lies another step's barrier.  In a cluster
 // they go by tile parity: a worker forms tile k + 2 once it has the state of tile k, and the folder
-// has read that tile's runs by then.  Blocks' runs go by tile modulo four: a block sends tile j when its workers have the
-// states of tile j - 2, for which every block has sent tile j - 2, and so has folded tile j - 4.
+// has read that tile's runs by then.  Blocks' runs go by tile modulo four: a block sends tile j
+// when its workers have the states of tile j - 2, for which every block has sent tile j - 2, and so
+// has folded tile j - 4.
 template <int kWarps, bool kCluster>
 struct alignas(128) ScanShared {
     Run run[kCluster ? 2 : 4][kWarps][32];
@@ -140,19 +159,24 @@ __device__ __forceinline__ bool runs_here(uint64_t* bar_, uint32_t parity) {
     return true;
 }
 
-// A worker's walk in a cluster.
-template <typename E, int kWarps, typename Form, typename Finish>
+// A worker's walk in a cluster.  form returns the warp's joined runs in the last group, e.before
+// what came before the lane's group.
+template <int kGroups, bool kSeqs, typename E, int kWarps, typename Form, typename Finish>
 __device__ __forceinline__ void scan_work(ScanShared<kWarps, true>& sh, int steps, int wid, int lane,
                                           Form form, Finish finish) {
     const int formed = blockDim.x, folded = 32 * (kWarps + 1);
+    constexpr int n = 32 / kGroups;
     auto give = [&](int k, E& e) {
-        sh.run[k & 1][wid][lane] = form(k, e);
+        const Run run = form(k, e);
+        if (lane >= 32 - n) sh.run[k & 1][wid][lane - (32 - n)] = run;
         bar_arrive(kFormed + (k & 1), formed);
     };
     auto turn = [&](int k, E& now, E& next) {
         if (k + 1 < steps) give(k + 1, next);
         bar_sync(kFolded + (k & 1), folded);
-        finish(k, now, sh.before[k & 1][wid][lane]);
+        F2 x = sh.before[k & 1][wid][lane % n];
+        if (kGroups > 1) x = run_apply<kSeqs>(now.before, x);
+        finish(k, now, x);
     };
     E even, odd;
     give(0, even);
@@ -164,7 +188,7 @@ __device__ __forceinline__ void scan_work(ScanShared<kWarps, true>& sh, int step
 
 // The folder's walk.  False if a wait ran out; the walk then goes on without waiting, so that all
 // threads meet at the barriers.
-template <bool kSeqs, int kWarps>
+template <int kGroups, bool kSeqs, int kWarps>
 __device__ __forceinline__ bool scan_fold(ScanShared<kWarps, true>& sh, int steps, int cluster, int rank,
                                           int lane, F2& carry) {
     bool ok = true;
@@ -172,7 +196,7 @@ __device__ __forceinline__ bool scan_fold(ScanShared<kWarps, true>& sh, int step
         const int par = k & 1;
         bar_sync(kFormed + par, blockDim.x);
         uint64_t* full = &sh.full[k & 3];
-        if (lane == 0) mbar_expect_tx(full, (uint32_t)cluster * 32 * sizeof(Run));
+        if (lane == 0) mbar_expect_tx(full, (uint32_t)cluster * (32 / kGroups) * sizeof(Run));
         // the maps from the block's first token to every worker, while the other blocks' runs come
         Run to[kWarps];
 #pragma unroll
@@ -199,7 +223,7 @@ __device__ __forceinline__ bool scan_fold(ScanShared<kWarps, true>& sh, int step
 }
 
 // The publisher's walk: joins the block's runs of every tile and sends them to all blocks.
-template <bool kSeqs, int kWarps>
+template <int kGroups, bool kSeqs, int kWarps>
 __device__ __forceinline__ void scan_publish(ScanShared<kWarps, true>& sh, int steps, int cluster, int rank,
                                              int lane) {
     for (int k = 0; k < steps; ++k) {
@@ -209,6 +233,7 @@ __device__ __forceinline__ void scan_publish(ScanShared<kWarps, true>& sh, int s
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) all = run_join<kSeqs>(all, r[w][lane]);
         const uint32_t to = smem_u32(&sh.block[k & 3][rank][lane]), bar = smem_u32(&sh.full[k & 3]);
+        if (lane >= 32 / kGroups) continue;
         for (int b = 0; b < cluster; ++b)
             asm volatile(
                 "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];"
@@ -242,12 +267,16 @@ __device__ __forceinline__ void scan_close() {
 // channels (4 or 8 bytes) where D is even; else through registers, one element at a time.
 enum Copy { kCopy16, kCopyPair, kCopyOne };
 
-// A warp's kSeg rows of 64 channels of one tensor in shared memory.
-template <typename E, int kSeg>
+// A warp's kSeg * kGroups rows of kSlab / kGroups channels of one tensor in shared memory, the rows
+// of a group behind a row's width of padding, so that the groups read different banks.
+template <typename E, int kSeg, int kGroups>
 struct Rows {
-    static constexpr int kBytes = kSeg * kSlab * (int)sizeof(E);
+    static constexpr int kRow = kSlab / kGroups * (int)sizeof(E);
+    static constexpr int kPad = kGroups > 1 ? kRow : 0;
+    static constexpr int kBytes = kGroups * (kSeg * kRow + kPad);
     static __device__ __forceinline__ F2 read(const char* p, int i, int lane) {
-        const char* q = p + i * kSlab * (int)sizeof(E) + lane * 2 * (int)sizeof(E);
+        constexpr int n = 32 / kGroups;
+        const char* q = p + lane / n * (kSeg * kRow + kPad) + i * kRow + lane % n * 2 * (int)sizeof(E);
         if constexpr (sizeof(E) == 2) {
             const uint32_t r = *reinterpret_cast<const uint32_t*>(q);
             return f2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
@@ -259,52 +288,59 @@ struct Rows {
 
 // Copies a warp's rows of one tensor, tile after tile.  Place 0 of a row's order is token
 // `origin`, and the order goes up or (dir = -1) down the tokens; places at or behind L are zero.
-template <typename E, Copy kCopy, int kSeg>
+template <typename E, Copy kCopy, int kSeg, int kGroups>
 struct Feed {
+    using R = Rows<E, kSeg, kGroups>;
+    static constexpr int kWidth = kSlab / kGroups;            // channels
     static constexpr int kEls = kCopy == kCopy16 ? 16 / (int)sizeof(E) : 2;
-    static constexpr int kPerRow = kSlab / kEls;              // lanes of a row
+    static constexpr int kPerRow = kWidth / kEls;             // lanes of a row
     static constexpr int kRows = 32 / kPerRow;                // rows of one pass of the warp
-    static_assert(kSeg % kRows == 0, "a pass copies whole rows of a run");
+    static constexpr int kPasses = kSeg * kGroups / kRows;
+    static_assert(kSeg * kGroups % kRows == 0 && (kSeg % kRows == 0 || kRows % kSeg == 0),
+                  "a pass copies whole rows of a run, or of several");
     const E* at;        // the lane's part of its first row of the next tile
     long long pass;     // elements from a pass to the next
     uint32_t dst;       // the lane's place in a stage
     int row, left;
 
+    static __device__ __forceinline__ constexpr int pass_bytes(int m) {
+        return m * kRows * R::kRow + m * kRows / kSeg * R::kPad;
+    }
     // src: the slab's first channel of the row's first token; `first`: the place of the warp's
     // first row; left: channels of the slab
     __device__ __forceinline__ void open(const E* src, int origin, int dir, long long first, int D,
                                          int channels, int lane) {
         row = lane / kPerRow;
         const int col = lane % kPerRow * kEls;
-        left = channels - col;
+        left = channels < kWidth ? channels - col : kWidth;
         at = src + (origin + dir * (first + row)) * D + col;
         pass = (long long)dir * kRows * D;
-        dst = (uint32_t)(row * kSlab + col) * (uint32_t)sizeof(E);
+        dst = (uint32_t)(row * R::kRow + row / kSeg * R::kPad + col * (int)sizeof(E));
     }
     // `place`: the tile's first row of this warp; hop: elements to the next tile
     __device__ __forceinline__ void tile(char* stage, int place, int L, long long hop) {
         const E* p = at;
         at += hop;
         if constexpr (kCopy == kCopyOne) {
-            E r[kSeg / kRows][2];
+            E r[kPasses][2];
 #pragma unroll
-            for (int m = 0; m < kSeg / kRows; ++m) {
+            for (int m = 0; m < kPasses; ++m) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
                     r[m][j] = j < left && place + row + m * kRows < L ? p[j] : from_f<E>(0.f);
                 p += pass;
             }
-            E* q = reinterpret_cast<E*>(stage + dst);
 #pragma unroll
-            for (int m = 0; m < kSeg / kRows; ++m) {
-                q[m * kRows * kSlab] = r[m][0];
-                q[m * kRows * kSlab + 1] = r[m][1];
+            for (int m = 0; m < kPasses; ++m) {
+                E* q = reinterpret_cast<E*>(stage + dst + pass_bytes(m));
+                q[0] = r[m][0];
+                q[1] = r[m][1];
             }
         } else {
             const uint32_t q = smem_u32(stage) + dst;
 #pragma unroll
-            for (int m = 0; m < kSeg / kRows; ++m) {
-                copy_async<kEls * (int)sizeof(E)>(q + m * kRows * kSlab * (int)sizeof(E), p,
+            for (int m = 0; m < kPasses; ++m) {
+                copy_async<kEls * (int)sizeof(E)>(q + pass_bytes(m), p,
                                                   left > 0 && place + row + m * kRows < L);
                 p += pass;
             }
@@ -353,19 +389,20 @@ __device__ __forceinline__ Seqs share_cu(Seqs q, int32_t* room) {
     return q;
 }
 
-// Which of a warp's tokens start or end a sequence, in the kernel's order, and (in lane i) the
-// sequence of token i.
+// Which of a warp's rows start or end a sequence, in the kernel's order, and (in lane i) the
+// sequence of row i.
 struct Marks {
     unsigned start, end;
     int seq;
     __device__ __forceinline__ bool any() const { return (start | end) != 0; }
 };
 
-// The sequence met last, so that runs inside one sequence need no search.
+// The sequence met last, so that rows inside one sequence need no search.
 struct Here {
     int b, e;
 };
 
+// n rows from place `first` on
 __device__ __forceinline__ Marks find_marks(const Seqs& q, Here& here, int origin, int dir,
                                             int first, int n, int lane) {
     Marks m{0u, 0u, 0};
@@ -389,6 +426,24 @@ __device__ __forceinline__ Marks find_marks(const Seqs& q, Here& here, int origi
     return m;
 }
 
+// A lane's share of the marks: whether token i of its run starts or ends a sequence, and that
+// sequence.  All lanes of the warp.
+template <int kSeg>
+struct Mark {
+    unsigned start, end;  // of the lane's run
+    int base;
+    __device__ __forceinline__ Mark(const Marks& m, int group) : base(group * kSeg) {
+        start = m.start >> base;
+        end = m.end >> base;
+    }
+    __device__ __forceinline__ bool starts(int i) const { return start >> i & 1u; }
+    __device__ __forceinline__ bool ends(int i) const { return end >> i & 1u; }
+    __device__ __forceinline__ int seq(const Marks& m, int i) const {
+        return __shfl_sync(0xffffffffu, m.seq, base + i);
+    }
+    __device__ __forceinline__ bool any_start() const { return (start & ((1u << kSeg) - 1)) != 0; }
+};
+
 // ---- launching ---------------------------------------------------------------------------------
 
 // Whether one row of the kernel holds all sequences: packed ones, and rows that would not fill
@@ -402,17 +457,28 @@ inline Copy scan_copy(const gdr_scan_args& a) {
     return a.D % (f32 ? 4 : 8) == 0 ? kCopy16 : a.D % 2 == 0 && !mixed ? kCopyPair : kCopyOne;
 }
 
-// How a call's units (slabs times rows) are laid out.  Many: a block each, two on an SM.  Few: a
-// cluster each, of as many blocks as the GPU holds at once, one on an SM.  (The blocks of a cluster
-// are in one part of the GPU: the occupancy query counts 74 clusters of 2, 45 of 3, 33 of 4, 26
-// of 5, 22 of 6 and 15 of 7 or 8.)
-// 0: single blocks.
-inline int scan_cluster(long long units) {
+// How a call is laid out.  Many slabs of 64 channels: a block each, two on an SM (cluster 0).  Few:
+// clusters, one block on an SM, of slabs so wide (groups) and of so many blocks that the walk takes
+// the fewest steps; a step takes about the same time in all of them.  The blocks of a cluster are
+// in one part of the GPU: the occupancy query counts 148 clusters of 1 block, 74 of 2, 45 of 3, 33
+// of 4, 26 of 5, 22 of 6 and 15 of 7 or 8.
+struct ScanPlan {
+    int groups, cluster;
+};
+inline ScanPlan scan_plan(int D, long long rows, long long L, int block_rows) {
     static const unsigned char most[kScanMaxCluster + 1] = {0, 148, 74, 45, 33, 26, 22, 15, 15};
-    if (units > 74) return units <= 148 ? 1 : 0;
-    int c = kScanMaxCluster;
-    while (units > most[c]) --c;
-    return c;
+    if ((D + kSlab - 1) / kSlab * rows > 148) return {1, 0};
+    ScanPlan best{1, 0};
+    long long fewest = -1;
+    for (int g = 1; g <= 4; g *= 2) {
+        const long long units = (D + kSlab / g - 1) / (kSlab / g) * rows;
+        for (int c = 1; c <= kScanMaxCluster; ++c) {
+            if (units > most[c]) break;
+            const long long stride = (long long)block_rows * g * c, steps = (L + stride - 1) / stride;
+            if (fewest < 0 || steps < fewest) { fewest = steps; best = {g, c}; }
+        }
+    }
+    return best;
 }
 
 template <typename P>
@@ -445,14 +511,15 @@ gdr_status scan_dispatch_write(const gdr_scan_args& a, const ScanPtrs& x, cudaSt
     }
 }
 
-template <typename Op>
-gdr_status scan_dispatch(const gdr_scan_args& a, const ScanPtrs& x, cudaStream_t st) {
-    using bf = __nv_bfloat16;
-    if (a.io_dtype == GDR_BF16)
-        return a.gate_dtype == GDR_BF16 ? scan_dispatch_write<Op, bf, bf>(a, x, st)
-                                        : scan_dispatch_write<Op, bf, float>(a, x, st);
-    return a.gate_dtype == GDR_BF16 ? scan_dispatch_write<Op, float, bf>(a, x, st)
-                                    : scan_dispatch_write<Op, float, float>(a, x, st);
+template <typename Op, typename IO>
+gdr_status scan_dispatch_gate(const gdr_scan_args& a, const ScanPtrs& x, cudaStream_t st) {
+    return a.gate_dtype == GDR_BF16 ? scan_dispatch_write<Op, IO, __nv_bfloat16>(a, x, st)
+                                    : scan_dispatch_write<Op, IO, float>(a, x, st);
 }
+
+template <int kValue>
+struct Int {
+    static constexpr int value = kValue;
+};
 
 }  // namespace gdr
