@@ -259,6 +259,14 @@ scan_bwd_kernel(const BwdParams<IO, GT> p, const int cluster) {
     scan_close<kCluster>();
 }
 
+// Slabs times rows from which single blocks are faster than clusters of one.  With beta: with 128
+// of them 172 us against 196 (2 x 8192 x 4096 in bf16), with 75 of them 68 against 59 (15 x 2677 x
+// 296), copied one by one 168 against 211 (15 x 2677 x 291).  Tied, with 128 of them: 209 against
+// 168 (4 x 8192 x 2048).
+template <int kWrite>
+constexpr int kSingleFrom = kWrite == GDR_WRITE_GATE ? 112 : 149;
+constexpr int kSingleOne = 75;
+
 template <typename IO, typename GT, int kWrite, Copy kCopy>
 gdr_status bwd_launch(const gdr_scan_args& a, const ScanPtrs& x, cudaStream_t st) {
     const bool seqs = scan_one_row(a, x.cu);
@@ -282,7 +290,8 @@ gdr_status bwd_launch(const gdr_scan_args& a, const ScanPtrs& x, cudaStream_t st
     // 16 warps' rings fit an SM's shared memory in bf16 only
     constexpr int kWide = sizeof(IO) + sizeof(GT) == 4 ? 16 : 8;
     const long long rows = seqs ? 1 : a.B;
-    const ScanPlan plan = scan_plan(a.D, rows, p.L, kWide * seg_of<IO, GT>(true));
+    const ScanPlan plan = scan_plan(a.D, rows, p.L, kWide * seg_of<IO, GT>(true),
+                                    kCopy == kCopyOne ? kSingleOne : kSingleFrom<kWrite>);
     const int width = kSlab / plan.groups;
     p.slabs = (a.D + width - 1) / width;
     auto launch = [&](auto kernel, int warps, int threads, size_t ring, size_t shared) {

@@ -208,6 +208,11 @@ scan_fwd_kernel(const FwdParams<IO, GT> p, const int cluster) {
     scan_close<kCluster>();
 }
 
+// Slabs times rows from which single blocks are faster than clusters of one: with 128 of them and
+// beta 100 us against 118 (2 x 8192 x 4096 in bf16), with 75 of them 43 against 41 (15 x 2677 x
+// 296), and copied one by one 96 against 147 (15 x 2677 x 291).
+constexpr int kSingleFrom = 112, kSingleOne = 75;
+
 template <typename IO, typename GT, int kWrite, Copy kCopy>
 gdr_status fwd_launch(const gdr_scan_args& a, const ScanPtrs& x, cudaStream_t st) {
     const bool seqs = scan_one_row(a, x.cu);
@@ -223,9 +228,11 @@ gdr_status fwd_launch(const gdr_scan_args& a, const ScanPtrs& x, cudaStream_t st
     p.D = a.D;
     p.L = seqs ? a.B * a.T : a.T;
     p.reverse = a.reverse;
-    constexpr int kSeg = seg_of<IO, GT>, kWide = 16;
+    constexpr int kSeg = seg_of<IO, GT>;
+    constexpr int kWide = 14;  // workers: with the two other warps 128 registers a thread (16: 96)
     const long long rows = seqs ? 1 : a.B;
-    const ScanPlan plan = scan_plan(a.D, rows, p.L, kWide * kSeg);
+    const ScanPlan plan = scan_plan(a.D, rows, p.L, kWide * kSeg,
+                                    kCopy == kCopyOne ? kSingleOne : kSingleFrom);
     const int width = kSlab / plan.groups;
     p.slabs = (a.D + width - 1) / width;
     auto launch = [&](auto kernel, int warps, int threads, size_t stage, size_t shared) {

@@ -465,9 +465,9 @@ inline Copy scan_copy(const gdr_scan_args& a) {
 struct ScanPlan {
     int groups, cluster;
 };
-inline ScanPlan scan_plan(int D, long long rows, long long L, int block_rows) {
+inline ScanPlan scan_plan(int D, long long rows, long long L, int block_rows, int single_from) {
     static const unsigned char most[kScanMaxCluster + 1] = {0, 148, 74, 45, 33, 26, 22, 15, 15};
-    if ((D + kSlab - 1) / kSlab * rows > 148) return {1, 0};
+    if ((D + kSlab - 1) / kSlab * rows >= single_from) return {1, 0};
     ScanPlan best{1, 0};
     long long fewest = -1;
     for (int g = 1; g <= 4; g *= 2) {
