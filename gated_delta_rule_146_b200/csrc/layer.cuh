@@ -42,6 +42,7 @@ struct Seqs {
 __device__ __forceinline__ void check_cu(const Seqs& q, int* status, int tid, int threads) {
     if (!q.cu || !status) return;
     bool bad = false;
+#pragma unroll 4
     for (int s = tid; s <= q.n; s += threads) {
         const int x = q.cu[s];
         bad |= (s == 0 && x != 0) || (s == q.n && x != q.total) || (s > 0 && x < q.cu[s - 1]);

@@ -74,15 +74,12 @@ scan_fwd_kernel(const FwdParams<IO, GT> p, const int cluster) {
     Seqs seqs = p.q;
     if constexpr (kSeqs) seqs = share_cu(p.q, reinterpret_cast<int32_t*>(smem + sizeof(sh)));
     scan_open<kCluster>(sh.full);
-    if (kSeqs && blockIdx.x == 0) check_cu(p.q, p.status, tid, 32 * (kWarps + 2 * kCluster));
-    if (kSeqs && rank == 0 && p.h_final) {  // empty sequences keep their state
-        for (int s = wid; s < seqs.n; s += kWarps + 2 * kCluster) {
-            if (seqs.begin(s) != seqs.end(s)) continue;
-            F2 x = f2(0.f);
-            if (p.h0) x = load_state<kCopy>(p.h0 + (size_t)s * D + c, mine);
+    if (kSeqs && blockIdx.x == 0) check_cu(seqs, p.status, tid, 32 * (kWarps + 2 * kCluster));
+    if (kSeqs && rank == 0 && p.h_final)  // empty sequences keep their state
+        each_empty(seqs, wid, kWarps + 2 * kCluster, lane, [&](int s) {
+            const F2 x = p.h0 ? load_state<kCopy>(p.h0 + (size_t)s * D + c, mine) : f2(0.f);
             store_pair<float, kCopy>(p.h_final + (size_t)s * D + c, x, mine);
-        }
-    }
+        });
 
     const size_t base = (size_t)row * L * D + slab * kWidth;
     const int stride = cluster * kTile, first0 = rank * kTile + wid * kRows;

@@ -389,6 +389,17 @@ __device__ __forceinline__ Seqs share_cu(Seqs q, int32_t* room) {
     return q;
 }
 
+// Calls f(s) in all lanes of a warp for the warp's share of the empty sequences.
+template <typename F>
+__device__ __forceinline__ void each_empty(const Seqs& q, int wid, int warps, int lane, F f) {
+    if (!q.cu) return;  // rows of at least a token
+    for (long long s0 = wid * 32; s0 < q.n; s0 += warps * 32) {
+        const int s = (int)s0 + lane;
+        unsigned m = __ballot_sync(0xffffffffu, s0 + lane < q.n && q.begin(s) == q.end(s));
+        for (; m; m &= m - 1) f((int)s0 + __ffs(m) - 1);
+    }
+}
+
 // Which of a warp's rows start or end a sequence, in the kernel's order, and (in lane i) the
 // sequence of row i.
 struct Marks {

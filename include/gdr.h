@@ -359,7 +359,8 @@ gdr_status gdr_decode_step(const gdr_decode_args* args,
  * - No workspace except where a `_workspace_size` is declared.  A cu_seqlens that does not
  *   start at 0, decreases or does not end at T is reported as GDR_ERR_DEVICE_CHECK in
  *   args->status (an optional device int as in gdr_chunk_args); the outputs are then
- *   unspecified, but no access leaves the tensors.
+ *   unspecified, but no access leaves the tensors.  gdr_scan_fwd and gdr_scan_bwd report there
+ *   too (GDR_ERR_TIMEOUT) if a bounded wait between the blocks of a cluster ran out.
  * - Channel arrays (weights, biases, their gradients) are fp32 and 4-byte aligned, everything
  *   else 16-byte aligned.  An output may not overlap an input unless that is said.
  * - Sums, states and statistics are fp32; results are rounded once.  Repeated calls give the

@@ -95,6 +95,12 @@ def test_without_bias_or_state():
     compare(make([33] * 2, 40, bias=False, state=False, seed=2, rows=True))
 
 
+def test_thousands_of_sequences():
+    lengths = torch.randint(0, 5, (2500,), generator=torch.Generator().manual_seed(9)).tolist()
+    compare(make(lengths, 36, 4, "bf16", seed=9))
+    compare(make(lengths, 33, 3, "f32", seed=10), True)
+
+
 def test_long_runs():
     """More tokens than the runs of one wave of warps: the partial sums span many blocks."""
     compare(make([9000, 3001], 8, 4, "f32", seed=3))

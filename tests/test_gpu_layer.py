@@ -125,3 +125,49 @@ def test_tensors_of_another_device_than_the_current_one():
     with torch.cuda.device(1):
         assert torch.equal(a, gdr.short_conv_fwd(x, w)[0])
         assert torch.equal(b, gdr.linear_scan_fwd(x, -x.abs())[0])
+
+
+def _tail(t, n):
+    return t[:, -n:].contiguous()
+
+
+def test_offsets_beyond_31_bits():
+    """More than 2^31 elements a tensor: the last tokens, cut off from the others by the
+    operators' own means, equal the same tokens in a short call."""
+    D, n = 4096, 700
+    T = (1 << 31) // D + 1000
+    gen = torch.Generator("cuda").manual_seed(1)
+    x = torch.empty(1, T, D, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    cu = torch.tensor([0, T - n, T], dtype=torch.int32, device="cuda")
+    one = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    g = torch.empty_like(x).uniform_(-1.0, -0.1, generator=gen)
+    close = lambda a, b: ((a.float() - b.float()).abs() <= 2.0 ** -7 * b.float().abs() + 1e-3).all()  # noqa: E731
+    o, hf = gdr.linear_scan_fwd(x, g, None, None, cu)
+    os_, hs = gdr.linear_scan_fwd(_tail(x, n), _tail(g, n), None, None, one)
+    assert close(_tail(o, n), os_) and (hf[1] - hs[0]).abs().max() < 1e-4
+    dv, dg, _, _ = gdr.linear_scan_bwd(x, g, None, o, x, None, cu)
+    a = gdr.linear_scan_bwd(_tail(x, n), _tail(g, n), None, _tail(o, n), _tail(x, n), None, one)
+    assert close(_tail(dv, n), a[0]) and close(_tail(dg, n), a[1])
+    del dv, dg, g
+    w = torch.randn(D, 4, device="cuda", generator=gen)
+    y, st = gdr.short_conv_fwd(x, w, cu_seqlens=cu)
+    ys, ss = gdr.short_conv_fwd(_tail(x, n), w, cu_seqlens=one)
+    assert torch.equal(_tail(y, n), ys) and torch.equal(st[1:], ss)
+    dx = gdr.short_conv_bwd(x, w, None, o, None, cu)[0]
+    assert torch.equal(_tail(dx, n), gdr.short_conv_bwd(_tail(x, n), w, None, _tail(o, n), None, one)[0])
+    del dx, y
+    h = (1, T, 32, 128)
+    nw = torch.rand(32, 128, device="cuda", generator=gen) + 0.5
+    for per in ("token", "sequence"):
+        big = gdr.group_norm_fwd(x.view(h), nw, None, o.view(h), cu, per=per, output_stats=per == "sequence")
+        small = gdr.group_norm_fwd(_tail(x, n).view(1, n, 32, 128), nw, None,
+                                   _tail(o, n).view(1, n, 32, 128), one, per=per,
+                                   output_stats=per == "sequence")
+        big, st = big if per == "sequence" else (big, None)
+        small, ss = small if per == "sequence" else (small, None)
+        assert close(_tail(big, n), small)
+        a = gdr.group_norm_bwd(x.view(h), nw, None, None, o.view(h), cu, per=per, stats=st)[0]
+        b = gdr.group_norm_bwd(_tail(x, n).view(1, n, 32, 128), nw, None, None,
+                               _tail(o, n).view(1, n, 32, 128), one, per=per, stats=ss)[0]
+        assert close(_tail(a, n), b)
+        del big, a

@@ -111,6 +111,11 @@ def test_sequence_lengths(lengths):
     compare(make(lengths, 2, 48, "bf16", gate=False, seed=4), "sequence", False)
 
 
+def test_thousands_of_sequences():
+    lengths = torch.randint(0, 4, (1500,), generator=torch.Generator().manual_seed(15)).tolist()
+    compare(make(lengths, 2, 32, "bf16", seed=15), "sequence")
+
+
 def test_rows_and_many_tokens():
     compare(make([130] * 3, 4, 64, "bf16", seed=5, rows=True), "sequence")
     compare(make([130] * 3, 4, 64, "bf16", seed=6, rows=True), "token")

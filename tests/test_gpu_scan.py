@@ -91,6 +91,25 @@ def test_widths(D):
     compare(make([90, 17], D, "bf16", write="gate", seed=D))
 
 
+@pytest.mark.parametrize("D", [8, 24, 50, 77, 96, 200, 520, 1032])
+@pytest.mark.parametrize("io,write", [("bf16", "gate"), ("f32", "tied"), ("bf16", "plain")])
+def test_layouts(D, io, write):
+    """Widths that are laid out as clusters of other sizes and groups, over several steps, with
+    bounds of sequences at odd places."""
+    r = np.random.default_rng(D)
+    cuts = np.sort(r.integers(0, 2500, 9))
+    lengths = np.diff(np.concatenate([[0], cuts, [2500]])).tolist()
+    compare(make(lengths, D, io, write=write, seed=D), reverse=D % 3 == 0)
+    compare(make([1300, 1300], D, io, write=write, seed=D, rows=True), reverse=D % 3 == 1)
+
+
+def test_thousands_of_sequences():
+    """More sequences than the kernels keep bounds of, many of them empty."""
+    r = np.random.default_rng(5)
+    compare(make(r.integers(0, 4, 2500).tolist(), 72, "bf16", write="gate", seed=6))
+    compare(make(r.integers(0, 3, 1500).tolist(), 33, "f32", seed=7), True)
+
+
 @pytest.mark.parametrize("B,T", [(1, 1), (3, 7), (2, 63), (2, 64), (5, 200), (1, 4099)])
 @pytest.mark.parametrize("reverse", [False, True])
 def test_rows(B, T, reverse):
