@@ -113,32 +113,32 @@ struct Ring {
     static constexpr int kBytes = kStages * kT * kBatch * kConvThreads * (int)sizeof(V);
     V* slot;              // the thread's first
     const IO* at[kT];     // the next token to be fetched
-    int ask, have, n;     // batches asked for, used, in all
+    int ask, have, n;     // batches asked for and used, tokens in all
 
     __device__ __forceinline__ V* place(int stage, int t, int u) {
         return slot + ((stage * kT + t) * kBatch + u) * kConvThreads;
     }
     __device__ __forceinline__ void next(long long hop, int left) {
-        if (ask < n) {
+        const int rest = n - ask * kBatch;
 #pragma unroll
-            for (int t = 0; t < kT; ++t) {
+        for (int t = 0; t < kT; ++t) {
 #pragma unroll
-                for (int u = 0; u < kBatch; ++u) {
-                    V* to = place(ask % kStages, t, u);
-                    if constexpr (kWhole) copy_async<(int)sizeof(V)>(smem_u32(to), at[t], true);
-                    else *to = fetch<IO, N, false>(at[t], left);
-                    at[t] += hop;
-                }
+            for (int u = 0; u < kBatch; ++u) {
+                if (u >= rest) break;
+                V* to = place(ask % kStages, t, u);
+                if constexpr (kWhole) copy_async<(int)sizeof(V)>(smem_u32(to), at[t], true);
+                else *to = fetch<IO, N, false>(at[t], left);
+                at[t] += hop;
             }
         }
         ++ask;
         copy_commit();
     }
-    // n batches from the given tokens on
-    __device__ __forceinline__ void open(char* smem, int thread, int batches, long long hop, int left) {
+    // `tokens` of them, from those at at[] on
+    __device__ __forceinline__ void open(char* smem, int thread, int tokens, long long hop, int left) {
         slot = reinterpret_cast<V*>(smem) + thread;
         ask = have = 0;
-        n = batches;
+        n = tokens;
         copy_wait<0>();
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) next(hop, left);
@@ -231,18 +231,21 @@ conv_fwd_kernel(const ConvParams<IO> p) {
             put<IO, N, kWhole>(out, y, left);
             out += hop;
         };
-        int i = i0;
         Ring<IO, N, kWhole, 1> ring;
         ring.at[0] = in;
-        ring.open(smem, wid * 32 + lane, (i1 - i0) / kBatch, hop, left);
-        for (; i + kBatch <= i1; i += kBatch) {
+        ring.open(smem, wid * 32 + lane, i1 - i0, hop, left);
+        for (int i = i0; i < i1; i += kBatch) {
             Vec<IO, N> v[1][kBatch];
             ring.take(v, hop, left);
+            if (i + kBatch <= i1) {
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) step(v[0][u]);
+                for (int u = 0; u < kBatch; ++u) step(v[0][u]);
+            } else {
+#pragma unroll
+                for (int u = 0; u < kBatch - 1; ++u)
+                    if (i + u < i1) step(v[0][u]);
+            }
         }
-        in += (long long)(i - i0) * hop;
-        for (; i < i1; ++i, in += hop) step(fetch<IO, N, kWhole>(in, left));
     }
 }
 
@@ -358,7 +361,7 @@ conv_bwd_kernel(const ConvParams<IO> p) {
                 Ring<IO, N, kWhole, 2> ring;
                 ring.at[0] = p.x + at;
                 ring.at[1] = p.dy + at;
-                ring.open(smem.ring, wid * 32 + lane, (i1 - i) / kBatch, hop, left);
+                ring.open(smem.ring, wid * 32 + lane, (i1 - i) / kBatch * kBatch, hop, left);
                 for (; i + kBatch <= i1; i += kBatch) {
                     Vec<IO, N> v[2][kBatch];
                     ring.take(v, hop, left);
