@@ -70,25 +70,21 @@ norm_token_fwd(const NormParams<typename S::IO> p, int used, long long slots) {
     const Pairs<S> b = load_affine<S>(p.b, 0.f, head, l, p.d, p.shared);
     const bool gate = p.z != nullptr;
     const typename S::IO* const src[2] = {p.x, p.z};
-    Ring<S, 2> ring(smem, l, p.d, gate ? 2 : 1);
     const size_t hop = (size_t)slots * p.d;
-    long long ask_row = slot;
-    size_t ask_at = (size_t)slot * p.d, at = ask_at;
-    auto ask = [&] {
-        ring.ask(src, ask_at, on && ask_row < p.rows);
-        ask_row += slots;
-        ask_at += hop;
-    };
-#pragma unroll
-    for (int i = 0; i < S::kStages - 1; ++i) ask();
-    // every lane takes part in the group sums until the block's last row
-    for (long long r0 = (long long)blockIdx.x * used; r0 < p.rows; r0 += slots, at += hop) {
+    size_t at = (size_t)slot * p.d;
+    // the slot's rows, and the most a slot of the block has: every lane takes part in the group sums
+    // until then
+    const int mine = on && slot < p.rows ? (int)((p.rows - 1 - slot) / slots) + 1 : 0;
+    const long long slot0 = (long long)blockIdx.x * used;
+    const int most = slot0 < p.rows ? (int)((p.rows - 1 - slot0) / slots) + 1 : 0;
+    Ring<S, 2> ring(smem, l, p.d, gate ? 2 : 1, (long long)hop);
+    ring.open(src, mine ? at : 0, mine);
+    for (int i = 0; i < most; ++i, at += hop) {
         Raw<S> raw[2];
-        ring.take(raw);
-        ask();
+        ring.take(src, raw);
         Pairs<S> x = widen<S>(raw[0]);
         const float rstd = token_stats<S>(x, l, p.d, p.center, p.eps);
-        if (on && r0 + g < p.rows)
+        if (i < mine)
             with_form(p.act, gate, [&](auto form) {
                 store_row<S>(p.y + at, l, p.d, norm_rows<S>(form, x, w, b, raw[1], rstd));
             });
@@ -96,7 +92,7 @@ norm_token_fwd(const NormParams<typename S::IO> p, int used, long long slots) {
     copy_wait<0>();
 }
 
-template <typename S>
+template <typename S, bool kBias>
 __global__ void __launch_bounds__(kNormThreads, S::kResident)
 norm_token_bwd(const NormParams<typename S::IO> p, int used, long long slots) {
     extern __shared__ __align__(16) char smem[];
@@ -110,28 +106,25 @@ norm_token_bwd(const NormParams<typename S::IO> p, int used, long long slots) {
     const bool gate = p.z != nullptr;
     const float inv = 1.f / p.d;
     const typename S::IO* const src[3] = {p.x, p.dy, p.z};
-    Ring<S, 3> ring(smem, l, p.d, gate ? 3 : 2);
     const size_t hop = (size_t)slots * p.d;
-    long long ask_row = slot;
-    size_t ask_at = (size_t)slot * p.d, at = ask_at;
-    auto ask = [&] {
-        ring.ask(src, ask_at, on && ask_row < p.rows);
-        ask_row += slots;
-        ask_at += hop;
-    };
-#pragma unroll
-    for (int i = 0; i < S::kStages - 1; ++i) ask();
-    for (long long r0 = (long long)blockIdx.x * used; r0 < p.rows; r0 += slots, at += hop) {
+    size_t at = (size_t)slot * p.d;
+    // the slot's rows, and the most a slot of the block has: every lane takes part in the group sums
+    // until then
+    const int mine = on && slot < p.rows ? (int)((p.rows - 1 - slot) / slots) + 1 : 0;
+    const long long slot0 = (long long)blockIdx.x * used;
+    const int most = slot0 < p.rows ? (int)((p.rows - 1 - slot0) / slots) + 1 : 0;
+    Ring<S, 3> ring(smem, l, p.d, gate ? 3 : 2, (long long)hop);
+    ring.open(src, mine ? at : 0, mine);
+    for (int i = 0; i < most; ++i, at += hop) {
         Raw<S> raw[3];
-        ring.take(raw);
-        ask();
-        const bool in = on && r0 + g < p.rows;
+        ring.take(src, raw);
+        const bool in = i < mine;
         Pairs<S> x = widen<S>(raw[0]);
         float rstd = token_stats<S>(x, l, p.d, p.center, p.eps);
         if (!in) rstd = 0.f;  // zeros throughout: nothing for the sums
         Back<S> o;
         with_form(p.act, gate, [&](auto form) {
-            o = back_rows<S, true>(form, x, raw[1], raw[2], w, b, rstd, dw, db);
+            o = back_rows<S, true, kBias>(form, x, raw[1], raw[2], w, b, rstd, dw, db);
         });
         const float mq = p.center ? group_sum<S::LPG>(o.s1) * inv : 0.f;
         const float mqn = group_sum<S::LPG>(o.s2) * inv;
@@ -149,7 +142,7 @@ norm_token_bwd(const NormParams<typename S::IO> p, int used, long long slots) {
     float* const sh = reinterpret_cast<float*>(smem);  // in the rings' place
     static_assert(sizeof(float) * S::kGroups * kCh <= Ring<S, 3>::kBytes, "the rings are larger");
     const int heads = p.shared ? 1 : p.H <= S::kGroups ? p.H : 0;
-    for (int which = 0; which < 2; ++which) {
+    for (int which = 0; which < 1 + kBias; ++which) {
 #pragma unroll
         for (int k = 0; k < S::NV; ++k) {
             if (heads == 0) {  // more heads than lane groups: nothing to join
@@ -225,7 +218,10 @@ struct TokenBwd {
         const Deal d = deal(a, S::kGroups, S::kResident, kPerSlot);
         auto p = norm_params<typename S::IO>(a, x);
         if (!x.dw && !x.db) p.part = nullptr;
-        norm_launch<Ring<S, 3>::kBytes>(norm_token_bwd<S>, d.blocks, st, p, d.used, d.slots);
+        if (x.b || x.db)
+            norm_launch<Ring<S, 3>::kBytes>(norm_token_bwd<S, true>, d.blocks, st, p, d.used, d.slots);
+        else
+            norm_launch<Ring<S, 3>::kBytes>(norm_token_bwd<S, false>, d.blocks, st, p, d.used, d.slots);
         if (p.part) launch_norm_reduce(a, x.ws, d.part_rows, x.dw, x.db, st);
     }
 };

@@ -81,47 +81,59 @@ __device__ __forceinline__ Raw<S> load_row(const typename S::IO* p, int l, int d
 // barrier.  Tensors behind the first `used` are left out.
 template <typename S, int kT>
 struct Ring {
-    using V = Vec<typename S::IO, S::VEC>;
-    static constexpr int kBytes = S::kStages * kT * S::NV * kNormThreads * (int)sizeof(V);
-    V* slot;
-    int l, d, used, put, got;
+    using IO = typename S::IO;
+    using V = Vec<IO, S::VEC>;
+    static constexpr int kStage = kT * S::NV * kNormThreads;   // vectors of a stage
+    static constexpr int kBytes = S::kStages * kStage * (int)sizeof(V);
+    V* first;
+    long long at, hop;  // the lane's first channel of the row to be asked for; elements to the next
+    int put, got;       // stages' first vectors
+    int l, d, used, rest;
 
-    __device__ __forceinline__ Ring(char* smem, int l_, int d_, int used_)
-        : slot(reinterpret_cast<V*>(smem) + threadIdx.x), l(l_), d(d_), used(used_), put(0), got(0) {}
-    __device__ __forceinline__ V* place(int stage, int t, int k) {
-        return slot + ((stage * kT + t) * S::NV + k) * kNormThreads;
-    }
-    // asks for the row at element `at` of every tensor (zeros if not `on`)
-    __device__ __forceinline__ void ask(const typename S::IO* const (&base)[kT], size_t at, bool on) {
+    __device__ __forceinline__ Ring(char* smem, int l_, int d_, int used_, long long hop_)
+        : first(reinterpret_cast<V*>(smem) + threadIdx.x), hop(hop_), l(l_), d(d_), used(used_) {}
+    // asks for the next row of the tensors, if there is one, and commits
+    __device__ __forceinline__ void ask(const IO* const (&base)[kT]) {
 #pragma unroll
         for (int t = 0; t < kT; ++t) {
             if (t >= used) break;
+            V* const to = first + put + t * S::NV * kNormThreads;
             if constexpr (S::kWhole) {
 #pragma unroll
-                for (int k = 0; k < S::NV; ++k) {
-                    const int c = (k * S::LPG + l) * S::VEC;
-                    const bool in = on && c < d;
-                    copy_async<16>(smem_u32(place(put, t, k)), base[t] + (in ? at + c : 0), in);
-                }
+                for (int k = 0; k < S::NV; ++k)
+                    copy_async<16>(smem_u32(to + k * kNormThreads), base[t] + at + k * S::LPG * S::VEC,
+                                   rest > 0 && (k * S::LPG + l) * S::VEC < d);
             } else {
-                const Raw<S> r = load_row<S>(base[t] + at, l, d, on);
+                const Raw<S> r = load_row<S>(base[t] + at - l * S::VEC, l, d, rest > 0);
 #pragma unroll
-                for (int k = 0; k < S::NV; ++k) *place(put, t, k) = r.v[k];
+                for (int k = 0; k < S::NV; ++k) to[k * kNormThreads] = r.v[k];
             }
         }
         copy_commit();
-        put = put == S::kStages - 1 ? 0 : put + 1;
+        at += hop;
+        --rest;
+        put = put == (S::kStages - 1) * kStage ? 0 : put + kStage;
     }
-    // the row asked for longest ago
-    __device__ __forceinline__ void take(Raw<S> (&r)[kT]) {
+    // `rows` rows from the ones at element `from` of the tensors on
+    __device__ __forceinline__ void open(const IO* const (&base)[kT], size_t from, int rows) {
+        copy_wait<0>();
+        put = got = 0;
+        rest = rows;
+        at = (long long)from + l * S::VEC;
+#pragma unroll
+        for (int i = 0; i < S::kStages - 1; ++i) ask(base);
+    }
+    // the row asked for longest ago; asks for another (zeros behind the last)
+    __device__ __forceinline__ void take(const IO* const (&base)[kT], Raw<S> (&r)[kT]) {
         copy_wait<S::kStages - 2>();
 #pragma unroll
         for (int t = 0; t < kT; ++t) {
             if (t >= used) break;
 #pragma unroll
-            for (int k = 0; k < S::NV; ++k) r[t].v[k] = *place(got, t, k);
+            for (int k = 0; k < S::NV; ++k) r[t].v[k] = first[got + (t * S::NV + k) * kNormThreads];
         }
-        got = got == S::kStages - 1 ? 0 : got + 1;
+        got = got == (S::kStages - 1) * kStage ? 0 : got + kStage;
+        ask(base);
     }
 };
 
@@ -256,13 +268,14 @@ __device__ __forceinline__ Pairs<S> norm_rows(Fm, const Pairs<S>& x, const Pairs
     return y;
 }
 
-// What the backward has of a row (x centred): n, q = du w, dz; du joins the sums for dw and db if kSums.
+// What the backward has of a row (x centred): n, q = du w, dz; du joins the sums for dw and (kBias)
+// db if kSums.  Without kBias there is no bias either: sixteen registers less.
 template <typename S>
 struct Back {
     Pairs<S> n, q, dz;
     float s1, s2;   // the lane's sums of q and q n
 };
-template <typename S, bool kSums, typename Fm>
+template <typename S, bool kSums, bool kBias, typename Fm>
 __device__ __forceinline__ Back<S> back_rows(Fm, const Pairs<S>& x, const Raw<S>& dy, const Raw<S>& z,
                                              const Pairs<S>& w, const Pairs<S>& b, float rstd,
                                              Pairs<S>& dw, Pairs<S>& db) {
@@ -274,7 +287,7 @@ __device__ __forceinline__ Back<S> back_rows(Fm, const Pairs<S>& x, const Raw<S>
 #pragma unroll
         for (int j = 0; j < S::VEC / 2; ++j) {
             const F2 n = mul2(x.f[k][j], r), g = pair_of(dy.v[k], j);
-            const F2 u = fma2(n, w.f[k][j], b.f[k][j]);
+            const F2 u = kBias ? fma2(n, w.f[k][j], b.f[k][j]) : mul2(n, w.f[k][j]);
             F2 a, da, du;
             act2_both<Fm::kAct, S::kFine>(Fm::kGate ? pair_of(z.v[k], j) : u, a, da);
             if constexpr (Fm::kGate) {
@@ -285,7 +298,7 @@ __device__ __forceinline__ Back<S> back_rows(Fm, const Pairs<S>& x, const Raw<S>
             }
             if (kSums) {
                 dw.f[k][j] = fma2(du, n, dw.f[k][j]);
-                db.f[k][j] = add2(db.f[k][j], du);
+                if (kBias) db.f[k][j] = add2(db.f[k][j], du);
             }
             const F2 q = mul2(du, w.f[k][j]);
             s1 = add2(s1, q);

@@ -139,25 +139,23 @@ norm_seq_apply(const NormParams<typename S::IO> p, int tokens) {
     const Pairs<S> b = load_affine<S>(p.b, 0.f, h, l, p.d, p.shared);
     const bool gate = p.z != nullptr;
     const typename S::IO* const src[2] = {p.x, p.z};
-    Ring<S, 2> ring(smem, l, p.d, gate ? 2 : 1);
     const size_t hop = (size_t)S::kGroups * p.H * p.d;
-    int ask_t = t0 + g;
-    size_t ask_at = ((size_t)ask_t * p.H + h) * p.d, at = ask_at;
-    auto ask = [&] {
-        ring.ask(src, ask_at, ask_t < t1);
-        ask_t += S::kGroups;
-        ask_at += hop;
-    };
-#pragma unroll
-    for (int i = 0; i < S::kStages - 1; ++i) ask();
+    const int mine = t0 + g < t1 ? (t1 - 1 - (t0 + g)) / S::kGroups + 1 : 0;
+    size_t at = mine ? ((size_t)(t0 + g) * p.H + h) * p.d : 0;
+    Ring<S, 2> ring(smem, l, p.d, gate ? 2 : 1, (long long)hop);
+    ring.open(src, at, mine);
     int s = t0 + g < t1 ? p.q.of(t0 + g) : 0;
     wait_before();  // for the statistics; the tensors are the caller's
+    int end = t0;   // of the sequence whose statistics are at hand
+    float2 st{};
     for (int t = t0 + g; t < t1; t += S::kGroups, at += hop) {
         Raw<S> raw[2];
-        ring.take(raw);
-        ask();
-        s = seq_from(p.q, s, t);
-        const float2 st = reinterpret_cast<const float2*>(p.stats)[(size_t)s * p.H + h];
+        ring.take(src, raw);
+        if (t >= end) {
+            s = seq_from(p.q, s, t);
+            end = s + 1 < p.q.n ? p.q.end(s) : t1;
+            st = reinterpret_cast<const float2*>(p.stats)[(size_t)s * p.H + h];
+        }
         Pairs<S> x = widen<S>(raw[0]);
         centre<S>(x, st.x, l, p.d);
         with_form(p.act, gate, [&](auto form) {
@@ -185,8 +183,8 @@ norm_seq_bwd_sums(const NormParams<typename S::IO> p, int tokens, float2* __rest
     Pairs<S> dw = fill<S>(0.f), db = fill<S>(0.f);
     const bool gate = p.z != nullptr;
     const typename S::IO* const src[3] = {p.x, p.dy, p.z};
-    Ring<S, 3> ring(smem, l, p.d, gate ? 3 : 2);
     const size_t hop = (size_t)S::kGroups * p.H * p.d;
+    Ring<S, 3> ring(smem, l, p.d, gate ? 3 : 2, (long long)hop);
     for (int s = t0 < t1 ? p.q.of(t0) : p.q.n; s < p.q.n; ++s) {
         const int sb = p.q.begin(s), se = p.q.end(s);
         if (sb >= t1) break;
@@ -194,26 +192,17 @@ norm_seq_bwd_sums(const NormParams<typename S::IO> p, int tokens, float2* __rest
         if (lo >= hi) continue;
         const float2 st = __ldg(reinterpret_cast<const float2*>(p.stats) + (size_t)s * p.H + h);
         float s1 = 0.f, s2 = 0.f;
-        int ask_t = lo + g;
-        size_t ask_at = ((size_t)ask_t * p.H + h) * p.d, at = ask_at;
-        auto ask = [&] {
-            ring.ask(src, ask_at, ask_t < hi);
-            ask_t += S::kGroups;
-            ask_at += hop;
-        };
-        copy_wait<0>();
-        ring.put = ring.got = 0;
-#pragma unroll
-        for (int i = 0; i < S::kStages - 1; ++i) ask();
+        const int mine = lo + g < hi ? (hi - 1 - (lo + g)) / S::kGroups + 1 : 0;
+        size_t at = mine ? ((size_t)(lo + g) * p.H + h) * p.d : 0;
+        ring.open(src, at, mine);
         for (int t = lo + g; t < hi; t += S::kGroups, at += hop) {
             Raw<S> raw[3];
-            ring.take(raw);
-            ask();
+            ring.take(src, raw);
             Pairs<S> x = widen<S>(raw[0]);
             centre<S>(x, st.x, l, p.d);
             Back<S> o;
             with_form(p.act, gate, [&](auto form) {
-                o = back_rows<S, true>(form, x, raw[1], raw[2], w, b, st.y, dw, db);
+                o = back_rows<S, true, true>(form, x, raw[1], raw[2], w, b, st.y, dw, db);
             });
             s1 += o.s1;
             s2 += o.s2;
@@ -290,30 +279,28 @@ norm_seq_bwd_apply(const NormParams<typename S::IO> p, int tokens,
     Pairs<S> none;
     const bool gate = p.z != nullptr;
     const typename S::IO* const src[3] = {p.x, p.dy, p.z};
-    Ring<S, 3> ring(smem, l, p.d, gate ? 3 : 2);
     const size_t hop = (size_t)S::kGroups * p.H * p.d;
-    int ask_t = t0 + g;
-    size_t ask_at = ((size_t)ask_t * p.H + h) * p.d, at = ask_at;
-    auto ask = [&] {
-        ring.ask(src, ask_at, ask_t < t1);
-        ask_t += S::kGroups;
-        ask_at += hop;
-    };
-#pragma unroll
-    for (int i = 0; i < S::kStages - 1; ++i) ask();
+    const int mine = t0 + g < t1 ? (t1 - 1 - (t0 + g)) / S::kGroups + 1 : 0;
+    size_t at = mine ? ((size_t)(t0 + g) * p.H + h) * p.d : 0;
+    Ring<S, 3> ring(smem, l, p.d, gate ? 3 : 2, (long long)hop);
+    ring.open(src, at, mine);
     int s = t0 + g < t1 ? p.q.of(t0 + g) : 0;
-    wait_before();  // for the statistics; the tensors are the caller's
+    wait_before();  // for the means; the tensors and statistics are the caller's
+    int end = t0;   // of the sequence whose statistics are at hand
+    float2 st{}, m{};
     for (int t = t0 + g; t < t1; t += S::kGroups, at += hop) {
         Raw<S> raw[3];
-        ring.take(raw);
-        ask();
-        s = seq_from(p.q, s, t);
-        const float2 st = __ldg(reinterpret_cast<const float2*>(p.stats) + (size_t)s * p.H + h);
-        const float2 m = means[(size_t)s * p.H + h];
+        ring.take(src, raw);
+        if (t >= end) {
+            s = seq_from(p.q, s, t);
+            end = s + 1 < p.q.n ? p.q.end(s) : t1;
+            st = __ldg(reinterpret_cast<const float2*>(p.stats) + (size_t)s * p.H + h);
+            m = means[(size_t)s * p.H + h];
+        }
         Pairs<S> x = widen<S>(raw[0]);
         centre<S>(x, st.x, l, p.d);
         with_form(p.act, gate, [&](auto form) {
-            const Back<S> o = back_rows<S, false>(form, x, raw[1], raw[2], w, b, st.y, none, none);
+            const Back<S> o = back_rows<S, false, true>(form, x, raw[1], raw[2], w, b, st.y, none, none);
             store_row<S>(p.dx + at, l, p.d, back_dx<S>(o, st.y, m.x, m.y));
         });
     }
