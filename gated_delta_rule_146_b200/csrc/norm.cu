@@ -93,7 +93,7 @@ norm_token_fwd(const NormParams<typename S::IO> p, int used, long long slots) {
 }
 
 template <typename S, bool kBias>
-__global__ void __launch_bounds__(kNormThreads, S::kResident)
+__global__ void __launch_bounds__(kNormThreads, S::kResidentSums)
 norm_token_bwd(const NormParams<typename S::IO> p, int used, long long slots) {
     extern __shared__ __align__(16) char smem[];
     const int g = threadIdx.x / S::LPG, l = threadIdx.x % S::LPG;
@@ -215,10 +215,11 @@ struct TokenFwd {
 struct TokenBwd {
     template <typename S>
     static void go(const gdr_norm_args& a, const NormPtrs& x, cudaStream_t st) {
-        const Deal d = deal(a, S::kGroups, S::kResident, kPerSlot);
+        const bool bias = x.b || x.db;
+        const Deal d = deal(a, S::kGroups, S::kResidentSums, kPerSlot);
         auto p = norm_params<typename S::IO>(a, x);
         if (!x.dw && !x.db) p.part = nullptr;
-        if (x.b || x.db)
+        if (bias)
             norm_launch<Ring<S, 3>::kBytes>(norm_token_bwd<S, true>, d.blocks, st, p, d.used, d.slots);
         else
             norm_launch<Ring<S, 3>::kBytes>(norm_token_bwd<S, false>, d.blocks, st, p, d.used, d.slots);
@@ -229,7 +230,7 @@ struct TokenBwd {
 struct TokenBwdSize {
     template <typename S>
     static void go(const gdr_norm_args& a, const NormPtrs& x, cudaStream_t) {
-        *reinterpret_cast<int*>(x.ws) = deal(a, S::kGroups, S::kResident, kPerSlot).part_rows;
+        *reinterpret_cast<int*>(x.ws) = deal(a, S::kGroups, S::kResidentSums, kPerSlot).part_rows;
     }
 };
 

@@ -36,7 +36,7 @@ constexpr int kHold = S::NV >= 8 ? 1 : 8 / S::NV;
 // part[(tile + s) * H + h] = (mean, sum of squares about it) of the piece's values; without
 // centering (0, sum of squares).
 template <typename S>
-__global__ void __launch_bounds__(kNormThreads)
+__global__ void __launch_bounds__(kNormThreads, 3)
 norm_seq_stats(const NormParams<typename S::IO> p) {
     constexpr int kTokens = S::kGroups * kHold<S>;
     __shared__ float sh[kNormWarps];
