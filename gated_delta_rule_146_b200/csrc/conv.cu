@@ -5,9 +5,13 @@
 // A thread owns N neighbouring channels (8 bytes of a row) and walks a run of tokens with the last
 // W inputs in registers, so that every input is read once (and W - 1 more at the start of each
 // run, which the cache serves).  Tokens arrive by asynchronous copies, two batches of four ahead,
-// in shared memory of the thread's own, which takes no registers and no barrier.  Channels go in pairs through packed fp32 arithmetic, and the activation costs one exponential
-// and one reciprocal: with an IEEE division the forward took 2.5 times as long as its bytes.  HBM
-// bounds all three kernels: 4 bytes per token and channel forward and 6 backward, in bf16.
+// in shared memory of the thread's own, which takes no registers and no barrier.  Channels go in
+// pairs through packed fp32 arithmetic, and the activation costs one exponential and one
+// reciprocal in place of an IEEE division.
+//
+// HBM bounds the forward (4 bytes per token and channel in bf16): 65537 x 4096 takes 183 us, 90 %
+// of the copy rate.  The backward (6 bytes) comes to 60 %: 8 x 4096 x 2048 takes 102 us, its 24
+// instructions an element waiting on one another in the 16 warps that its registers allow.
 //
 // The backward forms p again from x.  dx_t gathers dp of the W - 1 tokens behind it, so a run
 // reads that far ahead; the gradients of weights and bias are summed over the run in registers,

@@ -3,7 +3,9 @@
 // A group is one head's channels over a whole sequence, more than a block can hold, so each
 // direction is two passes over the tensors with the sums joined between them: sums of every
 // (tile of tokens, head), their join per (sequence, head), then the elements.  The second pass
-// reads x again: from L2 where the tensors fit there.
+// reads x again: from L2 where the tensors fit there.  16 segments of 2048 tokens x 12 x 64 in bf16
+// take 61 us backward (bytes read once: 23 us), its two passes at 64 to 67 % of the issue slots;
+// 8 x 4096 x 16 x 128, beyond L2, 175 us with a gate, at the rate of two passes' bytes (163 us).
 //
 // A tile may meet several sequences.  Tile i and sequence s have the piece number i + s: along
 // the token axis each step goes to the next tile or to the next sequence, so the numbers are

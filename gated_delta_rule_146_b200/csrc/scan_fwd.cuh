@@ -3,7 +3,9 @@
 //     h_t = alpha_t h_{t-1} + b_t,   alpha = exp(g),   b = v | beta v | (1 - alpha) v,   o = h
 //
 // Every element is read and written once (6 bytes per token and channel in bf16, 8 with beta),
-// for about twenty instructions a pair of channels: HBM bounds it.  The split is described in
+// for about twenty instructions a pair of channels: HBM bounds it.  8 x 4096 x 2048 in bf16 with
+// beta takes 86 us, 95 % of the copy rate.  Clusters come to 75 % (131072 x 1024, plain: 165 us),
+// bound by the instructions of a step on the 128 SMs they fill.  The split is described in
 // scan_impl.cuh.
 #pragma once
 
