@@ -100,15 +100,23 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _fits(*sizes):
+    """ctypes would keep the low 32 bits of a larger size."""
+    if max(sizes) > 0x7fffffff:
+        raise ValueError("every size must be below 2^31")
+
+
 def _rows(x, cu_seqlens):
     """(B, T, number of sequences) of a [B, T, ...] tensor."""
     if x.dim() < 3:
         raise ValueError("expected [B, T, channels...]")
     B, T = x.shape[:2]
+    _fits(B, T)
     if cu_seqlens is None:
         return B, T, B
     if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
         raise TypeError("cu_seqlens must be int32 [n_seqs + 1]")
+    _fits(cu_seqlens.numel())
     return B, T, cu_seqlens.numel() - 1
 
 
@@ -121,7 +129,9 @@ def _workspace(size, given, dev):
 
 
 def _count(shape):
-    return shape[0] if len(shape) == 1 else shape.numel()
+    n = shape[0] if len(shape) == 1 else shape.numel()
+    _fits(n)
+    return n
 
 
 # ---- gated linear recurrence ---------------------------------------------------------------------
@@ -202,6 +212,7 @@ def linear_scan_step(v, g, beta, h, *, tied=False, h_out=None, o=None, stream=No
     if v.dim() < 2:
         raise ValueError("expected [N, channels...]")
     N, chan = v.shape[0], v.shape[1:]
+    _fits(N)
     a = ScanArgs(N, 1, _count(chan), N, _code(v), _code(g), _write(v, g, beta, tied), 0, None)
     _expect("h", h, v.shape, torch.float32)
     _expect("h_out", h_out, v.shape, torch.float32)
@@ -231,6 +242,7 @@ def _conv_weights(weight, bias, D):
         raise ValueError(f"weight must be [channels, width] for {D} channels")
     _expect_channels("weight", weight, D * weight.shape[-1])
     _expect_channels("bias", bias, D)
+    _fits(weight.shape[-1])
     return weight.shape[-1]
 
 
@@ -302,6 +314,7 @@ def short_conv_step(x, weight, bias, state, *, activation="silu", state_out=None
     if x.dim() < 2:
         raise ValueError("expected [N, channels...]")
     N, chan = x.shape[0], x.shape[1:]
+    _fits(N)
     D = _count(chan)
     W = _conv_weights(weight, bias, D)
     a = ConvArgs(N, 1, D, N, W, _code(x), _activation(activation), 0, None)
@@ -327,6 +340,7 @@ def _norm_args(x, weight, bias, z, cu_seqlens, per, center, activation, eps, sta
     if per not in ("token", "sequence"):
         raise ValueError('per is "token" or "sequence"')
     H, d = x.shape[2:]
+    _fits(H, d)
     cu = cu_seqlens if per == "sequence" else None
     B, T, n = _rows(x, cu)
     shape = next((tuple(t.shape) for t in (weight, bias) if t is not None), (H, d))

@@ -214,3 +214,27 @@ def test_the_binding_checks_shapes_types_and_devices():
         with pytest.raises(err):
             call()
             raise AssertionError(f"call {i} went through")
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    """The C structs hold sizes in 32 bits: 2^32 + 5 tokens or channels must not become 5."""
+    n = (1 << 32) + 5
+    big = lambda *s, dtype=torch.float32: Fake(torch.zeros((), dtype=dtype).expand(*s))  # noqa: E731
+    row, many, wide = big(1, n, 1), big(n, 1, 1), big(1, 1, n)
+    bounds = big(n, dtype=torch.int32)
+    for call in (
+            lambda: gdr.linear_scan_fwd(row, row), lambda: gdr.linear_scan_fwd(many, many),
+            lambda: gdr.linear_scan_fwd(wide, wide),
+            lambda: gdr.linear_scan_fwd(big(1, 4, 8), big(1, 4, 8), cu_seqlens=bounds),
+            lambda: gdr.linear_scan_bwd(row, row, None, row, row),
+            lambda: gdr.linear_scan_step(big(n, 1), big(n, 1), None, big(n, 1)),
+            lambda: gdr.linear_scan_step(big(1, n), big(1, n), None, big(1, n)),
+            lambda: gdr.short_conv_fwd(row, big(1, 4)), lambda: gdr.short_conv_fwd(wide, big(n, 4)),
+            lambda: gdr.short_conv_fwd(big(1, 4, 1), big(1, n)),
+            lambda: gdr.short_conv_bwd(row, big(1, 4), None, row),
+            lambda: gdr.short_conv_step(big(n, 1), big(1, 4), None, big(n, 3, 1)),
+            lambda: gdr.group_norm_fwd(big(1, n, 1, 1)), lambda: gdr.group_norm_fwd(big(1, 1, n, 1)),
+            lambda: gdr.group_norm_fwd(big(1, 1, 1, n)),
+            lambda: gdr.group_norm_bwd(big(1, n, 1, 1), None, None, None, big(1, n, 1, 1))):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
