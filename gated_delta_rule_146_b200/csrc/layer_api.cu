@@ -27,6 +27,19 @@ bool any_null(std::initializer_list<const void*> ptrs) {
     return false;
 }
 
+// Whether an output is an input's array or another output's.  Kernels read ahead of what they
+// write, so that results would depend on their timing.
+bool overlap(std::initializer_list<const void*> outs, std::initializer_list<const void*> ins) {
+    for (auto o = outs.begin(); o != outs.end(); ++o) {
+        if (!*o) continue;
+        for (const void* i : ins)
+            if (i == *o) return true;
+        for (auto other = outs.begin(); other != o; ++other)
+            if (*other == *o) return true;
+    }
+    return false;
+}
+
 bool valid_dtype(gdr_dtype d) { return d == GDR_F32 || d == GDR_BF16; }
 
 // Token and channel counts of every operator: kernels hold token numbers (and one tile more) in
@@ -102,6 +115,8 @@ gdr_status gdr_scan_fwd(const gdr_scan_args* a, const void* v, const void* g, co
     if (off16({v, g, beta, h0, cu, o, h_final})) return GDR_ERR_ALIGNMENT;
     ScanPtrs p{};
     p.v = v; p.g = g; p.beta = beta; p.h0 = h0; p.cu = cu; p.o = o; p.h_final = h_final;
+    // (h_final may be h0)
+    if (overlap({o, h_final}, {v, g, beta}) || overlap({o}, {h0})) return GDR_ERR_INVALID_ARG;
     return launch_scan_fwd(*a, p, static_cast<cudaStream_t>(stream));
 }
 
@@ -119,6 +134,9 @@ gdr_status gdr_scan_bwd(const gdr_scan_args* a, const void* v, const void* g, co
     ScanPtrs p{};
     p.v = v; p.g = g; p.beta = beta; p.o_in = o; p.dO = dO; p.h0 = h0; p.cu = cu;
     p.dh_final = dh_final; p.dv = dv; p.dg = dg; p.dbeta = dbeta; p.dh0 = dh0;
+    // (dh0 may be dh_final)
+    if (overlap({dv, dg, dbeta, dh0}, {v, g, beta, o, dO, h0}) || overlap({dv, dg, dbeta}, {dh_final}))
+        return GDR_ERR_INVALID_ARG;
     return launch_scan_bwd(*a, p, static_cast<cudaStream_t>(stream));
 }
 
@@ -132,6 +150,7 @@ gdr_status gdr_scan_step(const gdr_scan_args* a, const void* v, const void* g, c
     if (off16({v, g, beta, h, h_out, o})) return GDR_ERR_ALIGNMENT;
     ScanPtrs p{};
     p.v = v; p.g = g; p.beta = beta; p.h0 = h; p.h_final = h_out; p.o = o;
+    if (overlap({o, h_out}, {v, g, beta}) || overlap({o}, {h})) return GDR_ERR_INVALID_ARG;
     return launch_scan_step(*a, p, static_cast<cudaStream_t>(stream));
 }
 
@@ -145,6 +164,7 @@ gdr_status gdr_conv_fwd(const gdr_conv_args* a, const void* x, const float* w, c
     if (off16({x, state, cu, y, state_out}) || off4({w, bias})) return GDR_ERR_ALIGNMENT;
     ConvPtrs p{};
     p.x = x; p.w = w; p.bias = bias; p.state = state; p.cu = cu; p.y = y; p.state_out = state_out;
+    if (overlap({y, state_out}, {x, w, bias, state})) return GDR_ERR_INVALID_ARG;
     return launch_conv_fwd(*a, p, static_cast<cudaStream_t>(stream));
 }
 
@@ -165,6 +185,7 @@ gdr_status gdr_conv_bwd(const gdr_conv_args* a, const void* x, const float* w, c
     ConvPtrs p{};
     p.x = x; p.w = w; p.bias = bias; p.dy = dy; p.state = state; p.cu = cu; p.dx = dx; p.dw = dw;
     p.dbias = dbias; p.dstate = dstate; p.ws = static_cast<float*>(workspace);
+    if (overlap({dx, dw, dbias, dstate, workspace}, {x, w, bias, dy, state})) return GDR_ERR_INVALID_ARG;
     return launch_conv_bwd(*a, p, static_cast<cudaStream_t>(stream));
 }
 
@@ -177,6 +198,7 @@ gdr_status gdr_conv_step(const gdr_conv_args* a, const void* x, const float* w, 
     if (off16({x, state, state_out, y}) || off4({w, bias})) return GDR_ERR_ALIGNMENT;
     ConvPtrs p{};
     p.x = x; p.w = w; p.bias = bias; p.state = state; p.y = y; p.state_out = state_out;
+    if (overlap({y, state_out}, {x, w, bias}) || overlap({y}, {state})) return GDR_ERR_INVALID_ARG;
     return launch_conv_step(*a, p, static_cast<cudaStream_t>(stream));
 }
 
@@ -196,6 +218,7 @@ gdr_status gdr_norm_fwd(const gdr_norm_args* a, const void* x, const float* w, c
     NormPtrs p{};
     p.x = x; p.w = w; p.b = bias; p.z = z; p.cu = cu; p.y = y; p.stats = stats;
     p.ws = static_cast<float*>(workspace);
+    if (overlap({y, stats, workspace}, {x, w, bias, z})) return GDR_ERR_INVALID_ARG;
     return launch_norm_fwd(*a, p, static_cast<cudaStream_t>(stream));
 }
 
@@ -218,6 +241,7 @@ gdr_status gdr_norm_bwd(const gdr_norm_args* a, const void* x, const float* w, c
     NormPtrs p{};
     p.x = x; p.w = w; p.b = bias; p.z = z; p.dy = dy; p.cu = cu; p.stats_in = stats; p.dx = dx;
     p.dw = dw; p.db = dbias; p.dz = dz; p.ws = static_cast<float*>(workspace);
+    if (overlap({dx, dw, dbias, dz, workspace}, {x, w, bias, z, dy, stats})) return GDR_ERR_INVALID_ARG;
     return launch_norm_bwd(*a, p, static_cast<cudaStream_t>(stream));
 }
 

@@ -238,3 +238,43 @@ def test_sizes_beyond_32_bits_are_refused():
             lambda: gdr.group_norm_bwd(big(1, n, 1, 1), None, None, None, big(1, n, 1, 1))):
         with pytest.raises(ValueError, match="2\\^31"):
             call()
+
+
+def test_an_output_in_an_inputs_place_is_refused(lib):
+    """Every pointer of its own is fine for the checks before, so INV is the overlap's."""
+    q = [P + 0x1000 * i for i in range(16)]
+
+    def each(fn, a, ptrs, pairs, tail=(None,)):
+        for out, other in pairs:
+            p = list(ptrs)
+            p[out] = p[other]
+            assert fn(a, *p, *tail) == INV, (fn.__name__, out, other)
+
+    gate = args(ScanArgs, SCAN, dict(write=1))
+    # v g beta h0 cu o h_final
+    each(lib.gdr_scan_fwd, gate, [*q[:4], None, q[5], q[6]], [(5, 0), (5, 1), (5, 2), (5, 3), (6, 5), (6, 0)])
+    # v g beta o dO h0 cu dh_final dv dg dbeta dh0
+    each(lib.gdr_scan_bwd, gate, [*q[:6], None, *q[7:12]],
+         [(8, 0), (8, 4), (9, 1), (10, 2), (9, 8), (10, 9), (8, 3), (11, 5), (8, 7)])
+    # v g beta h h_out o
+    each(lib.gdr_scan_step, args(ScanArgs, SCAN, dict(write=1, T=1)), q[:6],
+         [(5, 0), (5, 3), (4, 1), (5, 4)])
+    conv = args(ConvArgs, CONV, {})
+    # x w bias state cu y state_out
+    each(lib.gdr_conv_fwd, conv, [*q[:4], None, q[5], q[6]], [(5, 0), (5, 3), (6, 0), (6, 5), (5, 1)])
+    need = lib.gdr_conv_bwd_workspace_size(conv)
+    # x w bias dy state cu dx dw dbias dstate workspace
+    each(lib.gdr_conv_bwd, conv, [*q[:5], None, *q[6:11]],
+         [(6, 0), (6, 3), (9, 4), (7, 1), (8, 2), (8, 7), (10, 6), (10, 0)], (need, None))
+    each(lib.gdr_conv_step, args(ConvArgs, CONV, dict(T=1)), q[:6], [(5, 0), (5, 3), (4, 0), (5, 4)])
+    for kw in ({}, dict(per_sequence=1)):
+        norm = args(NormArgs, NORM, kw)
+        seq = bool(kw)
+        need = lib.gdr_norm_fwd_workspace_size(norm)
+        # x w bias z cu y stats workspace
+        each(lib.gdr_norm_fwd, norm, [*q[:4], None, q[5], q[6] if seq else None, q[7]],
+             [(5, 0), (5, 3), (5, 1)] + ([(6, 0), (7, 5)] if seq else []), (need, None))
+        need = lib.gdr_norm_bwd_workspace_size(norm)
+        # x w bias z dy cu stats dx dw dbias dz workspace
+        each(lib.gdr_norm_bwd, norm, [*q[:5], None, *q[6:12]],
+             [(7, 0), (7, 4), (10, 3), (8, 1), (9, 8), (10, 7), (11, 7)], (need, None))
