@@ -171,3 +171,56 @@ def test_offsets_beyond_31_bits():
                                _tail(o, n).view(1, n, 32, 128), one, per=per, stats=ss)[0]
         assert close(_tail(a, n), b)
         del big, a
+
+
+def run_layer(t, c, H, d, **kw):
+    """Forward and backward of all operators, the norm per token and per sequence."""
+    v, st = gdr.short_conv_fwd(t["x"], t["w"], t["b"], t["st"], c, **kw)
+    h, hf = gdr.linear_scan_fwd(v, t["g"], None, t["h0"], c, tied=True, **kw)
+    hh = h.view(1, -1, H, d)
+    y = gdr.group_norm_fwd(hh, t["nw"], None, t["z"], center=False, **kw)
+    ys, stats = gdr.group_norm_fwd(hh, t["nw"], None, t["z"], c, per="sequence", output_stats=True,
+                                   **kw)
+    dh, dnw, _, dz = gdr.group_norm_bwd(hh, t["nw"], None, t["z"], t["dy"], center=False, **kw)
+    sh, snw, _, sz = gdr.group_norm_bwd(hh, t["nw"], None, t["z"], t["dy"], c, per="sequence",
+                                        stats=stats, **kw)
+    dv, dg, _, dh0 = gdr.linear_scan_bwd(v, t["g"], None, h, dh.view_as(v), t["h0"], c, tied=True,
+                                         **kw)
+    dx, dw, db, dst = gdr.short_conv_bwd(t["x"], t["w"], t["b"], dv, t["st"], c, **kw)
+    return [st, h, hf, y, ys, stats, dh, dnw, dz, sh, snw, sz, dv, dg, dh0, dx, dw, db, dst]
+
+
+def test_calls_that_overlap_on_two_streams():
+    """Two layers' calls at once, eagerly and as two graphs' replays, give the bits of calls one
+    after the other.  Clusters' walks (few slabs) and single blocks' (many) meet."""
+    sizes = [(4, 64, [900, 0, 1, 300]), (64, 128, [500, 77])]
+    cases, want = [], []
+    for i, (H, d, lengths) in enumerate(sizes):
+        cu = np.concatenate([[0], np.cumsum(lengths)]).tolist()
+        t = {k: v.cuda() for k, v in layer_inputs(cu[-1], H, d, len(lengths), torch.bfloat16,
+                                                  20 + i).items()}
+        c = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        cases.append((t, c, H, d))
+        want.append(run_layer(*cases[-1]))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[], []]
+    for _ in range(6):
+        for i, case in enumerate(cases):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(run_layer(*case))
+    torch.cuda.synchronize()
+    graphs, out = [], []
+    for case in cases:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out.append(run_layer(*case))
+        graphs.append(g)
+    for _ in range(6):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for i, w in enumerate(want):
+        for r in got[i] + [out[i]]:
+            assert all(torch.equal(a, b) for a, b in zip(r, w)), i
