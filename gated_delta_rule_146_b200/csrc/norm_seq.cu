@@ -4,12 +4,15 @@
 // direction is two passes over the tensors with the sums joined between them: sums of every
 // (tile of tokens, head), their join per (sequence, head), then the elements.  The second pass
 // reads x again: from L2 where the tensors fit there.  16 segments of 2048 tokens x 12 x 64 in bf16
-// take 61 us backward (bytes read once: 23 us), its two passes at 64 to 67 % of the issue slots;
-// 8 x 4096 x 16 x 128, beyond L2, 175 us with a gate, at the rate of two passes' bytes (163 us).
+// take 59 us backward (bytes read once: 23 us), its two passes at 64 to 67 % of the issue slots;
+// 8 x 4096 x 16 x 128, beyond L2, 166 us with a gate, at the rate of two passes' bytes (163 us).
 //
 // A tile may meet several sequences.  Tile i and sequence s have the piece number i + s: along
 // the token axis each step goes to the next tile or to the next sequence, so the numbers are
-// distinct and a sequence's pieces lie side by side, whatever the lengths.
+// distinct and a sequence's pieces lie side by side, whatever the lengths.  A block takes its
+// tile's sequences one after the other, so the first pass slows down where they are shorter than
+// its tile: 32768 tokens x 16 x 64 take 57 us forward and 78 backward in sequences of 1024, 250 and
+// 320 in sequences of 8, 1550 and 1970 in sequences of one.
 //
 // Variances: each piece's sum of squares is taken about the piece's own mean, from registers,
 // and pieces are joined pairwise with the difference of their means, so that no large squares
@@ -28,6 +31,25 @@ __device__ __forceinline__ float block_sum(float x, float* sh) {
     float v = 0.f;
 #pragma unroll
     for (int i = 0; i < kNormWarps; ++i) v += sh[i];
+    return v;
+}
+
+// Two sums over a block behind one barrier, in two buffers by turns: behind a call's barrier all
+// threads have read the call before it, so the next one may overwrite that.  (Against two sums of
+// block_sum: 166 instead of 174 us on the shape above.  The statistics pass gains nothing by it.)
+__device__ __forceinline__ float2 block_sums(float x, float y, float2 (*sh)[kNormWarps], int& turn) {
+    x = warp_sum(x);
+    y = warp_sum(y);
+    float2* const mine = sh[turn];
+    turn ^= 1;
+    if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5] = make_float2(x, y);
+    __syncthreads();
+    float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kNormWarps; ++i) {
+        v.x += mine[i].x;
+        v.y += mine[i].y;
+    }
     return v;
 }
 
@@ -174,7 +196,8 @@ __global__ void __launch_bounds__(kNormThreads, S::kResident)
 norm_seq_bwd_sums(const NormParams<typename S::IO> p, int tokens, float2* __restrict__ pieces) {
     extern __shared__ __align__(16) char smem[];
     constexpr int kCh = S::LPG * S::VEC;
-    __shared__ float sh[kNormWarps];
+    __shared__ float2 sh[2][kNormWarps];
+    int turn = 0;
     const int g = threadIdx.x / S::LPG, l = threadIdx.x % S::LPG;
     const int tile = blockIdx.x / p.H, h = blockIdx.x % p.H;
     if (blockIdx.x == 0) check_cu(p.q, p.status, threadIdx.x, kNormThreads);
@@ -210,9 +233,8 @@ norm_seq_bwd_sums(const NormParams<typename S::IO> p, int tokens, float2* __rest
             s2 += o.s2;
             if (gate) store_row<S>(p.dz + at, l, p.d, o.dz);
         }
-        s1 = block_sum(s1, sh);
-        s2 = block_sum(s2, sh);
-        if (threadIdx.x == 0) pieces[((size_t)tile + s) * p.H + h] = make_float2(s1, s2);
+        const float2 sums = block_sums(s1, s2, sh, turn);
+        if (threadIdx.x == 0) pieces[((size_t)tile + s) * p.H + h] = sums;
     }
     copy_wait<0>();
     let_follow();
