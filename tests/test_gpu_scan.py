@@ -1,4 +1,6 @@
 """Gated linear recurrence on the GPU against its 64-bit definition."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -301,3 +303,92 @@ def test_streams_and_graphs():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, w))
         assert all(a is b is None or torch.equal(a, b) for a, b in zip(grads, wg))
+
+
+# ---- single blocks -------------------------------------------------------------------------------
+# At most 148 clusters of one block are resident, so more slabs of 64 channels (times rows) than
+# that are always laid out as single blocks, whose walk is another one than the clusters'.
+
+def single(write, io="bf16", gate=None, D=4864, packed=False, seed=0, T=330):
+    """Inputs for single blocks, over six steps in bf16 and eleven in fp32."""
+    if packed:
+        D += 4864
+    units = -(-D // 64) * (1 if packed else 2)
+    assert units > 148
+    lengths = [T // 5, 0, 1, T - T // 5 - 5, 3, 1, 0] if packed else [T] * 2
+    return make(lengths, D, io, gate, write, seed=seed, rows=not packed)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("write", ["plain", "gate", "tied"])
+@pytest.mark.parametrize("io,gate", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32"),
+                                     ("f32", "bf16")])
+def test_single_blocks(io, gate, write, packed):
+    compare(single(write, io, gate, packed=packed, seed=20), reverse=packed)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("D", [4866, 4865])
+@pytest.mark.parametrize("io,write", [("bf16", "gate"), ("bf16", "tied"), ("f32", "plain")])
+def test_single_blocks_of_odd_widths(io, write, D, packed):
+    """Rows that are copied two channels and one channel at a time."""
+    compare(single(write, io, D=D, packed=packed, seed=D), reverse=not packed)
+
+
+@pytest.mark.parametrize("T", [64, 65, 127, 128, 129, 192, 257])
+def test_single_blocks_of_other_lengths(T):
+    compare(single("tied", T=T, seed=T), reverse=T % 2 == 0)
+    compare(single("plain", T=T, packed=True, seed=T), reverse=T % 2 == 1)
+
+
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("packed", [False, True])
+def test_single_blocks_keep_sequences_apart(packed, reverse):
+    """Infinities and NaN of one sequence (the longest) leave the others' results as they are."""
+    x = single("gate", packed=packed, seed=21)
+    s = 3 if packed else 0
+    d = dev(x)
+    o, hf = forward(d, reverse)
+    grads = backward(d, o, reverse)
+    bad = {k: t.clone() if torch.is_tensor(t) else t for k, t in d.items()}
+    b, e = x["cu"][s], x["cu"][s + 1]
+    for k, v in (("v", float("nan")), ("dO", float("inf"))):
+        flat(bad[k])[b:e] = v
+    bad["h0"][s] = float("inf")
+    bad["dhf"][s] = float("nan")
+    o2, hf2 = forward(bad, reverse)
+    g2 = backward(bad, o2, reverse)
+    keep = torch.ones(x["cu"][-1], dtype=torch.bool, device="cuda")
+    keep[b:e] = False
+    rest = [i for i in range(len(x["cu"]) - 1) if i != s]
+    assert not torch.isfinite(flat(o2)[b:e]).any()
+    for a, c in zip((o, *grads[:3]), (o2, *g2[:3])):
+        assert torch.equal(flat(a)[keep], flat(c)[keep])
+    assert torch.equal(hf2[rest], hf[rest]) and torch.equal(g2[3][rest], grads[3][rest])
+
+
+def raw_backward(d, o, dv, dg, dh0, dhf, status=None, n=None):
+    """gdr_scan_bwd of a plain write on outputs of the caller's."""
+    B, T, D = d["v"].shape
+    a = _abi.ScanArgs(B, T, D, n or len(d["cu"]) - 1, _abi.F32 if d["v"].dtype == torch.float32 else
+                      _abi.BF16, _abi.F32 if d["g"].dtype == torch.float32 else _abi.BF16,
+                      _abi.WRITE_PLAIN, 0, None if status is None else status.data_ptr())
+    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    _abi.check(_abi.lib().gdr_scan_bwd(
+        ctypes.byref(a), p(d["v"]), p(d["g"]), None, p(o), p(d["dO"]), p(d["h0"]), p(d["cu_t"]),
+        p(dhf), p(dv), p(dg), None, p(dh0), torch.cuda.current_stream().cuda_stream))
+
+
+def test_backward_reports_bad_cu_seqlens_and_stays_inside():
+    D, T = 64, 100
+    for cu in ([0, 60, 40, 100], [0, 50, 99], [1, 50, 100], [0, -7, 100], [0, 200, 100]):
+        n = len(cu) - 1
+        d = dev(make([T], D, seed=13))
+        d["cu_t"] = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        d["h0"], dhf = torch.zeros(n, D, device="cuda"), torch.zeros(n, D, device="cuda")
+        dv, dg = (torch.full((T + 8, D), 7.0, device="cuda") for _ in range(2))
+        dh0 = torch.full((n + 4, D), 7.0, device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        raw_backward(d, d["v"], dv, dg, dh0, dhf, status, n)
+        assert status.item() == _abi.GDR_ERR_DEVICE_CHECK, cu
+        assert (dv[T:] == 7).all() and (dg[T:] == 7).all() and (dh0[n:] == 7).all()
