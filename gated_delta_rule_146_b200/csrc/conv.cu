@@ -437,16 +437,13 @@ conv_step_kernel(const IO* __restrict__ x, const float* __restrict__ w,
     if (left <= 0) return;
     const size_t n = blockIdx.y;
     const IO* st = state + n * (W - 1) * D + c;
-    // the state may be updated in place: all of it is read before any of it is written, and not
-    // through the read-only path
+    // the state may be updated in place: all of it is read before any of it is written
     F2 win[W][P], wr[W][P], b[P];
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) {
         Vec<IO, N> v;
         if constexpr (kWhole) {
-            using R = typename RawOf<sizeof(IO) * N>::T;
-            const R r = *reinterpret_cast<const R*>(st + (size_t)k * D);
-            memcpy(&v, &r, sizeof(R));
+            v = load_in_place<IO, N>(st + (size_t)k * D);
         } else {
 #pragma unroll
             for (int j = 0; j < N; ++j) v.x[j] = j < left ? st[(size_t)k * D + j] : from_f<IO>(0.f);

@@ -87,6 +87,17 @@ __device__ __forceinline__ Vec<E, N> load_vec(const E* p) {
     return v;
 }
 
+// The same of an array that the kernel may also write (a state updated in place): an ordinary
+// load, which keeps its place among the barriers and stores around it.
+template <typename E, int N>
+__device__ __forceinline__ Vec<E, N> load_in_place(const E* p) {
+    using R = typename RawOf<sizeof(E) * N>::T;
+    Vec<E, N> v;
+    const R r = *reinterpret_cast<const R*>(p);
+    memcpy(&v, &r, sizeof(R));
+    return v;
+}
+
 template <typename E, int N>
 __device__ __forceinline__ void store_vec(E* p, const float (&f)[N]) {
     using R = typename RawOf<sizeof(E) * N>::T;

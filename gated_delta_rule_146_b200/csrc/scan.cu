@@ -14,7 +14,7 @@ scan_step_kernel(const IO* __restrict__ v, const GT* __restrict__ g, const GT* _
     const long long at = ((long long)blockIdx.x * 256 + threadIdx.x) * VEC;
     if (at >= n) return;
     float fh[VEC], fv[VEC], fg[VEC], fb[VEC] = {};
-    load_f<float, VEC>(h + at, fh);
+    const Vec<float, VEC> state = load_in_place<float, VEC>(h + at);  // h_out may be h
     load_f<IO, VEC>(v + at, fv);
     load_f<GT, VEC>(g + at, fg);
     if constexpr (kWrite == GDR_WRITE_GATE) load_f<GT, VEC>(beta + at, fb);
@@ -24,7 +24,7 @@ scan_step_kernel(const IO* __restrict__ v, const GT* __restrict__ g, const GT* _
         float b = fv[j];
         if constexpr (kWrite == GDR_WRITE_GATE) b *= fb[j];
         if constexpr (kWrite == GDR_WRITE_TIED) b *= one_minus(g2, a).lo();
-        fh[j] = fmaf(a.lo(), fh[j], b);
+        fh[j] = fmaf(a.lo(), state.x[j], b);
     }
     store_vec<float, VEC>(h_out + at, fh);
     store_vec<IO, VEC>(o + at, fh);

@@ -360,12 +360,16 @@ __device__ __forceinline__ void store_pair(E* p, F2 f, int left) {
     }
 }
 
-// A lane's two channels of a state row.
+// A lane's two channels of a state row, which may be the row that the kernel writes.
 template <Copy kCopy>
 __device__ __forceinline__ F2 load_state(const float* p, int left) {
     float f[2] = {0.f, 0.f};
     if constexpr (kCopy != kCopyOne) {
-        if (left > 0) load_f<float, 2>(p, f);
+        if (left > 0) {
+            const Vec<float, 2> v = load_in_place<float, 2>(p);
+            f[0] = v.x[0];
+            f[1] = v.x[1];
+        }
     } else {
         if (left > 0) f[0] = p[0];
         if (left > 1) f[1] = p[1];

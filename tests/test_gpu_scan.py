@@ -392,3 +392,27 @@ def test_backward_reports_bad_cu_seqlens_and_stays_inside():
         raw_backward(d, d["v"], dv, dg, dh0, dhf, status, n)
         assert status.item() == _abi.GDR_ERR_DEVICE_CHECK, cu
         assert (dv[T:] == 7).all() and (dg[T:] == 7).all() and (dh0[n:] == 7).all()
+
+
+@pytest.mark.parametrize("case", ["clusters", "clusters packed", "blocks", "blocks packed",
+                                  "empty", "one by one"])
+def test_states_in_place_in_every_layout(case):
+    """h_final in h0's place and dh0 in dh_final's give the bits of arrays of their own."""
+    packed = "packed" in case
+    x = (single("plain", packed=packed, seed=22) if "blocks" in case else
+         make([40, 0, 300, 1, 0], 65, seed=23) if case == "one by one" else
+         make([0, 0], 64, seed=24) if case == "empty" else
+         make([500, 0, 1, 700] if packed else [600] * 3, 200, "bf16", seed=25, rows=not packed))
+    d = dev(x)
+    o, hf = forward(d)
+    for _ in range(3):
+        d2 = dict(d, h0=d["h0"].clone())
+        o2, hf2 = forward(d2, h_final=d2["h0"])
+        assert hf2.data_ptr() == d2["h0"].data_ptr()
+        assert torch.equal(o2, o) and torch.equal(hf2, hf)
+    dv, dg, _, dh0 = backward(d, o)
+    for _ in range(3):
+        state = d["dhf"].clone()
+        dv2, dg2 = torch.empty_like(dv), torch.empty_like(dg)
+        raw_backward(d, o, dv2, dg2, state, state)
+        assert torch.equal(dv2, dv) and torch.equal(dg2, dg) and torch.equal(state, dh0)
