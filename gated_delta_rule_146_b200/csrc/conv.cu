@@ -408,8 +408,7 @@ conv_bwd_kernel(const ConvParams<IO> p) {
 // dw, dbias from the partial sums: 32 channels a block, its 8 warps over the rows.
 template <int W>
 __global__ void __launch_bounds__(256)
-conv_reduce_kernel(const float* __restrict__ part, int rows, int D, float* __restrict__ dw,
-                   float* __restrict__ dbias) {
+conv_reduce_kernel(const float* part, int rows, int D, float* dw, float* dbias) {
     __shared__ float sh[8][32];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane, k = blockIdx.y;

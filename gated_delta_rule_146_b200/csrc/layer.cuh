@@ -281,7 +281,9 @@ __device__ __forceinline__ void store_raw(E* p, const Vec<E, N>& v) {
 
 // ---- kernels that follow one another --------------------------------------------------------------
 // A follower is launched while its predecessor still runs, and waits for its results here, before
-// it reads or writes anything.  The predecessor lets it come when it calls let_follow, or ends.
+// it reads any of them or writes anything.  The predecessor lets it come when it calls let_follow,
+// or ends.  What a predecessor writes while a follower runs is not read-only to the follower, which
+// takes it through ordinary pointers (not __restrict__, no __ldg): their loads stay behind the wait.
 __device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_follow() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -180,8 +180,7 @@ norm_token_bwd(const NormParams<typename S::IO> p, int used, long long slots) {
 
 // 32 channels of one head a block (all heads for a shared weight); its 32 warps over the rows.
 __global__ void __launch_bounds__(1024)
-norm_reduce_kernel(const float* __restrict__ part, int rows, int H, int d, float* __restrict__ dw,
-                   float* __restrict__ db) {
+norm_reduce_kernel(const float* part, int rows, int H, int d, float* dw, float* db) {
     __shared__ float sh[32][33];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane, h = blockIdx.y, which = blockIdx.z;

@@ -108,8 +108,7 @@ norm_seq_stats(const NormParams<typename S::IO> p) {
 
 // One warp per (sequence, head): joins the pieces' (mean, sum of squares).
 __global__ void __launch_bounds__(128)
-norm_seq_join_stats(Seqs q, int H, int d, int tokens, float eps, const float2* __restrict__ part,
-                    float2* __restrict__ stats) {
+norm_seq_join_stats(Seqs q, int H, int d, int tokens, float eps, const float2* part, float2* stats) {
     const long long unit = (long long)blockIdx.x * 4 + threadIdx.x / 32;
     const int lane = threadIdx.x & 31;
     wait_before();
@@ -193,7 +192,7 @@ norm_seq_apply(const NormParams<typename S::IO> p, int tokens) {
 // and q n.
 template <typename S>
 __global__ void __launch_bounds__(kNormThreads, S::kResident)
-norm_seq_bwd_sums(const NormParams<typename S::IO> p, int tokens, float2* __restrict__ pieces) {
+norm_seq_bwd_sums(const NormParams<typename S::IO> p, int tokens, float2* pieces) {
     extern __shared__ __align__(16) char smem[];
     constexpr int kCh = S::LPG * S::VEC;
     __shared__ float2 sh[2][kNormWarps];
@@ -267,8 +266,8 @@ norm_seq_bwd_sums(const NormParams<typename S::IO> p, int tokens, float2* __rest
 
 // One warp per (sequence, head): means of q and q n over the group.
 __global__ void __launch_bounds__(128)
-norm_seq_join_sums(Seqs q, int H, int d, int tokens, int center, const float2* __restrict__ pieces,
-                   float2* __restrict__ means) {
+norm_seq_join_sums(Seqs q, int H, int d, int tokens, int center, const float2* pieces,
+                   float2* means) {
     const long long unit = (long long)blockIdx.x * 4 + threadIdx.x / 32;
     const int lane = threadIdx.x & 31;
     wait_before();
