@@ -95,6 +95,18 @@ gdr_status check_norm(const gdr_norm_args* a) {
     return norm_supported(*a) ? GDR_OK : GDR_ERR_UNSUPPORTED;
 }
 
+// A call of no tokens launches none of the kernels that check the bounds on their way.
+__global__ void __launch_bounds__(256) check_cu_kernel(Seqs q, int* status) {
+    check_cu(q, status, threadIdx.x, 256);
+}
+
+template <typename A>
+gdr_status check_empty(const A* a, const int32_t* cu, cudaStream_t st) {
+    if (!cu || !a->status) return GDR_OK;
+    check_cu_kernel<<<1, 256, 0, st>>>(Seqs{cu, a->n_seqs, 0, 0}, a->status);
+    return cudaGetLastError() == cudaSuccess ? GDR_OK : GDR_ERR_CUDA;
+}
+
 gdr_status check_workspace(const void* ws, size_t have, size_t need) {
     if (need == 0) return GDR_OK;
     if (!ws || have < need) return GDR_ERR_WORKSPACE;
@@ -117,6 +129,7 @@ gdr_status gdr_scan_fwd(const gdr_scan_args* a, const void* v, const void* g, co
     p.v = v; p.g = g; p.beta = beta; p.h0 = h0; p.cu = cu; p.o = o; p.h_final = h_final;
     // (h_final may be h0)
     if (overlap({o, h_final}, {v, g, beta}) || overlap({o}, {h0})) return GDR_ERR_INVALID_ARG;
+    if (!tokens && (st = check_empty(a, cu, static_cast<cudaStream_t>(stream))) != GDR_OK) return st;
     return launch_scan_fwd(*a, p, static_cast<cudaStream_t>(stream));
 }
 
@@ -137,6 +150,7 @@ gdr_status gdr_scan_bwd(const gdr_scan_args* a, const void* v, const void* g, co
     // (dh0 may be dh_final)
     if (overlap({dv, dg, dbeta, dh0}, {v, g, beta, o, dO, h0}) || overlap({dv, dg, dbeta}, {dh_final}))
         return GDR_ERR_INVALID_ARG;
+    if (!tokens && (st = check_empty(a, cu, static_cast<cudaStream_t>(stream))) != GDR_OK) return st;
     return launch_scan_bwd(*a, p, static_cast<cudaStream_t>(stream));
 }
 
@@ -211,7 +225,8 @@ gdr_status gdr_norm_fwd(const gdr_norm_args* a, const void* x, const float* w, c
                         size_t workspace_bytes, void* stream) {
     gdr_status st = check_norm(a);
     if (st != GDR_OK || (st = check_layout(a, cu)) != GDR_OK) return st;
-    if ((long long)a->B * a->T > 0 && any_null({x, y})) return GDR_ERR_INVALID_ARG;
+    const bool tokens = (long long)a->B * a->T > 0;
+    if (tokens && any_null({x, y})) return GDR_ERR_INVALID_ARG;
     if (stats && !a->per_sequence) return GDR_ERR_INVALID_ARG;
     if (off16({x, z, cu, y, stats}) || off4({w, bias})) return GDR_ERR_ALIGNMENT;
     if ((st = check_workspace(workspace, workspace_bytes, norm_fwd_workspace(*a))) != GDR_OK) return st;
@@ -219,6 +234,9 @@ gdr_status gdr_norm_fwd(const gdr_norm_args* a, const void* x, const float* w, c
     p.x = x; p.w = w; p.b = bias; p.z = z; p.cu = cu; p.y = y; p.stats = stats;
     p.ws = static_cast<float*>(workspace);
     if (overlap({y, stats, workspace}, {x, w, bias, z})) return GDR_ERR_INVALID_ARG;
+    if (!tokens && a->per_sequence &&
+        (st = check_empty(a, cu, static_cast<cudaStream_t>(stream))) != GDR_OK)
+        return st;
     return launch_norm_fwd(*a, p, static_cast<cudaStream_t>(stream));
 }
 
@@ -242,6 +260,9 @@ gdr_status gdr_norm_bwd(const gdr_norm_args* a, const void* x, const float* w, c
     p.x = x; p.w = w; p.b = bias; p.z = z; p.dy = dy; p.cu = cu; p.stats_in = stats; p.dx = dx;
     p.dw = dw; p.db = dbias; p.dz = dz; p.ws = static_cast<float*>(workspace);
     if (overlap({dx, dw, dbias, dz, workspace}, {x, w, bias, z, dy, stats})) return GDR_ERR_INVALID_ARG;
+    if (!tokens && a->per_sequence &&
+        (st = check_empty(a, cu, static_cast<cudaStream_t>(stream))) != GDR_OK)
+        return st;
     return launch_norm_bwd(*a, p, static_cast<cudaStream_t>(stream));
 }
 

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import gated_delta_rule_146_b200 as gdr
+from gated_delta_rule_146_b200 import _abi
 from oracle import layer as ol
 
 pytestmark = pytest.mark.gpu
@@ -224,3 +225,52 @@ def test_calls_that_overlap_on_two_streams():
     for i, w in enumerate(want):
         for r in got[i] + [out[i]]:
             assert all(torch.equal(a, b) for a, b in zip(r, w)), i
+
+
+def test_bad_bounds_of_no_tokens_are_reported():
+    """A row of no tokens has bounds to check too: [0, 5] does not end at 0, [3, 0] neither
+    starts there nor rises.  The results are those of empty sequences all the same."""
+    e = torch.empty(1, 0, 4, 16, device="cuda")
+    h0 = torch.randn(1, 4, 16, device="cuda")
+    w = torch.randn(4, 16, 4, device="cuda")
+    past = torch.randn(1, 3, 4, 16, device="cuda")
+    stats = torch.ones(1, 4, 2, device="cuda")
+    calls = dict(
+        scan_fwd=lambda **k: gdr.linear_scan_fwd(e, e, None, h0, **k)[1],
+        scan_bwd=lambda **k: gdr.linear_scan_bwd(e, e, None, e, e, None, dh_final=h0, **k)[3],
+        conv_fwd=lambda **k: gdr.short_conv_fwd(e, w, None, past, **k)[1],
+        conv_bwd=lambda **k: gdr.short_conv_bwd(e, w, None, e, past, **k)[1],
+        norm_fwd=lambda **k: gdr.group_norm_fwd(e, per="sequence", eps=0.25, output_stats=True, **k)[1],
+        norm_bwd=lambda **k: gdr.group_norm_bwd(e, w[..., 0].contiguous(), None, None, e, stats=stats,
+                                                per="sequence", **k)[1])
+    want = dict(scan_fwd=h0, scan_bwd=h0, conv_fwd=past, conv_bwd=torch.zeros_like(w),
+                norm_fwd=torch.tensor([0.0, 2.0], device="cuda").expand(1, 4, 2),
+                norm_bwd=torch.zeros(4, 16, device="cuda"))
+    for cu, st in (([0, 0], _abi.GDR_OK), ([0, 5], _abi.GDR_ERR_DEVICE_CHECK),
+                   ([3, 0], _abi.GDR_ERR_DEVICE_CHECK), ([-1, 0], _abi.GDR_ERR_DEVICE_CHECK)):
+        c = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        for name, call in calls.items():
+            status = torch.zeros(1, dtype=torch.int32, device="cuda")
+            got = call(cu_seqlens=c, status=status)
+            assert status.item() == st, (name, cu)
+            assert torch.equal(got, want[name]), (name, cu)
+            assert torch.equal(call(cu_seqlens=c), want[name]), (name, cu)
+
+
+def test_calls_of_no_tokens_in_a_graph():
+    """Captured as a graph's first node, and behind one that is no kernel."""
+    e = torch.empty(2, 0, 3, 16, device="cuda")
+    w = torch.ones(3, 16, device="cuda")
+    for first in (False, True):
+        g = torch.cuda.CUDAGraph()
+        other = torch.ones(8, device="cuda")
+        with torch.cuda.graph(g):
+            if not first:
+                other.zero_()
+            _, st = gdr.group_norm_fwd(e, w, per="sequence", output_stats=True, eps=0.25)
+            other.zero_()
+            _, dw, _, _ = gdr.group_norm_bwd(e, w, None, None, e, per="sequence", stats=st)
+        dw.fill_(1.0)
+        g.replay()
+        assert torch.equal(st, torch.tensor([0.0, 2.0], device="cuda").expand(2, 3, 2))
+        assert not dw.any() and not other.any()
