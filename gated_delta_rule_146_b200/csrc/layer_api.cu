@@ -27,18 +27,31 @@ bool any_null(std::initializer_list<const void*> ptrs) {
     return false;
 }
 
-// Whether an output is an input's array or another output's.  Kernels read ahead of what they
-// write, so that results would depend on their timing.
-bool overlap(std::initializer_list<const void*> outs, std::initializer_list<const void*> ins) {
+// An array of a call, for the comparison of places; an absent one has no bytes.
+struct Place {
+    uintptr_t at;
+    unsigned long long bytes;
+    Place(const void* p, unsigned long long n)
+        : at(reinterpret_cast<uintptr_t>(p)), bytes(p ? n : 0) {}
+    bool meets(const Place& o) const {
+        return bytes && o.bytes && at < o.at + o.bytes && o.at < at + bytes;
+    }
+};
+
+// Whether an output shares bytes with an input or with another output.  Kernels read ahead of what
+// they write, so that results would depend on their timing.
+bool overlap(std::initializer_list<Place> outs, std::initializer_list<Place> ins) {
     for (auto o = outs.begin(); o != outs.end(); ++o) {
-        if (!*o) continue;
-        for (const void* i : ins)
-            if (i == *o) return true;
+        for (const Place& i : ins)
+            if (o->meets(i)) return true;
         for (auto other = outs.begin(); other != o; ++other)
-            if (*other == *o) return true;
+            if (o->meets(*other)) return true;
     }
     return false;
 }
+
+// The same of a state that may be updated in place, but not over a part of the old one.
+bool overlap_in_place(const Place& out, const Place& in) { return out.at != in.at && out.meets(in); }
 
 bool valid_dtype(gdr_dtype d) { return d == GDR_F32 || d == GDR_BF16; }
 
@@ -50,6 +63,39 @@ gdr_status check_sizes(long long B, long long T, long long D, long long n_seqs) 
     if (D > (1 << 20)) return GDR_ERR_UNSUPPORTED;
     return GDR_OK;
 }
+
+unsigned long long size_of(gdr_dtype d) { return d == GDR_BF16 ? 2 : 4; }
+
+// Bytes of a call's arrays: the tokens' (in either type), the states', the bounds.
+struct ScanBytes {
+    unsigned long long x, g, h, cu;
+    explicit ScanBytes(const gdr_scan_args& a) {
+        const unsigned long long n = (unsigned long long)a.B * a.T * a.D;
+        x = n * size_of(a.io_dtype);
+        g = n * size_of(a.gate_dtype);
+        h = (unsigned long long)a.n_seqs * a.D * sizeof(float);
+        cu = (a.n_seqs + 1ull) * sizeof(int32_t);
+    }
+};
+struct ConvBytes {
+    unsigned long long x, state, w, bias, cu;
+    explicit ConvBytes(const gdr_conv_args& a) {
+        x = (unsigned long long)a.B * a.T * a.D * size_of(a.io_dtype);
+        state = (unsigned long long)a.n_seqs * (a.width - 1) * a.D * size_of(a.io_dtype);
+        bias = (unsigned long long)a.D * sizeof(float);
+        w = bias * a.width;
+        cu = (a.n_seqs + 1ull) * sizeof(int32_t);
+    }
+};
+struct NormBytes {
+    unsigned long long x, w, stats, cu;
+    explicit NormBytes(const gdr_norm_args& a) {
+        x = (unsigned long long)a.B * a.T * a.H * a.d * size_of(a.io_dtype);
+        w = (a.shared_weight ? 1ull : a.H) * a.d * sizeof(float);
+        stats = (unsigned long long)a.n_seqs * a.H * 2 * sizeof(float);
+        cu = (a.n_seqs + 1ull) * sizeof(int32_t);
+    }
+};
 
 template <typename A>
 gdr_status check_layout(const A* a, const int32_t* cu) {
@@ -127,8 +173,11 @@ gdr_status gdr_scan_fwd(const gdr_scan_args* a, const void* v, const void* g, co
     if (off16({v, g, beta, h0, cu, o, h_final})) return GDR_ERR_ALIGNMENT;
     ScanPtrs p{};
     p.v = v; p.g = g; p.beta = beta; p.h0 = h0; p.cu = cu; p.o = o; p.h_final = h_final;
+    const ScanBytes n(*a);
     // (h_final may be h0)
-    if (overlap({o, h_final}, {v, g, beta}) || overlap({o}, {h0})) return GDR_ERR_INVALID_ARG;
+    if (overlap({{o, n.x}, {h_final, n.h}}, {{v, n.x}, {g, n.g}, {beta, n.g}, {cu, n.cu}}) ||
+        overlap({{o, n.x}}, {{h0, n.h}}) || overlap_in_place({h_final, n.h}, {h0, n.h}))
+        return GDR_ERR_INVALID_ARG;
     if (!tokens && (st = check_empty(a, cu, static_cast<cudaStream_t>(stream))) != GDR_OK) return st;
     return launch_scan_fwd(*a, p, static_cast<cudaStream_t>(stream));
 }
@@ -147,8 +196,12 @@ gdr_status gdr_scan_bwd(const gdr_scan_args* a, const void* v, const void* g, co
     ScanPtrs p{};
     p.v = v; p.g = g; p.beta = beta; p.o_in = o; p.dO = dO; p.h0 = h0; p.cu = cu;
     p.dh_final = dh_final; p.dv = dv; p.dg = dg; p.dbeta = dbeta; p.dh0 = dh0;
+    const ScanBytes n(*a);
     // (dh0 may be dh_final)
-    if (overlap({dv, dg, dbeta, dh0}, {v, g, beta, o, dO, h0}) || overlap({dv, dg, dbeta}, {dh_final}))
+    if (overlap({{dv, n.x}, {dg, n.g}, {dbeta, n.g}, {dh0, n.h}},
+                {{v, n.x}, {g, n.g}, {beta, n.g}, {o, n.x}, {dO, n.x}, {h0, n.h}, {cu, n.cu}}) ||
+        overlap({{dv, n.x}, {dg, n.g}, {dbeta, n.g}}, {{dh_final, n.h}}) ||
+        overlap_in_place({dh0, n.h}, {dh_final, n.h}))
         return GDR_ERR_INVALID_ARG;
     if (!tokens && (st = check_empty(a, cu, static_cast<cudaStream_t>(stream))) != GDR_OK) return st;
     return launch_scan_bwd(*a, p, static_cast<cudaStream_t>(stream));
@@ -164,7 +217,10 @@ gdr_status gdr_scan_step(const gdr_scan_args* a, const void* v, const void* g, c
     if (off16({v, g, beta, h, h_out, o})) return GDR_ERR_ALIGNMENT;
     ScanPtrs p{};
     p.v = v; p.g = g; p.beta = beta; p.h0 = h; p.h_final = h_out; p.o = o;
-    if (overlap({o, h_out}, {v, g, beta}) || overlap({o}, {h})) return GDR_ERR_INVALID_ARG;
+    const ScanBytes n(*a);
+    if (overlap({{o, n.x}, {h_out, n.h}}, {{v, n.x}, {g, n.g}, {beta, n.g}}) ||
+        overlap({{o, n.x}}, {{h, n.h}}) || overlap_in_place({h_out, n.h}, {h, n.h}))
+        return GDR_ERR_INVALID_ARG;
     return launch_scan_step(*a, p, static_cast<cudaStream_t>(stream));
 }
 
@@ -174,11 +230,14 @@ gdr_status gdr_conv_fwd(const gdr_conv_args* a, const void* x, const float* w, c
     gdr_status st = check_conv(a);
     if (st != GDR_OK || (st = check_layout(a, cu)) != GDR_OK) return st;
     if ((long long)a->B * a->T > 0 && any_null({x, y})) return GDR_ERR_INVALID_ARG;
-    if (!w || (state && state == state_out)) return GDR_ERR_INVALID_ARG;
+    if (!w) return GDR_ERR_INVALID_ARG;
     if (off16({x, state, cu, y, state_out}) || off4({w, bias})) return GDR_ERR_ALIGNMENT;
     ConvPtrs p{};
     p.x = x; p.w = w; p.bias = bias; p.state = state; p.cu = cu; p.y = y; p.state_out = state_out;
-    if (overlap({y, state_out}, {x, w, bias, state})) return GDR_ERR_INVALID_ARG;
+    const ConvBytes n(*a);
+    if (overlap({{y, n.x}, {state_out, n.state}},
+                {{x, n.x}, {w, n.w}, {bias, n.bias}, {state, n.state}, {cu, n.cu}}))
+        return GDR_ERR_INVALID_ARG;
     return launch_conv_fwd(*a, p, static_cast<cudaStream_t>(stream));
 }
 
@@ -195,11 +254,15 @@ gdr_status gdr_conv_bwd(const gdr_conv_args* a, const void* x, const float* w, c
     if ((long long)a->B * a->T > 0 && any_null({x, dy, dx})) return GDR_ERR_INVALID_ARG;
     if (!w || !dw) return GDR_ERR_INVALID_ARG;
     if (off16({x, dy, state, cu, dx, dstate}) || off4({w, bias, dw, dbias})) return GDR_ERR_ALIGNMENT;
-    if ((st = check_workspace(workspace, workspace_bytes, conv_bwd_workspace(*a))) != GDR_OK) return st;
+    const size_t need = conv_bwd_workspace(*a);
+    if ((st = check_workspace(workspace, workspace_bytes, need)) != GDR_OK) return st;
     ConvPtrs p{};
     p.x = x; p.w = w; p.bias = bias; p.dy = dy; p.state = state; p.cu = cu; p.dx = dx; p.dw = dw;
     p.dbias = dbias; p.dstate = dstate; p.ws = static_cast<float*>(workspace);
-    if (overlap({dx, dw, dbias, dstate, workspace}, {x, w, bias, dy, state})) return GDR_ERR_INVALID_ARG;
+    const ConvBytes n(*a);
+    if (overlap({{dx, n.x}, {dw, n.w}, {dbias, n.bias}, {dstate, n.state}, {workspace, need}},
+                {{x, n.x}, {w, n.w}, {bias, n.bias}, {dy, n.x}, {state, n.state}, {cu, n.cu}}))
+        return GDR_ERR_INVALID_ARG;
     return launch_conv_bwd(*a, p, static_cast<cudaStream_t>(stream));
 }
 
@@ -212,7 +275,11 @@ gdr_status gdr_conv_step(const gdr_conv_args* a, const void* x, const float* w, 
     if (off16({x, state, state_out, y}) || off4({w, bias})) return GDR_ERR_ALIGNMENT;
     ConvPtrs p{};
     p.x = x; p.w = w; p.bias = bias; p.state = state; p.y = y; p.state_out = state_out;
-    if (overlap({y, state_out}, {x, w, bias}) || overlap({y}, {state})) return GDR_ERR_INVALID_ARG;
+    const ConvBytes n(*a);
+    if (overlap({{y, n.x}, {state_out, n.state}}, {{x, n.x}, {w, n.w}, {bias, n.bias}}) ||
+        overlap({{y, n.x}}, {{state, n.state}}) ||
+        overlap_in_place({state_out, n.state}, {state, n.state}))
+        return GDR_ERR_INVALID_ARG;
     return launch_conv_step(*a, p, static_cast<cudaStream_t>(stream));
 }
 
@@ -229,11 +296,15 @@ gdr_status gdr_norm_fwd(const gdr_norm_args* a, const void* x, const float* w, c
     if (tokens && any_null({x, y})) return GDR_ERR_INVALID_ARG;
     if (stats && !a->per_sequence) return GDR_ERR_INVALID_ARG;
     if (off16({x, z, cu, y, stats}) || off4({w, bias})) return GDR_ERR_ALIGNMENT;
-    if ((st = check_workspace(workspace, workspace_bytes, norm_fwd_workspace(*a))) != GDR_OK) return st;
+    const size_t need = norm_fwd_workspace(*a);
+    if ((st = check_workspace(workspace, workspace_bytes, need)) != GDR_OK) return st;
     NormPtrs p{};
     p.x = x; p.w = w; p.b = bias; p.z = z; p.cu = cu; p.y = y; p.stats = stats;
     p.ws = static_cast<float*>(workspace);
-    if (overlap({y, stats, workspace}, {x, w, bias, z})) return GDR_ERR_INVALID_ARG;
+    const NormBytes n(*a);
+    if (overlap({{y, n.x}, {stats, n.stats}, {workspace, need}},
+                {{x, n.x}, {w, n.w}, {bias, n.w}, {z, n.x}, {a->per_sequence ? cu : nullptr, n.cu}}))
+        return GDR_ERR_INVALID_ARG;
     if (!tokens && a->per_sequence &&
         (st = check_empty(a, cu, static_cast<cudaStream_t>(stream))) != GDR_OK)
         return st;
@@ -255,11 +326,17 @@ gdr_status gdr_norm_bwd(const gdr_norm_args* a, const void* x, const float* w, c
     if (tokens && (z != nullptr) != (dz != nullptr)) return GDR_ERR_INVALID_ARG;
     if (a->per_sequence && !stats) return GDR_ERR_INVALID_ARG;
     if (off16({x, z, dy, cu, stats, dx, dz}) || off4({w, bias, dw, dbias})) return GDR_ERR_ALIGNMENT;
-    if ((st = check_workspace(workspace, workspace_bytes, norm_bwd_workspace(*a))) != GDR_OK) return st;
+    const size_t need = norm_bwd_workspace(*a);
+    if ((st = check_workspace(workspace, workspace_bytes, need)) != GDR_OK) return st;
     NormPtrs p{};
     p.x = x; p.w = w; p.b = bias; p.z = z; p.dy = dy; p.cu = cu; p.stats_in = stats; p.dx = dx;
     p.dw = dw; p.db = dbias; p.dz = dz; p.ws = static_cast<float*>(workspace);
-    if (overlap({dx, dw, dbias, dz, workspace}, {x, w, bias, z, dy, stats})) return GDR_ERR_INVALID_ARG;
+    const NormBytes n(*a);
+    if (overlap({{dx, n.x}, {dw, n.w}, {dbias, n.w}, {dz, n.x}, {workspace, need}},
+                {{x, n.x}, {w, n.w}, {bias, n.w}, {z, n.x}, {dy, n.x},
+                 {a->per_sequence ? stats : nullptr, n.stats},
+                 {a->per_sequence ? cu : nullptr, n.cu}}))
+        return GDR_ERR_INVALID_ARG;
     if (!tokens && a->per_sequence &&
         (st = check_empty(a, cu, static_cast<cudaStream_t>(stream))) != GDR_OK)
         return st;

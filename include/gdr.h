@@ -362,8 +362,9 @@ gdr_status gdr_decode_step(const gdr_decode_args* args,
  *   unspecified, but no access leaves the tensors.  gdr_scan_fwd and gdr_scan_bwd report there
  *   too (GDR_ERR_TIMEOUT) if a bounded wait between the blocks of a cluster ran out.
  * - Channel arrays (weights, biases, their gradients) are fp32 and 4-byte aligned, everything
- *   else 16-byte aligned.  An output may not overlap an input or another output unless that
- *   is said; one that starts where such an array starts is GDR_ERR_INVALID_ARG.
+ *   else 16-byte aligned.  An output (or workspace) that shares bytes with an input or another
+ *   output is GDR_ERR_INVALID_ARG unless it is said that it may be that array; then it has to be
+ *   the whole of it.
  * - Sums, states and statistics are fp32; results are rounded once.  Repeated calls give the
  *   same bits.  Calls that overlap on the GPU share nothing but their arguments.
  */

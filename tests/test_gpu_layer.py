@@ -274,3 +274,36 @@ def test_calls_of_no_tokens_in_a_graph():
         g.replay()
         assert torch.equal(st, torch.tensor([0.0, 2.0], device="cuda").expand(2, 3, 2))
         assert not dw.any() and not other.any()
+
+
+def test_neighbouring_arrays_of_one_buffer():
+    """Inputs, outputs and states that touch without sharing a byte go through, with the results
+    of arrays of their own."""
+    n, T, D = 2, 70, 64
+    gen = torch.Generator("cuda").manual_seed(5)
+    flat_, state = n * T * D, n * D
+    buf = torch.empty(4 * flat_ + 2 * state, device="cuda").normal_(generator=gen)
+    v, g, o, y = (buf[i * flat_:(i + 1) * flat_].view(n, T, D) for i in range(4))
+    h0, hf = (buf[4 * flat_ + i * state:4 * flat_ + (i + 1) * state].view(n, D) for i in range(2))
+    g.abs_().neg_()
+    w = torch.randn(D, 4, device="cuda", generator=gen)
+    want = gdr.linear_scan_fwd(v.clone(), g.clone(), None, h0.clone())
+    gdr.linear_scan_fwd(v, g, None, h0, o=o, h_final=hf)
+    assert torch.equal(o, want[0]) and torch.equal(hf, want[1])
+    assert torch.equal(gdr.short_conv_fwd(o, w, y=y)[0], gdr.short_conv_fwd(o.clone(), w)[0])
+    x4, y4 = o.view(n, T, 1, D), y.view(n, T, 1, D)
+    assert torch.equal(gdr.group_norm_fwd(x4, y=y4), gdr.group_norm_fwd(x4.clone()))
+
+
+def test_outputs_that_begin_inside_an_input_are_refused():
+    T, D = 70, 64
+    buf = torch.randn(1, T + 1, D, device="cuda")
+    x, later = buf[:, :T], buf[:, 1:]
+    w = torch.randn(D, 4, device="cuda")
+    rows, states = torch.randn(2, T, D, device="cuda"), torch.zeros(3, D, device="cuda")
+    for call in (lambda: gdr.linear_scan_fwd(x, -torch.ones_like(x), o=later),
+                 lambda: gdr.linear_scan_fwd(rows, -rows.abs(), None, states[:2], h_final=states[1:]),
+                 lambda: gdr.short_conv_fwd(x, w, y=later),
+                 lambda: gdr.group_norm_fwd(x.view(1, T, 1, D), y=later.view(1, T, 1, D))):
+        with pytest.raises(gdr.GdrError):
+            call()

@@ -278,3 +278,56 @@ def test_an_output_in_an_inputs_place_is_refused(lib):
         # x w bias z dy cu stats dx dw dbias dz workspace
         each(lib.gdr_norm_bwd, norm, [*q[:5], None, *q[6:12]],
              [(7, 0), (7, 4), (10, 3), (8, 1), (9, 8), (10, 7), (11, 7)], (need, None))
+
+
+def test_an_output_that_shares_bytes_with_another_array_is_refused(lib):
+    """An output whose first or last 16 bytes lie in an input's or another output's; in place,
+    only the whole array will do."""
+    x, h, w, b, cs = 2 * 100 * 64 * 2, 2 * 64 * 4, 64 * 4 * 4, 64 * 4, 2 * 3 * 64 * 2
+    nx, nw, ns = 2 * 100 * 4 * 64 * 2, 4 * 64 * 4, 2 * 4 * 2 * 4
+
+    def each(fn, a, sizes, outs, absent=(), in_place=(), tail=(None,)):
+        q = [None if i in absent else P + (i + 1 << 32) for i in range(len(sizes))]
+        for o in outs:
+            for i in range(len(sizes)):
+                if i == o or q[i] is None:
+                    continue
+                places = [q[i] + sizes[i] - 16, q[i] - sizes[o] + 16]
+                if (o, i) not in in_place:
+                    places.append(q[i])
+                for at in places:
+                    if at == q[i] and (o, i) in in_place:
+                        continue  # arrays of 16 bytes
+                    assert fn(a, *(at if j == o else v for j, v in enumerate(q)), *tail) == INV, \
+                        (fn.__name__, o, i, at - q[i])
+
+    def sequences(a, cls, base):
+        """Packed: B = 1 and bounds (of two sequences)."""
+        return args(cls, {**base, **a}, dict(B=1, T=200))
+
+    scan = sequences(dict(write=1), ScanArgs, SCAN)
+    each(lib.gdr_scan_fwd, scan, [x, x, x, h, 16, x, h], (5, 6), in_place=[(6, 3)])
+    each(lib.gdr_scan_bwd, scan, [x, x, x, x, x, h, 16, h, x, x, x, h], (8, 9, 10, 11),
+         in_place=[(11, 7)])
+    one = args(ScanArgs, SCAN, dict(write=1, T=1))
+    each(lib.gdr_scan_step, one, [x // 100] * 3 + [h, h, x // 100], (4, 5), in_place=[(4, 3)])
+    conv = sequences({}, ConvArgs, CONV)
+    each(lib.gdr_conv_fwd, conv, [x, w, b, cs, 16, x, cs], (5, 6))
+    need = lib.gdr_conv_bwd_workspace_size(conv)
+    each(lib.gdr_conv_bwd, conv, [x, w, b, x, cs, 16, x, w, b, cs], (6, 7, 8, 9),
+         tail=(P + (20 << 32), need, None))
+    each(lib.gdr_conv_step, args(ConvArgs, CONV, dict(T=1)), [x // 100, w, b, cs, cs, x // 100], (4, 5),
+         in_place=[(4, 3)])
+    for per in (0, 1):
+        norm = sequences(dict(per_sequence=per), NormArgs, NORM) if per else args(NormArgs, NORM, {})
+        need = lib.gdr_norm_fwd_workspace_size(norm)
+        each(lib.gdr_norm_fwd, norm, [nx, nw, nw, nx, 16, nx, ns], (5, 6) if per else (5,),
+             absent=() if per else (4, 6), tail=(P + (20 << 32), need, None))
+        need = lib.gdr_norm_bwd_workspace_size(norm)
+        each(lib.gdr_norm_bwd, norm, [nx, nw, nw, nx, nx, 16, ns, nx, nw, nw, nx], (7, 8, 9, 10),
+             absent=() if per else (5, 6), tail=(P + (20 << 32), need, None))
+        # the workspace in an input's place, 256-byte aligned: its last bytes over x's first
+        q = [P + (i + 1 << 32) for i in range(11)]
+        if not per:
+            q[5] = q[6] = None
+        assert lib.gdr_norm_bwd(norm, *q, q[0] - need + 256, need, None) == INV
