@@ -93,7 +93,7 @@ scan_bwd_kernel(const BwdParams<IO, GT> p, const int cluster) {
         carry = load_state<kCopy>(p.dh_final + (size_t)row * D + c, mine);
     Seqs seqs = p.q;
     if constexpr (kSeqs) seqs = share_cu(p.q, reinterpret_cast<int32_t*>(smem + sizeof(sh)));
-    scan_open<kCluster>(sh.full);
+    scan_open(sh);
     if (kSeqs && blockIdx.x == 0) check_cu(seqs, p.status, tid, 32 * (kWarps + 2 * kCluster));
     if (kSeqs && rank == 0 && p.dh0)  // the state's gradient passes an empty sequence unchanged
         each_empty(seqs, wid, kWarps + 2 * kCluster, lane, [&](int s) {
@@ -127,13 +127,14 @@ scan_bwd_kernel(const BwdParams<IO, GT> p, const int cluster) {
         if constexpr (kWrite == GDR_WRITE_GATE) fb.tile(s + R::beta, place_of(k), L, hop);
     };
     if constexpr (kCluster) if (wid >= kWarps) {
+        bool ok = true;
         if (wid > kWarps) {
             scan_publish<kGroups, kSeqs>(sh, steps, cluster, rank, lane);
         } else {
-            const bool ok = scan_fold<kGroups, kSeqs>(sh, steps, cluster, rank, lane, carry);
+            ok = scan_fold<kGroups, kSeqs>(sh, steps, cluster, rank, lane, carry);
             if (!ok && p.status && lane == 0) atomicCAS(p.status, (int)GDR_OK, (int)GDR_ERR_TIMEOUT);
         }
-        scan_close<kCluster>();
+        scan_close<kCluster>(!ok);
         return;
     }
     // copy group k: the first ring's tile k, with the second's kEarlyStages - 1 tiles behind it

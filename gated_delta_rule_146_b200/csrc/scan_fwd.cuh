@@ -75,7 +75,7 @@ scan_fwd_kernel(const FwdParams<IO, GT> p, const int cluster) {
         carry = load_state<kCopy>(p.h0 + (size_t)row * D + c, mine);
     Seqs seqs = p.q;
     if constexpr (kSeqs) seqs = share_cu(p.q, reinterpret_cast<int32_t*>(smem + sizeof(sh)));
-    scan_open<kCluster>(sh.full);
+    scan_open(sh);
     if (kSeqs && blockIdx.x == 0) check_cu(seqs, p.status, tid, 32 * (kWarps + 2 * kCluster));
     if (kSeqs && rank == 0 && p.h_final)  // empty sequences keep their state
         each_empty(seqs, wid, kWarps + 2 * kCluster, lane, [&](int s) {
@@ -104,15 +104,16 @@ scan_fwd_kernel(const FwdParams<IO, GT> p, const int cluster) {
         copy_commit();
     };
     if constexpr (kCluster) if (wid >= kWarps) {
+        bool ok = true;
         if (wid > kWarps) {
             scan_publish<kGroups, kSeqs>(sh, steps, cluster, rank, lane);
         } else {
-            const bool ok = scan_fold<kGroups, kSeqs>(sh, steps, cluster, rank, lane, carry);
+            ok = scan_fold<kGroups, kSeqs>(sh, steps, cluster, rank, lane, carry);
             if (!ok && p.status && lane == 0) atomicCAS(p.status, (int)GDR_OK, (int)GDR_ERR_TIMEOUT);
             if (!kSeqs && p.h_final && rank == 0 && group == 0)
                 store_pair<float, kCopy>(p.h_final + (size_t)row * D + c, carry, mine);
         }
-        scan_close<kCluster>();
+        scan_close<kCluster>(!ok);
         return;
     }
 #pragma unroll

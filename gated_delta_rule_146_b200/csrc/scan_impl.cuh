@@ -35,7 +35,10 @@ using namespace tc;
 constexpr int kScanMaxCluster = 8;             // a warp hands the block's run to one block
 constexpr int kSlab = 64;                      // channels of a block without groups
 constexpr float kReset = -1.f;
-constexpr uint64_t kScanWaitNs = 2000000000ull;
+#ifndef GDR_SCAN_WAIT_NS   // (the test of a wait that runs out takes a shorter one)
+#define GDR_SCAN_WAIT_NS 2000000000ull
+#endif
+constexpr uint64_t kScanWaitNs = GDR_SCAN_WAIT_NS;
 
 // 1 - e^g given a = e^g: the series of e^g - 1 near zero (|g| < 1/2; the term left out is below
 // 2^-26 of the sum), the difference elsewhere.
@@ -96,12 +99,18 @@ __device__ __forceinline__ Run join_groups(Run& run, int lane) {
 // has read that tile's runs by then.  Blocks' runs go by tile modulo four: a block sends tile j
 // when its workers have the states of tile j - 2, for which every block has sent tile j - 2, and so
 // has folded tile j - 4.
+//
+// A block whose wait has run out is late, and stays so.  Its folder then neither waits nor arms a
+// barrier; it hands NaN to the workers and keeps it as the state, so that every value that misses a
+// run is NaN and no wrong one is written.  Its publisher sends nothing more, since it is no longer
+// bound to the order above; the other blocks miss its runs and become late in turn.
 template <int kWarps, bool kCluster>
 struct alignas(128) ScanShared {
     Run run[kCluster ? 2 : 4][kWarps][32];
     F2 before[kCluster ? 2 : 1][kCluster ? kWarps : 1][32];
     Run block[kCluster ? 4 : 1][kScanMaxCluster][32];
     alignas(128) uint64_t full[4];   // bytes of block[] that have come
+    volatile int late;
 };
 
 // A single block's walk over the row's tiles.  E holds a lane's elements of a tile; form(k, e)
@@ -186,8 +195,8 @@ __device__ __forceinline__ void scan_work(ScanShared<kWarps, true>& sh, int step
     }
 }
 
-// The folder's walk.  False if a wait ran out; the walk then goes on without waiting, so that all
-// threads meet at the barriers.
+// The folder's walk.  False if a wait ran out; the walk then goes on, late, so that all threads meet
+// at the barriers.
 template <int kGroups, bool kSeqs, int kWarps>
 __device__ __forceinline__ bool scan_fold(ScanShared<kWarps, true>& sh, int steps, int cluster, int rank,
                                           int lane, F2& carry) {
@@ -196,15 +205,20 @@ __device__ __forceinline__ bool scan_fold(ScanShared<kWarps, true>& sh, int step
         const int par = k & 1;
         bar_sync(kFormed + par, blockDim.x);
         uint64_t* full = &sh.full[k & 3];
-        if (lane == 0) mbar_expect_tx(full, (uint32_t)cluster * (32 / kGroups) * sizeof(Run));
+        if (ok && lane == 0)
+            mbar_expect_tx(full, (uint32_t)cluster * (32 / kGroups) * sizeof(Run));
         // the maps from the block's first token to every worker, while the other blocks' runs come
         Run to[kWarps];
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) to[w] = sh.run[par][w][lane];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) to[w] = run_join<kSeqs>(to[w - 1], to[w]);
-        if (ok) ok = runs_here(full, (uint32_t)(k >> 2) & 1u);
-        ok = __all_sync(0xffffffffu, ok);
+        if (ok) ok = __all_sync(0xffffffffu, runs_here(full, (uint32_t)(k >> 2) & 1u));
+        if (!ok) {
+            sh.late = 1;
+            __threadfence_block();  // before a worker overwrites what the publisher may be reading
+            carry = f2(__int_as_float(0x7fffffff));
+        }
         F2 x = carry;
         Run blocks[kScanMaxCluster];
 #pragma unroll
@@ -212,7 +226,7 @@ __device__ __forceinline__ bool scan_fold(ScanShared<kWarps, true>& sh, int step
 #pragma unroll
         for (int r = 0; r < kScanMaxCluster; ++r) {
             if (r == rank) x = carry;
-            if (r < cluster) carry = run_apply<kSeqs>(blocks[r], carry);
+            if (r < cluster && ok) carry = run_apply<kSeqs>(blocks[r], carry);
         }
         sh.before[par][0][lane] = x;
 #pragma unroll
@@ -233,7 +247,8 @@ __device__ __forceinline__ void scan_publish(ScanShared<kWarps, true>& sh, int s
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) all = run_join<kSeqs>(all, r[w][lane]);
         const uint32_t to = smem_u32(&sh.block[k & 3][rank][lane]), bar = smem_u32(&sh.full[k & 3]);
-        if (lane >= 32 / kGroups) continue;
+        __threadfence_block();
+        if (lane >= 32 / kGroups || sh.late) continue;
         for (int b = 0; b < cluster; ++b)
             asm volatile(
                 "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];"
@@ -244,22 +259,25 @@ __device__ __forceinline__ void scan_publish(ScanShared<kWarps, true>& sh, int s
 }
 
 // The blocks of a cluster start together, their barriers ready, and end together, so that nothing
-// is sent to a block that is gone.
-template <bool kCluster>
-__device__ __forceinline__ void scan_open(uint64_t (&full)[4]) {
+// is sent to a block that is gone.  A late block has not waited for what was sent to it: its folder
+// stays until that has come.
+template <int kWarps, bool kCluster>
+__device__ __forceinline__ void scan_open(ScanShared<kWarps, kCluster>& sh) {
     if (!kCluster) return;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 4; ++i) mbar_init(&full[i], 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&sh.full[i], 1);
+        sh.late = 0;
         mbar_init_fence();
     }
     __syncwarp();
     cluster_sync_all();
 }
 template <bool kCluster>
-__device__ __forceinline__ void scan_close() {
+__device__ __forceinline__ void scan_close(bool late = false) {
     if (!kCluster) return;
     __syncwarp();
     cluster_sync_all();
+    if (late) __nanosleep(1000000u);
 }
 
 // ---- feeding -----------------------------------------------------------------------------------

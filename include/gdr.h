@@ -360,7 +360,8 @@ gdr_status gdr_decode_step(const gdr_decode_args* args,
  *   start at 0, decreases or does not end at T is reported as GDR_ERR_DEVICE_CHECK in
  *   args->status (an optional device int as in gdr_chunk_args); the outputs are then
  *   unspecified, but no access leaves the tensors.  gdr_scan_fwd and gdr_scan_bwd report there
- *   too (GDR_ERR_TIMEOUT) if a bounded wait between the blocks of a cluster ran out.
+ *   too (GDR_ERR_TIMEOUT) if a bounded wait between the blocks of a cluster ran out; with or
+ *   without a status word, every value that misses what was waited for is then NaN.
  * - Channel arrays (weights, biases, their gradients) are fp32 and 4-byte aligned, everything
  *   else 16-byte aligned.  An output (or workspace) that shares bytes with an input or another
  *   output is GDR_ERR_INVALID_ARG unless it is said that it may be that array; then it has to be
