@@ -4,7 +4,7 @@ import torch
 
 import gated_delta_rule_146_b200 as gdr
 from gated_delta_rule_146_b200 import _abi
-from layer_helpers import check, conv_tol
+from layer_helpers import E, check, conv_tol
 from oracle import layer as ol
 
 pytestmark = pytest.mark.gpu
@@ -212,3 +212,24 @@ def test_streams_graphs_and_repeats():
         torch.cuda.synchronize()
         for a, b in zip(out, w):
             assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_activation_in_fp32_at_large_sums():
+    """One weight of one leaves p exact: what is left is the activation's own error, 8 E of y (its
+    exponential, sum, reciprocal and product), and 24 E of the terms of its slope s (1 + p (1 - s)).
+    (An exponent rounded before the exponential would be off by |p| E.)"""
+    p = torch.cat([torch.linspace(-80, 80, 40001), torch.linspace(-3, 3, 4097)])
+    x = p.view(1, 1, -1).cuda()
+    D = p.numel()
+    w = torch.zeros(D, 4)
+    w[:, 3] = 1.0
+    y = gdr.short_conv_fwd(x, w.cuda())[0]
+    dx = gdr.short_conv_bwd(x, w.cuda(), None, torch.ones_like(x))[0]
+    z = torch.zeros(1, 3, D, device="cuda")
+    step = gdr.short_conv_step(x[0], w.cuda(), None, z)
+    assert torch.equal(step, y[0])
+    q = p.double()
+    s = 1 / (1 + torch.exp(-q))
+    rest = 1 / (1 + torch.exp(q))
+    check("y", y[0], (q * s)[None].numpy(), (8 * E * (q * s).abs())[None].numpy())
+    check("dx", dx[0], (s * (1 + q * rest))[None].numpy(), (24 * E * s * (1 + q.abs() * rest))[None].numpy())
