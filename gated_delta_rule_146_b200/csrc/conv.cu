@@ -9,9 +9,10 @@
 // pairs through packed fp32 arithmetic, and the activation costs one exponential and one
 // reciprocal in place of an IEEE division.
 //
-// HBM bounds the forward (4 bytes per token and channel in bf16): 65537 x 4096 takes 183 us, 90 %
-// of the copy rate.  The backward (6 bytes) comes to 60 %: 8 x 4096 x 2048 takes 102 us, its 24
-// instructions an element waiting on one another in the 16 warps that its registers allow.
+// HBM bounds the forward (4 bytes per token and channel in bf16): 65537 x 4096 takes 182 us, 90 %
+// of the copy rate.  The backward (6 bytes) comes to 60 %: 8 x 4096 x 2048 takes 100 to 102 us, its
+// 24 instructions an element waiting on one another in the 16 warps that its registers allow.  In
+// fp32 these 8 x 4096 x 2048 take 100 to 106 us forward and 160 backward (82 and 76 %).
 //
 // The backward forms p again from x.  dx_t gathers dp of the W - 1 tokens behind it, so a run
 // reads that far ahead; the gradients of weights and bias are summed over the run in registers,
@@ -26,8 +27,8 @@ namespace {
 constexpr int kConvWarps = 4;
 constexpr int kConvThreads = 32 * kConvWarps;
 
-// Results in bf16 do not show the coarser sigmoid's error (layer.cuh); fp32 ones do, where p is large
-// and the sum of one exact term.
+// Results in bf16 do not show the coarser sigmoid's error (layer.cuh); fp32 ones do where p is large
+// and exact.  The fine one costs fp32 2 to 4 % (8 x 4096 x 2048: 102 -> 106 us, backward 156 -> 160).
 template <typename IO>
 constexpr bool kFine = sizeof(IO) == 4;
 
@@ -258,7 +259,7 @@ conv_fwd_kernel(const ConvParams<IO> p) {
     }
 }
 
-// Blocks on an SM: five spill (115 instead of 102 us).
+// Blocks on an SM: five spill (115 instead of 100 to 102 us).
 constexpr int kBwdResident = 4;
 
 template <typename IO, int W, int N, bool kWhole, int kAct>
@@ -502,7 +503,7 @@ ConvGrid conv_grid(const gdr_conv_args& a, int across, int resident, int most) {
 // Measured on 65537 x 4096 (forward) and 8 x 4096 x 2048 (backward) in bf16.  Forward: a block's
 // warps on four neighbouring slabs 186 us, on four runs of one slab 190; runs of up to 64, 128, 256
 // tokens 195, 186, 198.  Backward: one slab 98 us, four 104; runs of up to 32, 64, 128, 256 tokens
-// 131, 108, 100, 98.
+// 131, 108, 100, 98.  (Each series on one box and build, which differ by a few percent.)
 ConvGrid fwd_grid(const gdr_conv_args& a) { return conv_grid(a, 4, 8, 128); }
 ConvGrid bwd_grid(const gdr_conv_args& a) { return conv_grid(a, 1, kBwdResident, 256); }
 

@@ -8,7 +8,8 @@
 // (sums of squares about the mean, no cancellation), the tensors are read and written once: 4 or
 // 6 (gate) bytes per element forward, 6 or 10 backward in bf16.  HBM bounds both with a gate: 8 x
 // 4096 x 16 x 128 in bf16 takes 66 us forward and 113 to 119 backward, 94 and 86 to 91 % of the copy
-// rate.  Without one: 59 and 100 us, 69 and 61 %, bound by instructions.
+// rate.  Without one: 59 and 100 us (54 and 84 without centering), 69 and 61 %: the activation waits
+// for the row's statistics, so that a row is one chain of dependent instructions and shuffles.
 //
 // Each lane group keeps one head, so that weights, and in the backward the sums for dw and db,
 // stay in registers over all its rows; the sums are joined over the block, then over the blocks

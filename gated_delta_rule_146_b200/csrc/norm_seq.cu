@@ -4,15 +4,17 @@
 // direction is two passes over the tensors with the sums joined between them: sums of every
 // (tile of tokens, head), their join per (sequence, head), then the elements.  The second pass
 // reads x again: from L2 where the tensors fit there.  16 segments of 2048 tokens x 12 x 64 in bf16
-// take 59 us backward (bytes read once: 23 us), its two passes at 64 to 67 % of the issue slots;
-// 8 x 4096 x 16 x 128, beyond L2, 166 us with a gate, at the rate of two passes' bytes (163 us).
+// take 45 us forward and 60 backward (bytes read once: 15 and 23), the backward's two passes at 64 %
+// of the issue slots.  8 x 4096 x 16 x 128, beyond L2, takes 165 us backward with a gate, at the rate
+// of two passes' bytes (163), and 104 us forward without one: the statistics pass 47, where its bytes
+// take 20 (its many short blocks load, join and end), and the second 54, where they take 41.
 //
 // A tile may meet several sequences.  Tile i and sequence s have the piece number i + s: along
 // the token axis each step goes to the next tile or to the next sequence, so the numbers are
 // distinct and a sequence's pieces lie side by side, whatever the lengths.  A block takes its
 // tile's sequences one after the other, so the first pass slows down where they are shorter than
 // its tile: 32768 tokens x 16 x 64 take 57 us forward and 78 backward in sequences of 1024, 250 and
-// 320 in sequences of 8, 1550 and 1970 in sequences of one.
+// 320 in sequences of 8, 1540 and 1990 in sequences of one.
 //
 // Variances: each piece's sum of squares is taken about the piece's own mean, from registers,
 // and pieces are joined pairwise with the difference of their means, so that no large squares

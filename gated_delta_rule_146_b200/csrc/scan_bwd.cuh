@@ -6,8 +6,9 @@
 // (scan_impl.cuh).  dg_t = m_t h_{t-1} reads h from the forward's output, so nothing is
 // recomputed and every element is read and written once: 10 (plain), 12 (tied) or 16 (gate)
 // bytes per token and channel in bf16.  HBM bounds it: 8 x 4096 x 2048 in bf16 with beta takes 174
-// to 182 us, 90 to 94 % of the copy rate.  Clusters are bound by the instructions of a step (52 % of the issue
-// slots of the 120 SMs they fill): 49157 packed tokens x 768, plain, 143 us, 40 %.
+// to 182 us, 90 to 94 % of the copy rate.  Clusters wait at the barriers of a step and on dependent
+// instructions (52 % of the issue slots of the 120 SMs they fill): 49157 packed tokens x 768, plain,
+// 143 us, 40 %.
 #pragma once
 
 #include "scan_impl.cuh"

@@ -4,9 +4,11 @@
 //
 // Every element is read and written once (6 bytes per token and channel in bf16, 8 with beta),
 // for about twenty instructions a pair of channels: HBM bounds it.  8 x 4096 x 2048 in bf16 with
-// beta takes 86 us, 95 % of the copy rate.  Clusters come to 75 % (131072 x 1024, plain: 165 us),
-// bound by the instructions of a step on the 128 SMs they fill.  The split is described in
-// scan_impl.cuh.
+// beta takes 86 us, 95 % of the copy rate; tied (98 to 102 us, 62 %) the instructions of 1 - e^g
+// bound it.  Clusters come to 75 % (131072 x 1024, plain: 164 us): with one block on an SM nothing
+// covers the barriers and dependent instructions of a step, at 55 % of the issue slots of the 128
+// SMs they fill.  Packed sequences add the work at their bounds (32768 x 1024: 47 us as one, 65 in
+// 32).  The split is described in scan_impl.cuh.
 #pragma once
 
 #include "scan_impl.cuh"

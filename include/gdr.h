@@ -378,7 +378,7 @@ gdr_status gdr_decode_step(const gdr_decode_args* args,
  *     b_t = beta_t v_t           write = GDR_WRITE_GATE
  *     b_t = (1 - alpha_t) v_t    write = GDR_WRITE_TIED
  *
- * g may be -inf (alpha = 0: the state is dropped).  Where decays grow (g > 0), their product
+ * g may be -inf (alpha = 0: a finite state is dropped).  Where decays grow (g > 0), their product
  * over any run of tokens of a sequence has to stay in the fp32 range, since runs of tokens are
  * formed at once and joined by it.  A sequence never sees another one's values, infinities and
  * NaN included.
